@@ -15,6 +15,8 @@ Operations (TransformerEngine pages "[PyTorch] cuda graph support" and
   fp8_amax_and_scale_update delayed-scaling update with the infinite-scale guard
   fp8_transpose             FP8 byte transpose (transpose-cache fill)
   fp8_cast                  cast without transpose
+  MoePlan, moe_*, fp8_moe_dispatch   tokens sorted by expert and back (moe.py)
+  block_norm, block_norm_backward    norm, gate, residual sum, norm (norms.py)
 Every call accepts ``noop_flag``: a CUDA fp32 scalar tensor; when it holds a
 nonzero value at run time the kernels write nothing.
 """
@@ -98,7 +100,27 @@ def lib() -> ctypes.CDLL:
             L.ct_selftest_bounded_wait.restype = i32
             L.ct_fp8_convert_f32.argtypes = [vp, i64, i32, vp, vp]
             L.ct_fp8_convert_f32.restype = i32
-            for name in ("fp8_cast_transpose", "fp8_cast_transpose_ex", "fp8_cast",
+            L.moe_sorted_rows.restype = i64
+            L.moe_sorted_rows.argtypes = [i64, i32, i32, i32]
+            L.moe_sort_workspace_size.restype = c.c_size_t
+            L.moe_sort_workspace_size.argtypes = [i64, i32, i32]
+            L.moe_sort.argtypes = [vp, i32, i64, i32, i32, i32, i64, vp, vp, vp, vp, vp,
+                                   c.c_size_t, vp, vp]
+            L.moe_dispatch.argtypes = [vp, i64, i32, i64, i32, vp, vp, i64, vp, vp, vp]
+            L.moe_dispatch_backward.argtypes = [vp, i64, i32, i64, i32, vp, i64, vp, vp, vp]
+            L.fp8_moe_dispatch.argtypes = [vp, i64, i32, i64, vp, i64, vp, vp, vp, vp, vp, vp, i32,
+                                           vp, vp]
+            L.moe_combine.argtypes = [vp, i64, i32, i64, i32, vp, vp, i64, vp, vp, vp]
+            L.moe_combine_backward.argtypes = [vp, vp, i64, i32, i64, i32, vp, vp, vp, i64, vp, vp,
+                                               vp, vp]
+            L.block_norm.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
+            L.block_norm_backward_workspace_size.restype = c.c_size_t
+            L.block_norm_backward_workspace_size.argtypes = [i64, i64]
+            L.block_norm_backward.argtypes = [vp] * 13 + [c.c_size_t, vp, vp]
+            for name in ("moe_sort", "moe_dispatch", "moe_dispatch_backward", "fp8_moe_dispatch",
+                         "moe_combine", "moe_combine_backward", "block_norm",
+                         "block_norm_backward",
+                         "fp8_cast_transpose", "fp8_cast_transpose_ex", "fp8_cast",
                          "fp8_dbias_cast_transpose", "fp8_dbias_cast_transpose_ex",
                          "fp8_multi_cast_transpose", "fp8_multi_cast_transpose_ex",
                          "fp8_amax_and_scale_update", "fp8_amax_and_scale_update_ex",
@@ -334,3 +356,9 @@ def empty_outputs(x: torch.Tensor):
     rows, cols = _rc(x)
     return (torch.empty(rows, cols, dtype=torch.uint8, device=x.device),
             torch.empty(cols, rows, dtype=torch.uint8, device=x.device))
+
+
+from .moe import (MoePlan, fp8_moe_dispatch, moe_combine, moe_combine_backward,  # noqa: E402
+                  moe_dispatch, moe_dispatch_backward, moe_sort, moe_sorted_rows)
+from .norms import (block_norm, block_norm_backward,  # noqa: E402
+                    block_norm_backward_workspace_size)

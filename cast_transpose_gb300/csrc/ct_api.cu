@@ -8,6 +8,7 @@
 // synchronised, and no device memory is read, so every call can be captured
 // in a CUDA graph.
 #include "../../include/cast_transpose.h"
+#include "ct_checks.h"
 #include "ct_internal.h"
 
 #include <cuda.h>
@@ -67,16 +68,10 @@ bool encode_bf16_map(CUtensorMap* map, const void* x, int64_t rows, int64_t cols
 // ---- argument checks ---------------------------------------------------------
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;   // TMA coordinates are int32
 
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-};
-inline Range range_of(const void* p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + static_cast<uintptr_t>(bytes)};
-}
-inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+using ct::aligned;
+using ct::overlap;
+using ct::Range;
+using ct::range_of;
 
 bool shape_ok(int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 0) return false;
@@ -130,7 +125,7 @@ bool ragged_rows_eligible(const void* x, int64_t rows, int64_t cols, const void*
            aligned(x, 16) && aligned(out, 16) && (out_t == nullptr || aligned(out_t, 16));
 }
 
-inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? CT_OK : CT_ERR_CUDA; }
+using ct::cuda_status;
 
 void fill_tensor(FastTensor& t, const void* out, const void* out_t, const float* scale,
                  float* amax, float* scale_inv, int64_t rows, int64_t cols, int64_t tile_begin) {

@@ -1,0 +1,163 @@
+// ct_types.cuh -- eight columns at a time of bf16, fp16 or fp32 rows, and
+// the block-wide sum, for the norm and expert-movement kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ct {
+namespace dev {
+
+// The 16-byte words that hold eight elements.
+template <typename T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+    return r;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+// One rounding to the stored type, to nearest even.
+__device__ __forceinline__ void from_f32(float& d, float v) { d = v; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_f32(__half& d, float v) { d = __float2half_rn(v); }
+
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(r.v[i].x);
+        f[4 * i + 1] = __uint_as_float(r.v[i].y);
+        f[4 * i + 2] = __uint_as_float(r.v[i].z);
+        f[4 * i + 3] = __uint_as_float(r.v[i].w);
+    }
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&f)[8]) {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack8(const Raw8<__half>& r, float (&f)[8]) {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
+        f[2 * i] = __low2float(h);
+        f[2 * i + 1] = __high2float(h);
+    }
+}
+
+__device__ __forceinline__ Raw8<float> pack8(const float (&f)[8], float) {
+    Raw8<float> r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        r.v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                            __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+    return r;
+}
+__device__ __forceinline__ Raw8<__nv_bfloat16> pack8(const float (&f)[8], __nv_bfloat16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return Raw8<__nv_bfloat16>{{make_uint4(w[0], w[1], w[2], w[3])}};
+}
+__device__ __forceinline__ Raw8<__half> pack8(const float (&f)[8], __half) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 b = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return Raw8<__half>{{make_uint4(w[0], w[1], w[2], w[3])}};
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+    const Raw8<T> r = pack8(f, T{});
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
+}
+
+// The eight columns a thread holds of a row of H.  VEC: the consecutive ones
+// of vector `vi` (H % 8 == 0, rows 16-byte aligned).  Otherwise, for any H and
+// alignment, eight columns `step` apart, so that a warp's threads stay on
+// neighbouring elements.
+template <bool VEC>
+struct Cols {
+    int first, step, H;
+    __device__ __forceinline__ Cols(int vi, int threads, int H_) : H(H_) {
+        if (VEC) {
+            first = vi * 8;
+            step = 1;
+        } else {
+            first = (vi / threads) * threads * 8 + vi % threads;
+            step = threads;
+        }
+    }
+    __device__ __forceinline__ int at(int j) const { return first + j * step; }
+    __device__ __forceinline__ bool any() const { return first < H; }
+    __device__ __forceinline__ bool has(int j) const { return VEC ? first < H : at(j) < H; }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_cols(const T* row, const Cols<VEC>& c, float (&f)[8]) {
+    if constexpr (VEC) {
+        if (c.any()) {
+            unpack8(load8(row + c.first), f);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = c.has(j) ? to_f32(row[c.at(j)]) : 0.0f;
+    }
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_cols(T* row, const Cols<VEC>& c, const float (&f)[8]) {
+    if constexpr (VEC) {
+        if (c.any()) store8(row + c.first, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c.has(j)) from_f32(row[c.at(j)], f[j]);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// Sum over the block, the same in every thread, in a fixed order.  `slots`
+// has one float per warp; it may be used again after another __syncthreads
+// (callers that sum twice in a row alternate between two).
+__device__ __forceinline__ float block_sum(float v, float* slots) {
+    v = warp_sum(v);
+    const int warps = (blockDim.x + 31) >> 5, lane = threadIdx.x & 31;
+    if (warps == 1) return v;
+    if (lane == 0) slots[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum(lane < warps ? slots[lane] : 0.0f);
+}
+
+}  // namespace dev
+}  // namespace ct

@@ -442,6 +442,177 @@ int fp8_dbias_cast_transpose_noalloc(const void* dy, int64_t rows, int64_t cols,
  */
 int ct_fp8_convert_f32(const float* in, int64_t n, int fmt, void* out, void* stream);
 
+/* ==========================================================================
+ * Tokens sorted by expert and back
+ *
+ * The experts of a mixture-of-experts block are FP8 linears whose inputs and
+ * output gradients this library casts and transposes; these entry points move
+ * the rows between token order and expert order.  The pages have no
+ * counterpart to them.
+ *
+ * T tokens choose K experts each (slot s = t*K + k), E experts.  Sorted
+ * buffers have `rows` rows: expert e owns rows [offsets[e], offsets[e+1]), a
+ * multiple of `align` of them, with its slots in slot order from offsets[e]
+ * on; its other rows and those from offsets[E] on are padding.  align = 16
+ * makes the columns of every expert's slice of an FP8 transpose start on 16
+ * bytes.  moe_sorted_rows() rows hold every slot whatever the routing, so no
+ * size has to be read back from the device.  With fewer, a slot whose row
+ * would be `rows` or beyond is dropped: the last experts lose theirs.
+ *
+ *   row_of   int32 [T, K]: the sorted row of each slot, -1 where it is dropped
+ *            (also where expert_idx is outside [0, E): a padding token)
+ *   src      int32 [rows]: the slot of each sorted row, -1 for padding
+ *   offsets  int32 [E + 1], each at most `rows`
+ *   counts   int32 [E]: slots that chose the expert, dropped ones included
+ *
+ * Data types are ct_dtype values.  Rows are dense, of `hidden` elements, and
+ * have no alignment beyond their element's; rows of a multiple of 16 bytes in
+ * 16-byte-aligned buffers are moved as 16-byte vectors.  Indexes outside
+ * [0, rows) in row_of, or outside [0, T*K) in src, are treated as -1.
+ * Arithmetic is fp32, rounded once to the output's type; sums run over k in
+ * order and every result is the same from call to call.
+ * Limits: 1 <= E <= 1024, 1 <= K <= 64, 1 <= align <= 1024, T*K and rows
+ * below 2^31.  Buffers that a call writes must not overlap any other buffer.
+ * Errors: CT_ERR_NULL, CT_ERR_SHAPE, CT_ERR_ALIGN, CT_ERR_FORMAT (data type,
+ * fmt), CT_ERR_ARG (E, K, align), CT_ERR_ALIAS, CT_ERR_WORKSPACE, CT_ERR_CUDA.
+ * ========================================================================== */
+typedef enum { CT_BF16 = 0, CT_FP16 = 1, CT_FP32 = 2 } ct_dtype;
+
+/* Rows that hold every slot: T*K + min(E, T*K) * (align - 1), rounded up to a
+ * multiple of align (0 for arguments outside the limits). */
+int64_t moe_sorted_rows(int64_t tokens, int topk, int experts, int align);
+
+/* Bytes of workspace moe_sort needs (16-byte aligned; 0 for small T*K). */
+size_t moe_sort_workspace_size(int64_t tokens, int topk, int experts);
+
+/*
+ * moe_sort -- the plan of the four calls below, from the router's choices.
+ *
+ *   expert_idx  [T, K], int32 (index_bytes = 4) or int64 (index_bytes = 8)
+ *
+ * A stable counting sort.  Writes all of row_of, src, offsets and counts (T = 0
+ * too: then nothing but padding).
+ */
+int moe_sort(const void* expert_idx, int index_bytes, int64_t tokens, int topk, int experts,
+             int align, int64_t rows, int* row_of, int* src, int* offsets, int* counts,
+             void* workspace, size_t workspace_bytes, const float* noop_flag, void* stream);
+
+/*
+ * moe_dispatch -- out[row_of[t,k]] = x[t]; padding rows are set to zero.
+ *   x [T, hidden], out [rows, hidden], both of type `dtype`
+ */
+int moe_dispatch(const void* x, int64_t tokens, int topk, int64_t hidden, int dtype,
+                 const int* row_of, const int* src, int64_t rows, void* out,
+                 const float* noop_flag, void* stream);
+
+/* moe_dispatch_backward -- dx[t] = sum over k of dout[row_of[t,k]]. */
+int moe_dispatch_backward(const void* dout, int64_t tokens, int topk, int64_t hidden, int dtype,
+                          const int* row_of, int64_t rows, void* dx, const float* noop_flag,
+                          void* stream);
+
+/*
+ * fp8_moe_dispatch -- moe_dispatch and fp8_cast_transpose in one: row r of the
+ * sorted matrix is w[src[r]] * x[src[r] / K] (one fp32 product; no weights:
+ * x itself), cast as out = fp8(row * scale), with its transpose, and amax
+ * max-merged with the largest magnitude of the rows before the scale.  With
+ * the weights and dy for x it is the FP8 form of moe_combine_backward's dys.
+ *
+ *   x        bf16 [T, hidden]
+ *   weights  nullable, fp32 [T, K]
+ *   out      uint8 [rows, hidden];  out_t  nullable, uint8 [hidden, rows]
+ *   scale, amax, scale_inv, fmt  as in fp8_cast_transpose
+ */
+int fp8_moe_dispatch(const void* x, int64_t tokens, int topk, int64_t hidden, const int* src,
+                     int64_t rows, const float* weights, const float* scale, float* amax,
+                     float* scale_inv, void* out, void* out_t, int fmt, const float* noop_flag,
+                     void* stream);
+
+/*
+ * moe_combine -- out[t] = sum over k of weights[t,k] * ys[row_of[t,k]]; a
+ * dropped slot adds nothing (whatever its weight), a token with none gives 0.
+ *   ys [rows, hidden], out [T, hidden] of type `dtype`; weights fp32 [T, K]
+ */
+int moe_combine(const void* ys, int64_t tokens, int topk, int64_t hidden, int dtype,
+                const int* row_of, const float* weights, int64_t rows, void* out,
+                const float* noop_flag, void* stream);
+
+/*
+ * moe_combine_backward -- the gradients of moe_combine:
+ *   dys[row_of[t,k]] = weights[t,k] * dout[t], zero in padding rows
+ *   dweights[t,k] = sum of dout[t] * ys[row_of[t,k]], 0 where dropped
+ * dys may be NULL (when fp8_moe_dispatch makes it in FP8); ys may be NULL with
+ * dweights.
+ */
+int moe_combine_backward(const void* dout, const void* ys, int64_t tokens, int topk,
+                         int64_t hidden, int dtype, const int* row_of, const int* src,
+                         const float* weights, int64_t rows, void* dys, float* dweights,
+                         const float* noop_flag, void* stream);
+
+/* ==========================================================================
+ * The junction between two blocks: the norm after a block, its gate, the
+ * residual sum and the norm before the next block, in one pass.  For every
+ * row, with a(w) = weight_offset + w (1 where w is NULL):
+ *     z       = u * rstd_post * a(w_post)     rstd_post = 1/sqrt(mean(u^2) + eps)
+ *     res_out = residual_scale * res + branch_scale * gate * z
+ *     y       = res_out * rstd_pre * a(w_pre) rstd_pre = 1/sqrt(mean(res_out^2) + eps)
+ * Without CT_NORM_POST z = u; without CT_NORM_PRE there is no y.  gate is
+ * [ceil(rows / rows_per_gate), hidden], row i using gate row i / rows_per_gate
+ * (rows_per_gate >= rows: one gate for all), NULL for 1.  u NULL (before the
+ * first block): y alone, of res; res_out is then NULL too.
+ *
+ * Everything between the inputs and the outputs is fp32 (y is computed from
+ * res_out before its rounding); each output is rounded once.  The pages have
+ * no counterpart to these two calls.
+ * ========================================================================== */
+typedef enum { CT_NORM_POST = 1, CT_NORM_PRE = 2 } ct_norm_flags;
+
+typedef struct {              /* a host struct, read during the call */
+    int64_t rows, hidden;     /* hidden <= 32768 */
+    int64_t rows_per_gate;    /* >= 1 where there is a gate */
+    const void* w_post;       /* [hidden] of param_dtype, nullable */
+    const void* w_pre;        /* [hidden] of param_dtype, nullable */
+    const void* gate;         /* [groups, hidden] of param_dtype, nullable */
+    float eps, branch_scale, residual_scale, weight_offset;
+    int dtype;                /* ct_dtype of u and y */
+    int res_dtype;            /* of res and res_out: dtype or CT_FP32 */
+    int param_dtype;          /* of w_post, w_pre and gate: dtype or CT_FP32 */
+    int flags;                /* ct_norm_flags */
+} ct_block_norm_config;
+
+/*
+ * block_norm -- the junction's forward pass.
+ *   u [rows, hidden], res and res_out [rows, hidden]; res_out may be res
+ *   itself (updated in place)
+ *   y         [rows, hidden] of type dtype, or, where `scale` is not NULL,
+ *             uint8: y = fp8(y * scale), with amax (max-merged, of y before
+ *             the scale) and scale_inv as in fp8_cast_transpose
+ *   rstd_post, rstd_pre  fp32 [rows], nullable: kept for the backward pass
+ *
+ * Errors: CT_ERR_NULL, CT_ERR_SHAPE, CT_ERR_ALIGN, CT_ERR_FORMAT (types, fmt),
+ * CT_ERR_ARG (flags, rows_per_gate, eps < 0), CT_ERR_ALIAS, CT_ERR_CUDA.
+ */
+int block_norm(const ct_block_norm_config* cfg, const void* u, const void* res, void* res_out,
+               void* y, float* rstd_post, float* rstd_pre, const float* scale, float* amax,
+               float* scale_inv, int fmt, const float* noop_flag, void* stream);
+
+/* Bytes of workspace block_norm_backward needs (16-byte aligned). */
+size_t block_norm_backward_workspace_size(int64_t rows, int64_t hidden);
+
+/*
+ * block_norm_backward -- its gradients.  From dy (of y) and dres_out (of
+ * res_out, nullable: zero), the forward pass's u, res_out, rstd_post and
+ * rstd_pre (without u: res and rstd_pre):
+ *   du [rows, hidden], dres [rows, hidden] (of type res_dtype)
+ *   dw_post, dw_pre [hidden], dgate [groups, hidden], of type param_dtype,
+ *   each nullable.  With rows = 0 they are set to zero.
+ * Column sums are fp32 in a fixed order: the same from call to call.
+ */
+int block_norm_backward(const ct_block_norm_config* cfg, const void* dy, const void* dres_out,
+                        const void* u, const void* res_out, const float* rstd_post,
+                        const float* rstd_pre, void* du, void* dres, void* dw_post, void* dw_pre,
+                        void* dgate, void* workspace, size_t workspace_bytes,
+                        const float* noop_flag, void* stream);
+
 /*
  * ct_device_error -- diagnostic word of the current device.  Kernels that
  * wait on an mbarrier give up after a bounded time (about two seconds)
