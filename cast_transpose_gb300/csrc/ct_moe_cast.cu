@@ -1,73 +1,202 @@
 // ct_moe_cast.cu -- rows gathered into expert order, weighted, cast to FP8 and
-// transposed in one pass.
+// transposed in one pass: q[r] = fp8(w[s] * x[s / K] * scale), s = src[r].
 #include "ct_device.cuh"
 #include "ct_ops.h"
 
 namespace ct {
 namespace {
 
-constexpr int kThreads_ = 256;
-constexpr int kPitch = 128 + 4;
+constexpr int kCastThreads = 256;
+constexpr int kStripTiles = 8;
 
-// One 128x128 tile of the sorted matrix per block, any shape and alignment:
-// element by element, with an FP8 copy in shared memory for the transpose.
+// Token of a sorted row and its weight; -1 for padding.
+__device__ __forceinline__ int token_of(const SortedCastArgs& a, int64_t row, float& w) {
+    const int s = a.src[row];
+    w = 0.0f;
+    if (s < 0 || s >= a.tokens * a.topk) return -1;
+    if (a.weights) w = a.weights[s];
+    return s / a.topk;
+}
+
+__device__ __forceinline__ unsigned max_bits(unsigned m, float v) {
+    return max(m, __float_as_uint(v) & 0x7FFFFFFFu);
+}
+
+// One 128x128 tile of the sorted matrix per block: hidden a multiple of 8, x
+// 16-byte and out 8-byte aligned; with the transpose, rows a multiple of 16
+// and out_t 16-byte aligned.
+template <int FMT, bool WEIGHTED, bool TRANSPOSE>
+__global__ void __launch_bounds__(kCastThreads, 4)
+    sorted_cast_kernel(const SortedCastArgs a, int tile_rows, int tile_cols) {
+    __shared__ __align__(16) uint8_t sq[TRANSPOSE ? 128 * 128 : 16];
+    __shared__ int token[128];
+    __shared__ float weight[WEIGHTED ? 128 : 1];
+    __shared__ unsigned warp_max[kCastThreads / 32];
+    dev::pdl_launch_dependents();
+    // strips of kStripTiles tile columns, top to bottom
+    const int strip = blockIdx.x / (kStripTiles * tile_rows);
+    const int width = min(kStripTiles, tile_cols - strip * kStripTiles);
+    const int in_strip = blockIdx.x - strip * kStripTiles * tile_rows;
+    const int rt = in_strip / width;
+    const int64_t row0 = int64_t(rt) * 128;
+    const int64_t col0 = int64_t(strip * kStripTiles + in_strip - rt * width) * 128;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    dev::pdl_wait();
+    if (a.noop && *a.noop != 0.0f) return;
+    if (tid < 128) {
+        float w = 0.0f;
+        token[tid] = row0 + tid < a.rows ? token_of(a, row0 + tid, w) : -1;
+        if (WEIGHTED) weight[tid] = w;
+    }
+    const float scale = *a.scale;
+    __syncthreads();
+
+    // columns 8c .. 8c+7 of rows rg + 16 i: all eight loads in flight at once
+    const int c = tid & 15, rg = tid >> 4;
+    const bool col_ok = col0 + 8 * c < a.hidden;
+    const uint16_t* x = a.x + col0 + 8 * c;
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int t = token[rg + 16 * i];
+        v[i] = col_ok && t >= 0 ? __ldg(reinterpret_cast<const uint4*>(x + t * a.hidden))
+                                : make_uint4(0u, 0u, 0u, 0u);
+    }
+    unsigned most = 0;
+    uint8_t* q = a.out + row0 * a.hidden + col0 + 8 * c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = rg + 16 * i;
+        uint2 q8;
+        if constexpr (WEIGHTED) {
+            // the product with the weight is a rounded fp32 value: it is what
+            // amax is taken of and what the scale multiplies
+            const float w = weight[r];
+            const uint32_t word[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                dev::mul2_rn(dev::bf16_lo(word[e]), dev::bf16_hi(word[e]), w, lo, hi);
+                most = max_bits(max_bits(most, lo), hi);
+                dev::mul2_rn(lo, hi, scale, lo, hi);
+                h[e] = dev::cvt_fp8x2<FMT>(lo, hi);
+            }
+            // a padding row's weight is 0 and its x is 0
+            q8 = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        } else {
+            most = dev::absmax_pair(most, v[i].x);
+            most = dev::absmax_pair(most, v[i].y);
+            most = dev::absmax_pair(most, v[i].z);
+            most = dev::absmax_pair(most, v[i].w);
+            q8 = dev::cast8<FMT>(v[i], scale);
+        }
+        if (col_ok && row0 + r < a.rows) __stcs(reinterpret_cast<uint2*>(q + r * a.hidden), q8);
+        if constexpr (TRANSPOSE)
+            *reinterpret_cast<uint2*>(sq + r * 128 + ((2 * c) ^ dev::swz(r)) * 4) = q8;
+    }
+    most = __reduce_max_sync(0xFFFFFFFFu, WEIGHTED ? most : dev::pair_to_f32_bits(most));
+    if (lane == 0) warp_max[warp] = most;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 1; i < kCastThreads / 32; ++i) most = max(most, warp_max[i]);
+        if (most) atomicMax(reinterpret_cast<unsigned*>(a.amax), most);
+        if (blockIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, scale);
+    }
+    if constexpr (TRANSPOSE) {
+        // rows 16b .. 16b+15 of the four columns of word w
+        const int b = lane & 7, w = warp * 4 + (lane >> 3);
+        const uint32_t* sq32 = reinterpret_cast<const uint32_t*>(sq);
+        uint32_t in[16], o[4][4];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int r = 16 * b + j;
+            in[j] = sq32[r * 32 + (w ^ dev::swz(r))];
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            dev::transpose4x4(in[4 * g], in[4 * g + 1], in[4 * g + 2], in[4 * g + 3], o[0][g],
+                              o[1][g], o[2][g], o[3][g]);
+        const int64_t row = row0 + 16 * b;
+        if (row < a.rows) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t col = col0 + 4 * w + k;
+                if (col < a.hidden)
+                    __stcs(reinterpret_cast<uint4*>(a.out_t + col * a.rows + row),
+                           make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]));
+            }
+        }
+    }
+}
+
+// Any shape and alignment, element by element, without the transpose: one
+// block per sorted row.
 template <int FMT>
-__global__ void __launch_bounds__(kThreads_) sorted_cast_kernel(SortedCastArgs a, int tile_cols) {
-    __shared__ uint8_t tile[128 * kPitch];
-    __shared__ int slot_of[128];
-    __shared__ unsigned amax_bits;
+__global__ void __launch_bounds__(kCastThreads) sorted_cast_any_kernel(const SortedCastArgs a) {
+    __shared__ unsigned warp_max[kCastThreads / 32];
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
+    const int64_t row = blockIdx.x;
     const int tid = threadIdx.x;
-    const int64_t row0 = int64_t(blockIdx.x / tile_cols) * 128;
-    const int64_t col0 = int64_t(blockIdx.x % tile_cols) * 128;
-    const int rows = static_cast<int>(min(int64_t(128), a.rows - row0));
-    const int cols = static_cast<int>(min(int64_t(128), a.hidden - col0));
     const float scale = *a.scale;
-    if (tid < 128) {
-        int s = tid < rows ? a.src[row0 + tid] : -1;
-        if (s >= a.tokens * a.topk) s = -1;
-        slot_of[tid] = s;
-    }
-    if (tid == 0) amax_bits = 0;
-    __syncthreads();
+    float w;
+    const int t = token_of(a, row, w);
     unsigned most = 0;
-    for (int i = tid; i < 128 * 128; i += kThreads_) {
-        const int r = i >> 7, c = i & 127;
-        if (r >= rows || c >= cols) continue;
-        const int s = slot_of[r];
+    for (int c = tid; c < a.hidden; c += kCastThreads) {
         float v = 0.0f;
-        if (s >= 0) {
-            v = __uint_as_float(uint32_t(a.x[int64_t(s / a.topk) * a.hidden + col0 + c]) << 16);
-            if (a.weights) v = __fmul_rn(a.weights[s], v);
-            most = max(most, __float_as_uint(v) & 0x7FFFFFFFu);
+        if (t >= 0) {
+            v = __uint_as_float(uint32_t(a.x[t * a.hidden + c]) << 16);
+            if (a.weights) v = __fmul_rn(w, v);
+            most = max_bits(most, v);
         }
-        const uint8_t q = static_cast<uint8_t>(dev::cvt_fp8x2<FMT>(__fmul_rn(v, scale), 0.0f));
-        tile[r * kPitch + c] = q;
-        a.out[(row0 + r) * a.hidden + col0 + c] = q;
+        a.out[row * a.hidden + c] =
+            static_cast<uint8_t>(dev::cvt_fp8x2<FMT>(__fmul_rn(v, scale), 0.0f));
     }
-    atomicMax(&amax_bits, most);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if ((tid & 31) == 0) warp_max[tid >> 5] = most;
     __syncthreads();
-    if (a.out_t)
-        for (int i = tid; i < 128 * 128; i += kThreads_) {
-            const int c = i >> 7, r = i & 127;
-            if (r < rows && c < cols) a.out_t[(col0 + c) * a.rows + row0 + r] = tile[r * kPitch + c];
-        }
     if (tid == 0) {
-        if (amax_bits) atomicMax(reinterpret_cast<unsigned*>(a.amax), amax_bits);
-        if (blockIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+        for (int i = 1; i < kCastThreads / 32; ++i) most = max(most, warp_max[i]);
+        if (most) atomicMax(reinterpret_cast<unsigned*>(a.amax), most);
+        if (row == 0) *a.scale_inv = __fdiv_rn(1.0f, scale);
     }
+}
+
+bool at16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <int FMT>
+cudaError_t launch_fmt(const SortedCastArgs& a, cudaStream_t stream) {
+    const bool fast = a.hidden % 8 == 0 && at16(a.x) && reinterpret_cast<uintptr_t>(a.out) % 8 == 0;
+    const bool together = a.out_t && fast && a.rows % 16 == 0 && at16(a.out_t);
+    cudaError_t e;
+    if (fast) {
+        const int tile_rows = static_cast<int>((a.rows + 127) / 128);
+        const int tile_cols = static_cast<int>((a.hidden + 127) / 128);
+        const dim3 grid(static_cast<unsigned>(int64_t(tile_rows) * tile_cols));
+        auto* kernel = a.weights ? (together ? sorted_cast_kernel<FMT, true, true>
+                                             : sorted_cast_kernel<FMT, true, false>)
+                                 : (together ? sorted_cast_kernel<FMT, false, true>
+                                             : sorted_cast_kernel<FMT, false, false>);
+        e = launch_pdl(kernel, grid, dim3(kCastThreads), 0, stream, a, tile_rows, tile_cols);
+    } else {
+        e = launch_pdl(sorted_cast_any_kernel<FMT>, dim3(static_cast<unsigned>(a.rows)),
+                       dim3(kCastThreads), 0, stream, a);
+    }
+    if (e != cudaSuccess || !a.out_t || together) return e;
+    // rows that are no multiple of 16, or odd alignments: the byte transpose of
+    // what was just written
+    const bool aligned_t = a.rows % 16 == 0 && a.hidden % 16 == 0 && at16(a.out) && at16(a.out_t);
+    return launch_transpose(a.out, a.rows, a.hidden, a.out_t, a.noop, aligned_t, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_sorted_cast(const SortedCastArgs& a, int fmt, cudaStream_t stream) {
-    const int tile_cols = static_cast<int>((a.hidden + 127) / 128);
-    const int64_t tiles = (a.rows + 127) / 128 * tile_cols;
-    auto* kernel = fmt == 0 ? sorted_cast_kernel<0> : sorted_cast_kernel<1>;
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles)), dim3(kThreads_), 0, stream, a,
-                      tile_cols);
+    return fmt == 0 ? launch_fmt<0>(a, stream) : launch_fmt<1>(a, stream);
 }
 
 }  // namespace ct
