@@ -5,6 +5,9 @@
 #include "ct_ops.h"
 #include "ct_types.cuh"
 
+#include <algorithm>
+#include <cooperative_groups.h>
+
 namespace ct {
 namespace {
 
@@ -17,6 +20,17 @@ using dev::pdl_wait;
 // its expert's is (slots of earlier blocks) + (of earlier warps) + (earlier in
 // the warp's run): the first two are exclusive sums of counts, the third is
 // counted on the way, 32 slots at a time, from the lanes with the same expert.
+// Integers only, no atomics.  What it moves is small (12 bytes a slot); the
+// time is latency, so blocks learn each other's counts in the cheapest way
+// their number allows:
+//   kOne      one block, up to kSortOneBlock slots
+//   kCluster  one cluster of kSortCluster blocks, counts read from its other
+//             blocks' shared memory: still one launch
+//   kGrid     a first launch leaves every block's counts in the workspace
+enum SortMode { kOne, kCluster, kGrid };
+constexpr int kSortMaxThreads = 1024;
+constexpr int kSortCluster = 8;
+constexpr int kSortBatch = 4;         // groups of 32 slots loaded ahead of their counting
 
 __device__ __forceinline__ int expert_of(const SortArgs& a, int64_t s) {
     const int64_t e = a.index64 ? static_cast<const int64_t*>(a.idx)[s]
@@ -24,200 +38,378 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, int64_t s) {
     return e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
 }
 
-constexpr int kSortThreads = 512;
-constexpr int kSortWarps = kSortThreads / 32;
+// Calls f(slot, expert, lanes of the same expert) for the slots [lo, hi) of a
+// warp, 32 at a time in order; lanes past hi get expert -1.
+template <typename F>
+__device__ __forceinline__ void walk(const SortArgs& a, int64_t lo, int64_t hi, F&& f) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t s0 = lo; s0 < hi; s0 += 32 * kSortBatch) {
+        int e[kSortBatch];
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i) {
+            const int64_t s = s0 + 32 * i + lane;
+            e[i] = s < hi ? expert_of(a, s) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i) {
+            if (s0 + 32 * i >= hi) break;
+            f(s0 + 32 * i + lane, e[i], __match_any_sync(0xFFFFFFFFu, e[i]));
+            __syncwarp();
+        }
+    }
+}
 
-// One block: hist is [kSortWarps][E] in shared memory.
-__global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(SortArgs a) {
+// The run of this warp.
+__device__ __forceinline__ void run_of(const SortArgs& a, int64_t& lo, int64_t& hi) {
+    const int64_t warps = blockDim.x >> 5, runs = gridDim.x * warps;
+    const int64_t len = ((a.n + runs - 1) / runs + 31) / 32 * 32;
+    lo = min(a.n, len * (blockIdx.x * warps + (threadIdx.x >> 5)));
+    hi = min(a.n, lo + len);
+}
+
+// hist[warp][E]: the slots of each warp's run by expert.
+__device__ __forceinline__ void count_run(const SortArgs& a, int* hist, int64_t lo, int64_t hi) {
+    for (int i = threadIdx.x; i < int(blockDim.x >> 5) * a.experts; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    int* mine = hist + (threadIdx.x >> 5) * a.experts;
+    walk(a, lo, hi, [&](int64_t, int e, unsigned same) {
+        if (e >= 0 && int(threadIdx.x & 31) == __ffs(same) - 1) mine[e] += __popc(same);
+    });
+    __syncthreads();
+}
+
+// The block's slots of expert e, all warps.
+__device__ __forceinline__ int block_count(const SortArgs& a, const int* hist, int e) {
+    int count = 0;
+    for (int w = 0; w < int(blockDim.x >> 5); ++w) count += hist[w * a.experts + e];
+    return count;
+}
+
+// Counts of every block's run, block_counts[block][E], for kGrid.
+__global__ void __launch_bounds__(kSortMaxThreads) moe_count_kernel(SortArgs a, int* block_counts) {
     extern __shared__ int smem[];
-    int* hist = smem;
-    int* first = smem + kSortWarps * a.experts;   // [E]: first row of the expert
     pdl_launch_dependents();
     pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
+    int64_t lo, hi;
+    run_of(a, lo, hi);
+    count_run(a, smem, lo, hi);
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+        block_counts[int64_t(blockIdx.x) * a.experts + e] = block_count(a, smem, e);
+}
+
+// Ints of dynamic shared memory: the warps' counts, then per expert the sums
+// below, its first row (and the end), its total, the block's own count.
+__host__ __device__ constexpr int sort_ints(int warps, int experts) {
+    return (warps + 5) * experts + 1;
+}
+
+template <SortMode MODE>
+__global__ void __launch_bounds__(kSortMaxThreads)
+    moe_sort_kernel(SortArgs a, const int* block_counts) {
+    extern __shared__ int smem[];
+    __shared__ int64_t warp_sums[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.experts;
-    const int64_t per_warp = ((a.n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const int64_t lo = per_warp * warp, hi = min(a.n, lo + per_warp);
-    for (int i = tid; i < kSortWarps * E; i += kSortThreads) hist[i] = 0;
-    __syncthreads();
-    int* mine = hist + warp * E;
-    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
-        const int e = s0 + lane < hi ? expert_of(a, s0 + lane) : -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+    const int threads = blockDim.x, warps = threads >> 5;
+    const int b = blockIdx.x, blocks = gridDim.x;
+    int* hist = smem;                   // [warps][E]
+    int* before = hist + warps * E;     // [E]: slots of earlier blocks
+    int* total = before + E;            // [E]: of all blocks
+    int* own = total + E;               // [E]: of this block (kCluster)
+    int* first = own + E;               // [E + 1]: first row
+    pdl_launch_dependents();
+    pdl_wait();
+    if (a.noop && *a.noop != 0.0f) return;
+    int64_t lo, hi;
+    run_of(a, lo, hi);
+    count_run(a, hist, lo, hi);
+    if constexpr (MODE == kOne) {
+        for (int e = tid; e < E; e += threads) {
+            before[e] = 0;
+            total[e] = block_count(a, hist, e);
+        }
+    } else if constexpr (MODE == kCluster) {
+        const auto cluster = cooperative_groups::this_cluster();
+        for (int e = tid; e < E; e += threads) own[e] = block_count(a, hist, e);
+        cluster.sync();
+        for (int e = tid; e < E; e += threads) {
+            int c[kSortCluster], earlier = 0, all = 0;
+#pragma unroll
+            for (int o = 0; o < kSortCluster; ++o) c[o] = cluster.map_shared_rank(own, o)[e];
+#pragma unroll
+            for (int o = 0; o < kSortCluster; ++o) {
+                earlier += o < b ? c[o] : 0;
+                all += c[o];
+            }
+            before[e] = earlier;
+            total[e] = all;
+        }
+        cluster.sync();   // no block leaves while another reads its counts
+    } else {
+        for (int e = tid; e < E; e += threads) before[e] = total[e] = 0;
+        __syncthreads();
+        // `parts` threads per expert, each over a share of the blocks
+        const int parts = max(1, threads / E), share = (blocks + parts - 1) / parts;
+        for (int i = tid; i < parts * E; i += threads) {
+            const int e = i % E, o0 = i / E * share, o1 = min(blocks, o0 + share);
+            int earlier = 0, all = 0;
+#pragma unroll 8
+            for (int o = o0; o < o1; ++o) {
+                const int c = block_counts[int64_t(o) * E + e];
+                all += c;
+                earlier += o < b ? c : 0;
+            }
+            atomicAdd(&before[e], earlier);   // integers: any order gives the same
+            atomicAdd(&total[e], all);
+        }
     }
     __syncthreads();
-    // counts per expert, padded, and their exclusive sum in expert order
+    // first rows: the exclusive sum of the padded totals in expert order
     int64_t base = 0;
-    for (int e0 = 0; e0 < E; e0 += kSortThreads) {
+    for (int e0 = 0; e0 < E; e0 += threads) {
         const int e = e0 + tid;
-        int count = 0;
-        if (e < E)
-            for (int w = 0; w < kSortWarps; ++w) {
+        int64_t padded = 0;
+        if (e < E) {
+            padded = (int64_t(total[e]) + a.align - 1) / a.align * a.align;
+            int at = before[e];
+            for (int w = 0; w < warps; ++w) {
                 const int c = hist[w * E + e];
-                hist[w * E + e] = count;
-                count += c;
+                hist[w * E + e] = at;
+                at += c;
             }
-        const int padded = static_cast<int>((int64_t(count) + a.align - 1) / a.align * a.align);
+        }
         int64_t sum = padded;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += up;
         }
-        __shared__ int64_t warp_sums[kSortWarps];
         if (lane == 31) warp_sums[warp] = sum;
         __syncthreads();
-        int64_t before = base, all = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            if (w < warp) before += warp_sums[w];
-            all += warp_sums[w];
+        int64_t begin = base + sum - padded;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) begin += warp_sums[w];
+            base += warp_sums[w];
         }
-        const int64_t begin = before + sum - padded;
-        if (e < E) {
-            first[e] = static_cast<int>(min(begin, a.rows));
-            a.offsets[e] = first[e];
-            a.counts[e] = count;
-            // padding rows of this expert
-            const int64_t end = min(begin + padded, a.rows);
-            for (int64_t r = begin + count; r < end; ++r) a.src[r] = -1;
-        }
-        base += all;
+        if (e < E) first[e] = static_cast<int>(min(begin, a.rows));
         __syncthreads();
     }
-    const int64_t end = min(base, a.rows);
-    if (tid == 0) a.offsets[E] = static_cast<int>(end);
-    for (int64_t r = end + tid; r < a.rows; r += kSortThreads) a.src[r] = -1;
-    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
-        const int64_t s = s0 + lane;
-        const int e = s < hi ? expert_of(a, s) : -1;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
-        if (s < hi) {
-            int64_t row = -1;
-            if (e >= 0) {
-                row = int64_t(first[e]) + mine[e] + __popc(same & ((1u << lane) - 1));
-                if (row >= a.rows) row = -1;
-            }
-            a.row_of[s] = static_cast<int>(row);
-            if (row >= 0) a.src[row] = static_cast<int>(s);
+    const int end = static_cast<int>(min(base, a.rows));
+    if (tid == 0) first[E] = end;
+    __syncthreads();
+    walk(a, lo, hi, [&](int64_t s, int e, unsigned same) {
+        int* mine = hist + warp * E;
+        int64_t row = -1;
+        if (e >= 0) {
+            row = int64_t(first[e]) + mine[e] + __popc(same & ((1u << lane) - 1));
+            if (row >= a.rows) row = -1;
         }
+        if (s < hi) a.row_of[s] = static_cast<int>(row);
+        if (row >= 0) a.src[row] = static_cast<int>(s);
         __syncwarp();
         if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+    });
+    if (b == 0) {
+        for (int e = tid; e <= E; e += threads) a.offsets[e] = first[e];
+        for (int e = tid; e < E; e += threads) a.counts[e] = total[e];
     }
+    // padding rows: a warp per expert, then the rows after the last expert
+    for (int e = b * warps + warp; e < E; e += blocks * warps)
+        for (int64_t r = int64_t(first[e]) + total[e] + lane; r < first[e + 1]; r += 32) a.src[r] = -1;
+    for (int64_t r = int64_t(end) + b * threads + tid; r < a.rows; r += int64_t(blocks) * threads)
+        a.src[r] = -1;
 }
 
 // ---- row movement ----------------------------------------------------------
-__device__ __forceinline__ int64_t row_at(const MoveArgs& a, int64_t slot) {
-    const int r = a.row_of[slot];
-    return r >= 0 && r < a.rows ? r : -1;
+// One block per token: its row is read once and written to its K places, or
+// gathered from them, so that neither order's rows move twice.  Bound by HBM.
+constexpr int kMaxSlots = 64;         // K at most
+constexpr int kMoveThreads = 256;
+
+// The sorted row of each of token t's slots, -1 where dropped or out of range.
+__device__ __forceinline__ void token_rows(const MoveArgs& a, int64_t t, int (&rows)[kMaxSlots]) {
+    if (threadIdx.x < 32)
+        for (int k = threadIdx.x; k < a.topk; k += 32) {
+            const int r = a.row_of[t * a.topk + k];
+            rows[k] = r >= 0 && r < a.rows ? r : -1;
+        }
+    __syncthreads();
 }
 
-// W: the word that rows are moved in (their bytes are a multiple of it).
-// Blocks 0 .. T-1 copy their token's row to its K places; the others look
-// for padding rows, 32 rows to a block, and clear them.
-constexpr int kMoveThreads = 256;
+// A launch that writes sorted rows has blocks for the padding rows before
+// those of the tokens: each looks at 32 rows and clears the ones without a slot.
 constexpr int kPadRows = 32;
 
 template <typename W>
-__device__ void clear_padding(const MoveArgs& a, int64_t block, int words) {
-    const int64_t r0 = block * kPadRows;
-    for (int i = 0; i < kPadRows && r0 + i < a.rows; ++i) {
-        const int s = a.src[r0 + i];
-        if (s >= 0 && s < a.tokens * a.topk) continue;
-        W* row = static_cast<W*>(a.sorted) + (r0 + i) * words;
-        for (int c = threadIdx.x; c < words; c += blockDim.x) row[c] = W{};
+__device__ void clear_padding(const MoveArgs& a, int64_t words) {
+    const int64_t row0 = int64_t(blockIdx.x) * kPadRows, row = row0 + (threadIdx.x & 31);
+    bool empty = false;
+    if (row < a.rows) {
+        const int s = a.src[row];
+        empty = s < 0 || s >= a.tokens * a.topk;
+    }
+    for (unsigned left = __ballot_sync(0xFFFFFFFFu, empty); left; left &= left - 1) {
+        W* out = static_cast<W*>(a.sorted) + (row0 + __ffs(left) - 1) * words;
+        for (int64_t c = threadIdx.x; c < words; c += blockDim.x) out[c] = W{};
     }
 }
 
+// W: the word that rows are moved in.  kMoveWords loads of a thread are in
+// flight at a time.
+constexpr int kMoveWords = 4;
+
 template <typename W>
-__global__ void __launch_bounds__(kMoveThreads) moe_dispatch_kernel(MoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads) moe_dispatch_kernel(MoveArgs a, int pad_blocks) {
+    __shared__ int rows[kMaxSlots];
     pdl_launch_dependents();
     pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     const int words = static_cast<int>(a.hidden * a.elem_bytes / sizeof(W));
-    const int64_t t = blockIdx.x;
-    if (t >= a.tokens) {
-        clear_padding<W>(a, t - a.tokens, words);
+    if (blockIdx.x < pad_blocks) {
+        clear_padding<W>(a, words);
         return;
     }
+    const int64_t t = blockIdx.x - pad_blocks;
+    token_rows(a, t, rows);
     const W* x = static_cast<const W*>(a.x) + t * words;
-    W* out = static_cast<W*>(a.sorted);
-    for (int c = threadIdx.x; c < words; c += kMoveThreads) {
-        const W v = x[c];
-        for (int k = 0; k < a.topk; ++k) {
-            const int64_t r = row_at(a, t * a.topk + k);
-            if (r >= 0) out[r * words + c] = v;
+    for (int c0 = threadIdx.x; c0 < words; c0 += kMoveWords * blockDim.x) {
+        W v[kMoveWords];
+#pragma unroll
+        for (int i = 0; i < kMoveWords; ++i) {
+            const int c = c0 + i * blockDim.x;
+            if (c < words) v[i] = __ldcs(x + c);
         }
+        for (int k = 0; k < a.topk; ++k) {
+            if (rows[k] < 0) continue;
+            W* out = static_cast<W*>(a.sorted) + int64_t(rows[k]) * words;
+#pragma unroll
+            for (int i = 0; i < kMoveWords; ++i) {
+                const int c = c0 + i * blockDim.x;
+                if (c < words) __stcs(out + c, v[i]);
+            }
+        }
+    }
+}
+
+// Slots handled together, so that their rows' loads are in flight at once.
+constexpr int kSlotGroup = 4;
+
+// Calls f(cols) for the block's threads' groups of eight columns.
+template <bool VEC, typename F>
+__device__ __forceinline__ void each_cols(int H, F&& f) {
+    const int threads = blockDim.x;
+    for (int v = threadIdx.x; v / threads * threads * 8 < H; v += threads) {
+        const dev::Cols<VEC> cols(v, threads, H);
+        if (cols.any()) f(cols);
     }
 }
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMoveThreads) moe_combine_kernel(MoveArgs a) {
+    __shared__ int rows[kMaxSlots];
     pdl_launch_dependents();
     pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     const int64_t t = blockIdx.x;
-    const int H = static_cast<int>(a.hidden);
     const T* ys = static_cast<const T*>(a.ys);
-    for (int v = threadIdx.x; v * 8 < H + 8 * kMoveThreads; v += kMoveThreads) {
-        const dev::Cols<VEC> cols(v, kMoveThreads, H);
-        if (!cols.any()) continue;
+    const float* weights = a.weights ? a.weights + t * a.topk : nullptr;
+    token_rows(a, t, rows);
+    each_cols<VEC>(static_cast<int>(a.hidden), [&](const dev::Cols<VEC>& cols) {
         float sum[8] = {};
-        for (int k = 0; k < a.topk; ++k) {
-            const int64_t r = row_at(a, t * a.topk + k);
-            if (r < 0) continue;
-            float f[8];
-            dev::load_cols<VEC>(ys + r * a.hidden, cols, f);
-            const float w = a.weights ? a.weights[t * a.topk + k] : 1.0f;
+        for (int k0 = 0; k0 < a.topk; k0 += kSlotGroup) {
+            float f[kSlotGroup][8], w[kSlotGroup];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] = fmaf(w, f[j], sum[j]);
+            for (int i = 0; i < kSlotGroup; ++i) {
+                const int r = k0 + i < a.topk ? rows[k0 + i] : -1;
+                // a slot that is dropped takes no part, whatever its weight
+                w[i] = r >= 0 ? (weights ? weights[k0 + i] : 1.0f) : 0.0f;
+                if (r >= 0) {
+                    dev::load_cols<VEC>(ys + r * a.hidden, cols, f[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kSlotGroup; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] = fmaf(w[i], f[i][j], sum[j]);
         }
         dev::store_cols<VEC>(static_cast<T*>(a.out) + t * a.hidden, cols, sum);
-    }
+    });
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kMoveThreads) moe_combine_backward_kernel(MoveArgs a) {
-    __shared__ float slots[2][kMoveThreads / 32];
+__global__ void __launch_bounds__(kMoveThreads) moe_combine_backward_kernel(MoveArgs a, int pad_blocks) {
+    __shared__ int rows[kMaxSlots];
+    __shared__ float4 slots[2][kMoveThreads / 32];
+    static_assert(kSlotGroup == 4, "the sums of a group travel as a float4");
     pdl_launch_dependents();
     pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    const int64_t t = blockIdx.x;
     const int H = static_cast<int>(a.hidden);
-    if (t >= a.tokens) {
-        clear_padding<T>(a, t - a.tokens, H);
+    if (blockIdx.x < pad_blocks) {
+        if (VEC)
+            clear_padding<uint4>(a, a.hidden * sizeof(T) / 16);
+        else
+            clear_padding<T>(a, H);
         return;
     }
+    const int64_t t = blockIdx.x - pad_blocks;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const T* dout = static_cast<const T*>(a.x) + t * a.hidden;
     const T* ys = static_cast<const T*>(a.ys);
     T* dys = static_cast<T*>(a.sorted);
-    for (int k = 0; k < a.topk; ++k) {
-        const int64_t s = t * a.topk + k, r = row_at(a, s);
-        float dot = 0.0f;
-        if (r >= 0) {
-            const float w = a.weights ? a.weights[s] : 1.0f;
-            for (int v = threadIdx.x; v * 8 < H + 8 * kMoveThreads; v += kMoveThreads) {
-                const dev::Cols<VEC> cols(v, kMoveThreads, H);
-                if (!cols.any()) continue;
-                float g[8], f[8];
-                dev::load_cols<VEC>(dout, cols, g);
-                if (a.dweights) {
-                    dev::load_cols<VEC>(ys + r * a.hidden, cols, f);
+    token_rows(a, t, rows);
+    for (int k0 = 0; k0 < a.topk; k0 += kSlotGroup) {
+        int r[kSlotGroup];
+        float w[kSlotGroup], dot[kSlotGroup] = {};
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dot = fmaf(g[j], f[j], dot);
+        for (int i = 0; i < kSlotGroup; ++i) {
+            r[i] = k0 + i < a.topk ? rows[k0 + i] : -1;
+            w[i] = dys && r[i] >= 0 ? a.weights[t * a.topk + k0 + i] : 0.0f;
+        }
+        each_cols<VEC>(H, [&](const dev::Cols<VEC>& cols) {
+            float g[8], f[kSlotGroup][8];
+            dev::load_cols<VEC>(dout, cols, g);
+            if (a.dweights) {
+#pragma unroll
+                for (int i = 0; i < kSlotGroup; ++i) {
+                    if (r[i] >= 0) {
+                        dev::load_cols<VEC>(ys + r[i] * a.hidden, cols, f[i]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
+                    }
                 }
-                if (dys) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) g[j] *= w;
-                    dev::store_cols<VEC>(dys + r * a.hidden, cols, g);
+                for (int i = 0; i < kSlotGroup; ++i)
+                    if (r[i] >= 0) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) dot[i] = fmaf(g[j], f[i][j], dot[i]);
+                    }
+            }
+            if (dys) {
+#pragma unroll
+                for (int i = 0; i < kSlotGroup; ++i) {
+                    if (r[i] < 0) continue;
+                    float d[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[j] = w[i] * g[j];
+                    dev::store_cols<VEC>(dys + r[i] * a.hidden, cols, d);
                 }
             }
-        }
-        if (a.dweights) {
-            dot = dev::block_sum(dot, slots[k & 1]);
-            if (threadIdx.x == 0) a.dweights[s] = dot;
+        });
+        if (!a.dweights) continue;
+#pragma unroll
+        for (int i = 0; i < kSlotGroup; ++i) dot[i] = dev::warp_sum(dot[i]);
+        float4* half = slots[(k0 / kSlotGroup) & 1];
+        if (lane == 0) half[warp] = make_float4(dot[0], dot[1], dot[2], dot[3]);
+        __syncthreads();
+        if (threadIdx.x < kSlotGroup && k0 + threadIdx.x < a.topk) {
+            float sum = 0.0f;
+            for (int i = 0; i < warps; ++i) sum += reinterpret_cast<const float*>(half + i)[threadIdx.x];
+            a.dweights[t * a.topk + k0 + threadIdx.x] = sum;
         }
     }
 }
@@ -229,8 +421,14 @@ bool vectors(const MoveArgs& a) {
            ok(a.sorted) && ok(a.out);
 }
 
-unsigned pad_blocks(const MoveArgs& a) {
-    return static_cast<unsigned>(a.sorted ? (a.rows + kPadRows - 1) / kPadRows : 0);
+int pad_blocks(const MoveArgs& a) {
+    return static_cast<int>(a.sorted ? (a.rows + kPadRows - 1) / kPadRows : 0);
+}
+
+// Threads of a block whose rows have `groups` words or groups of columns.
+dim3 move_threads(int64_t groups, int per_thread) {
+    const int64_t t = (groups + per_thread - 1) / per_thread;
+    return dim3(static_cast<unsigned>(std::min<int64_t>(kMoveThreads, std::max<int64_t>(32, (t + 31) / 32 * 32))));
 }
 
 template <typename F>
@@ -242,43 +440,100 @@ cudaError_t by_type(int dtype, F&& f) {
 
 }  // namespace
 
-size_t sort_workspace(int64_t, int) { return 0; }
+constexpr int64_t kSortOneBlock = 1024, kSortClusterMost = 65536;
+constexpr int64_t kSortBlockSlots = 2048, kSortMaxBlocks = 128;
 
-cudaError_t launch_moe_sort(const SortArgs& a, void*, cudaStream_t stream) {
-    const size_t smem = sizeof(int) * (kSortWarps + 1) * a.experts;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+SortMode sort_mode(int64_t n) {
+    return n <= kSortOneBlock ? kOne : n <= kSortClusterMost ? kCluster : kGrid;
+}
+
+int grid_blocks(int64_t n) {
+    return static_cast<int>(std::min(kSortMaxBlocks, (n + kSortBlockSlots - 1) / kSortBlockSlots));
+}
+
+size_t sort_workspace(int64_t n, int experts) {
+    if (sort_mode(n) != kGrid) return 0;
+    return (sizeof(int) * grid_blocks(n) * size_t(experts) + 15) / 16 * 16;
+}
+
+cudaError_t launch_moe_sort(const SortArgs& a, void* workspace, cudaStream_t stream) {
+    const SortMode mode = sort_mode(a.n);
+    const int64_t most = std::max<int64_t>(a.n, a.experts);
+    const int threads = mode != kOne ? kSortMaxThreads
+                        : static_cast<int>(std::min<int64_t>(kSortMaxThreads, std::max<int64_t>(
+                                                                 128, (most + 31) / 32 * 32)));
+    const size_t smem = sizeof(int) * sort_ints(threads / 32, a.experts);
+    auto prepare = [&](const void* kernel) {
+        return smem <= 47 * 1024 ? cudaSuccess   // 48 KB with the static part
+                               
+                                 : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                        static_cast<int>(smem));
+    };
+    cudaError_t e;
+    if (mode == kOne) {
+        e = prepare(reinterpret_cast<const void*>(moe_sort_kernel<kOne>));
         if (e != cudaSuccess) return e;
+        return launch_pdl(moe_sort_kernel<kOne>, dim3(1), dim3(threads), smem, stream, a,
+                          static_cast<const int*>(nullptr));
     }
-    return launch_pdl(moe_sort_kernel, dim3(1), dim3(kSortThreads), smem, stream, a);
+    if (mode == kCluster) {
+        e = prepare(reinterpret_cast<const void*>(moe_sort_kernel<kCluster>));
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kSortCluster);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kSortCluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, moe_sort_kernel<kCluster>, a,
+                                  static_cast<const int*>(nullptr));
+    }
+    e = prepare(reinterpret_cast<const void*>(moe_sort_kernel<kGrid>));
+    if (e == cudaSuccess) e = prepare(reinterpret_cast<const void*>(moe_count_kernel));
+    if (e != cudaSuccess) return e;
+    const dim3 blocks(grid_blocks(a.n));
+    int* block_counts = static_cast<int*>(workspace);
+    e = launch_pdl(moe_count_kernel, blocks, dim3(threads), smem, stream, a, block_counts);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(moe_sort_kernel<kGrid>, blocks, dim3(threads), smem, stream, a,
+                      static_cast<const int*>(block_counts));
 }
 
 cudaError_t launch_moe_dispatch(const MoveArgs& a, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.tokens) + pad_blocks(a));
-    if (vectors(a))
-        return launch_pdl(moe_dispatch_kernel<uint4>, grid, dim3(kMoveThreads), 0, stream, a);
-    if (a.elem_bytes == 4)
-        return launch_pdl(moe_dispatch_kernel<uint32_t>, grid, dim3(kMoveThreads), 0, stream, a);
-    return launch_pdl(moe_dispatch_kernel<uint16_t>, grid, dim3(kMoveThreads), 0, stream, a);
+    const int pad = pad_blocks(a);
+    auto go = [&](auto w) {
+        using W = decltype(w);
+        return launch_pdl(moe_dispatch_kernel<W>, dim3(static_cast<unsigned>(a.tokens + pad)),
+                          move_threads(a.hidden * a.elem_bytes / int64_t(sizeof(W)), 3), 0, stream, a, pad);
+    };
+    if (vectors(a)) return go(uint4{});
+    return a.elem_bytes == 4 ? go(uint32_t{}) : go(uint16_t{});
 }
 
 cudaError_t launch_moe_combine(const MoveArgs& a, int dtype, cudaStream_t stream) {
     return by_type(dtype, [&](auto z) {
         using T = decltype(z);
         auto* kernel = vectors(a) ? moe_combine_kernel<T, true> : moe_combine_kernel<T, false>;
-        return launch_pdl(kernel, dim3(static_cast<unsigned>(a.tokens)), dim3(kMoveThreads), 0,
-                          stream, a);
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(a.tokens)),
+                          move_threads((a.hidden + 7) / 8, 1), 0, stream, a);
     });
 }
 
 cudaError_t launch_moe_combine_backward(const MoveArgs& a, int dtype, cudaStream_t stream) {
+    const int pad = pad_blocks(a);
     return by_type(dtype, [&](auto z) {
         using T = decltype(z);
         auto* kernel = vectors(a) ? moe_combine_backward_kernel<T, true>
                                   : moe_combine_backward_kernel<T, false>;
-        return launch_pdl(kernel, dim3(static_cast<unsigned>(a.tokens) + pad_blocks(a)),
-                          dim3(kMoveThreads), 0, stream, a);
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(a.tokens + pad)),
+                          move_threads((a.hidden + 7) / 8, 1), 0, stream, a, pad);
     });
 }
 
