@@ -10,6 +10,7 @@
 #include "../../include/cast_transpose.h"
 #include "ct_checks.h"
 #include "ct_internal.h"
+#include "ct_ops.h"
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -561,7 +562,11 @@ int ct_selftest_bounded_wait(unsigned int limit_us, void* stream) {
 
 int ct_device_error(unsigned int* value_out, int clear) {
     if (!value_out) return CT_ERR_NULL;
-    return cuda_status(ct::read_device_error(value_out, clear != 0));
+    unsigned casts = 0, norms = 0;
+    cudaError_t e = ct::read_device_error(&casts, clear != 0);
+    if (e == cudaSuccess) e = ct::read_norm_error(&norms, clear != 0);
+    if (e == cudaSuccess) *value_out = casts | norms;
+    return cuda_status(e);
 }
 
 }  // extern "C"

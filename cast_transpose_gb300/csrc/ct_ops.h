@@ -82,4 +82,7 @@ size_t norm_backward_workspace(int64_t rows, int64_t hidden);
 cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int res_dtype,
                                        cudaStream_t stream);
 
+// The block-norm kernels' own diagnostic word, as read_device_error.
+cudaError_t read_norm_error(unsigned* value, bool clear);
+
 }  // namespace ct

@@ -16,6 +16,7 @@ using ct::range_of;
 
 constexpr int kMaxExperts = 1024, kMaxTopk = 64, kMaxAlign = 1024;
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxElements = int64_t(1) << 40;   // of a sorted matrix
 constexpr int64_t kMaxMoveHidden = int64_t(1) << 20, kMaxNormHidden = 32768;
 
 bool dtype_ok(int d) { return d == CT_BF16 || d == CT_FP16 || d == CT_FP32; }
@@ -49,7 +50,8 @@ int check_move(int64_t tokens, int topk, int64_t hidden, int64_t rows, int dtype
     if (!dtype_ok(dtype)) return CT_ERR_FORMAT;
     if (topk < 1 || topk > kMaxTopk) return CT_ERR_ARG;
     if (tokens < 0 || hidden < 0 || rows < 0 || hidden > kMaxMoveHidden ||
-        tokens > kMaxIndex / topk || rows > kMaxIndex)
+        tokens > kMaxIndex / topk || rows > kMaxIndex ||
+        (hidden > 0 && rows > kMaxElements / hidden))
         return CT_ERR_SHAPE;
     return CT_OK;
 }
@@ -241,6 +243,11 @@ int fp8_moe_dispatch(const void* x, int64_t tokens, int topk, int64_t hidden, co
     return cuda_status(ct::launch_sorted_cast(a, fmt, static_cast<cudaStream_t>(stream)));
 }
 
+// rows_per_gate, no larger than what it can make a difference for.
+static int64_t gate_rows(const ct_block_norm_config& c) {
+    return c.rows_per_gate < c.rows ? c.rows_per_gate : (c.rows > 0 ? c.rows : 1);
+}
+
 // The config's own fields; `groups` receives the gate's rows.
 static int check_config(const ct_block_norm_config* c, int64_t* groups) {
     if (!c) return CT_ERR_NULL;
@@ -251,7 +258,7 @@ static int check_config(const ct_block_norm_config* c, int64_t* groups) {
     if (c->rows < 0 || c->hidden < 0 || c->hidden > kMaxNormHidden || c->rows > kMaxIndex)
         return CT_ERR_SHAPE;
     if (!(c->eps >= 0.0f) || (c->gate && c->rows_per_gate < 1)) return CT_ERR_ARG;
-    *groups = c->gate ? (c->rows + c->rows_per_gate - 1) / c->rows_per_gate : 0;
+    *groups = c->gate ? (c->rows + gate_rows(*c) - 1) / gate_rows(*c) : 0;
     return CT_OK;
 }
 
@@ -298,7 +305,7 @@ int block_norm(const ct_block_norm_config* cfg, const void* u, const void* res, 
     a.scale_inv = scale_inv;
     a.noop = noop_flag;
     a.rows = c.rows;
-    a.rows_per_gate = c.rows_per_gate;
+    a.rows_per_gate = gate_rows(c);
     a.eps = c.eps;
     a.branch_scale = c.branch_scale;
     a.residual_scale = c.residual_scale;
@@ -371,7 +378,7 @@ int block_norm_backward(const ct_block_norm_config* cfg, const void* dy, const v
     a.workspace = static_cast<float*>(workspace);
     a.noop = noop_flag;
     a.rows = c.rows;
-    a.rows_per_gate = c.rows_per_gate;
+    a.rows_per_gate = gate_rows(c);
     a.branch_scale = c.branch_scale;
     a.residual_scale = c.residual_scale;
     a.weight_offset = c.weight_offset;
