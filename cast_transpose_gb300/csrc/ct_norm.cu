@@ -2,43 +2,48 @@
 // norm, forward and backward.
 //
 // Both passes are bound by HBM: forward reads u and res and writes res_out and
-// y, backward reads dy, dres_out, u and res_out and writes du and dres, with a
-// few operations per element.  Each row needs two sums over its columns, the
-// second of which depends on the first, so what has to be avoided is memory
-// standing still while a row waits for them.  The design, common to both:
+// y, backward reads dy, dres_out, u and res_out and writes du and dres, with
+// some ten operations per element.  Each row needs two sums over its columns,
+// the second of which depends on the first, so what has to be avoided is
+// memory standing still while a row waits for them, and per-row work (sums
+// across warps, barriers, addresses) outweighing that on the columns.  The
+// design, common to both:
 //   - a cluster of blocks owns a contiguous run of rows, each of its blocks a
-//     fixed slice of the columns, each thread eight fixed columns: parameters
-//     stay in the thread's own shared memory, the backward pass's column sums
-//     in its registers;
+//     fixed slice of the columns, each thread 16 fixed columns: parameters stay
+//     in the thread's own shared memory, the backward pass's column sums in
+//     its registers;
 //   - rows arrive in a ring of shared-memory stages by bulk copies that one
 //     thread issues rows ahead, so loads are in flight during every barrier;
-//   - the first sum of row i+1 and the second sum of row i share one barrier.
-// Rows shorter than kMaxSlice columns take one block; longer ones a cluster of
-// 2, 4 or 8 that exchange partial sums through distributed shared memory.
-// Few rows, odd sizes and unaligned buffers take the same kernels with plain
-// loads in place of the ring.
+//   - the first sum of row i+1 and the second sum of row i are exchanged
+//     together, and the first sum of row i+2 is taken while they travel;
+//   - arithmetic on pairs of columns (f32x2).
+// Rows of up to kMaxSlice columns take one block; longer ones a cluster of 2,
+// 4 or 8 that exchange partial sums through distributed shared memory.  Rows
+// that are not whole 16-byte blocks take the same path, copied as the aligned
+// blocks that cover them; launches of few rows read global memory directly.
 #include "ct_device.cuh"
 #include "ct_ops.h"
 #include "ct_types.cuh"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace ct {
 namespace {
 
-constexpr int kMaxThreads = 768;      // 80 registers a thread
-constexpr int kMaxSlice = 8 * kMaxThreads;
+constexpr int kPer = 2;               // groups of eight columns per thread
+constexpr int kMaxThreads = 512;      // 128 registers a thread, 64 forward
+constexpr int kMaxSlice = 8 * kPer * kMaxThreads;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxStages = 4;
+constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxStages = 6;         // of either ring
 constexpr int kSmemPerSm = 227 * 1024;
-constexpr int kSmemFixed = 8 * 1024;  // static shared memory and the system's, per block
+constexpr int kSmemFixed = 3328;      // static shared memory and the system's, per block
 
 // How a launch divides the work.
 struct NormShape {
     int cluster;        // blocks per row
     int width;          // columns per block, a multiple of 8
-    int stages;         // of the ring; 0: plain loads
+    int lead, trail;    // stages of the rings; 0: plain loads, no rings
     int clusters;       // runs of rows
 };
 
@@ -54,10 +59,60 @@ __device__ __forceinline__ int64_t run_of(int64_t rows, int64_t r, int64_t runs)
     return ((r + 1) * runs - 1) / rows;
 }
 
-template <typename T>
-__device__ __forceinline__ float param(const void* p, int f32, int64_t i) {
-    return f32 ? static_cast<const float*>(p)[i] : dev::to_f32(static_cast<const T*>(p)[i]);
+// ---- eight columns as four pairs -------------------------------------------
+struct V8 {
+    uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
+__device__ __forceinline__ void halves(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ V8 pairs(const float (&f)[8]) {
+    return V8{{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+}
+__device__ __forceinline__ void floats(const V8& v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) halves(v.p[i], f[2 * i], f[2 * i + 1]);
+}
+
+// Columns past the row's end: a vector is read from column 0 instead, so that
+// no load is conditional; what it adds to a sum is dropped by on(), and it is
+// not stored.
+template <bool VEC>
+__device__ __forceinline__ bool on(const dev::Cols<VEC>& c) {
+    return !VEC || c.any();
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ V8 load_v8(const T* row, const dev::Cols<VEC>& c) {
+    float f[8];
+    if constexpr (VEC)
+        dev::unpack8(dev::load8(row + (c.any() ? c.first : 0)), f);
+    else
+        dev::load_cols<VEC>(row, c, f);
+    return pairs(f);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_v8(T* row, const dev::Cols<VEC>& c, const V8& v) {
+    float f[8];
+    floats(v, f);
+    dev::store_cols<VEC>(row, c, f);
+}
+
+// ---- parameters ------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void set_param(void* p, int f32, int64_t i, float v) {
     if (f32)
@@ -66,32 +121,13 @@ __device__ __forceinline__ void set_param(void* p, int f32, int64_t i, float v) 
         dev::from_f32(static_cast<T*>(p)[i], v);
 }
 
-// Eight fp32 values of a thread in shared memory that no other thread reads:
-// two planes of one float4 per thread, so that a warp's accesses are
-// consecutive.
-struct Own {
-    float4* base;
-    int threads;
-    __device__ __forceinline__ void put(int slot, const float (&f)[8]) const {
-        float4* p = base + 2 * slot * threads + threadIdx.x;
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[threads] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __device__ __forceinline__ void get(int slot, float (&f)[8]) const {
-        const float4* p = base + 2 * slot * threads + threadIdx.x;
-        const float4 a = p[0], b = p[threads];
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    }
-};
-
-// scale * (offset + w) of the thread's columns; scale without a weight.
+// offset + w of the thread's columns; 1 without a weight.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_param(const void* p, int f32, int64_t at, float offset,
-                                           float scale, const dev::Cols<VEC>& c, float (&f)[8]) {
+                                           const dev::Cols<VEC>& c, float (&f)[8]) {
     if (!p) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = scale;
+        for (int j = 0; j < 8; ++j) f[j] = 1.0f;
         return;
     }
     if (f32)
@@ -99,91 +135,190 @@ __device__ __forceinline__ void load_param(const void* p, int f32, int64_t at, f
     else
         dev::load_cols<VEC>(static_cast<const T*>(p) + at, c, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = scale * (offset + f[j]);
+    for (int j = 0; j < 8; ++j) f[j] += offset;
+}
+
+// alpha * gate * a(w_post): what the normed u is multiplied by.
+template <typename T, bool VEC, typename Args>
+__device__ __forceinline__ void branch_factor(const Args& a, int64_t gate_row, int col0,
+                                              const dev::Cols<VEC>& c, float (&f)[8]) {
+    float w[8];
+    load_param<T>(a.gate, a.param_f32, gate_row * a.hidden + col0, 0.0f, c, f);
+    load_param<T>(a.post ? a.w_post : nullptr, a.param_f32, col0, a.weight_offset, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= a.branch_scale * w[j];
+}
+
+// fp32 values of a thread's columns in shared memory that no other thread
+// reads: one float4 per thread and plane, so that a warp's accesses are
+// consecutive.
+struct Own {
+    float4* base;
+    __device__ __forceinline__ float4* at(int slot, int p) const {
+        return base + (slot * kPer + p) * 2 * blockDim.x + threadIdx.x;
+    }
+    __device__ __forceinline__ void put(int slot, int p, const float (&f)[8]) const {
+        float4* q = at(slot, p);
+        q[0] = make_float4(f[0], f[1], f[2], f[3]);
+        q[blockDim.x] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ V8 get(int slot, int p) const {
+        const ulonglong2* q = reinterpret_cast<const ulonglong2*>(at(slot, p));
+        const ulonglong2 a = q[0], b = q[blockDim.x];
+        return V8{{a.x, a.y, b.x, b.y}};
+    }
+};
+enum { kBranch, kPre, kOwnSlots };    // alpha gate a(w_post), a(w_pre)
+constexpr int kOwnBytes = 32 * kPer * kOwnSlots;   // per thread
+
+// dev::mbar_wait_bounded for a barrier that other blocks of the cluster complete.
+__device__ __forceinline__ bool cluster_wait_bounded(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = dev::globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(dev::smem_u32(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        if ((i & 63u) == 0 && dev::globaltimer_ns() - t0 > dev::kWaitLimitNs) return false;
+    }
 }
 
 // Sums of a and b over the cluster's blocks, the same in every thread, in a
-// fixed order; one barrier.  `slots` [2][kMaxCluster * warps]: a call writes
-// the half that the call before it did not, which everyone has finished with
-// once this call's barrier is passed.
+// fixed order, in two steps so that work can go on between them: send() leaves
+// the warps' sums in every block, get() waits for all of them and adds them
+// up.  Lanes 0..15 work on a, lanes 16..31 on b.  Two sets of slots and
+// barriers take turns: whoever sends the second time after a get() knows that
+// everyone has finished that get().
 struct RowSums {
-    float2 (*slots)[kMaxCluster * kMaxThreads / 32];
-    int cluster, rank, turn;
+    float (*slots)[2][kMaxCluster * kMaxWarps];
+    uint64_t* bars;
+    int cluster, rank;
+    int turn = 0;
+    uint32_t parity = 0;
 
-    __device__ __forceinline__ float2 operator()(float a, float b) {
+    // The arrivals of a turn: one per warp, or thread 0's with the bytes that
+    // the cluster's warps send.
+    __device__ __forceinline__ void init() const {
+        for (int i = 0; i < 2; ++i) dev::mbar_init(bars + i, cluster == 1 ? blockDim.x >> 5 : 1);
+    }
+    static __device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        return v;
+    }
+    __device__ __forceinline__ void send(float a, float b) {
         const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        a = dev::warp_sum(a);
-        b = dev::warp_sum(b);
-        float2* half = slots[turn];
-        turn ^= 1;
+        const bool upper = lane >= 16;
+        float v = upper ? b : a;
+        v = half_sum(v + __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16));
+        float* slot = slots[turn][upper] + rank * warps + warp;
         if (cluster == 1) {
-            if (lane == 0) half[warp] = make_float2(a, b);
-            __syncthreads();
+            if ((lane & 15) == 0) *slot = v;
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(bars + turn);
         } else {
-            if (lane < cluster) {
-                uint32_t remote;
+            if (threadIdx.x == 0) dev::mbar_arrive_expect_tx(bars + turn, cluster * warps * 8);
+            if ((lane & 15) < cluster) {
+                uint32_t to, bar;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                             : "=r"(remote)
-                             : "r"(dev::smem_u32(half + rank * warps + warp)), "r"(lane));
-                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(a), "f"(b)
-                             : "memory");
+                             : "=r"(to) : "r"(dev::smem_u32(slot)), "r"(lane & 15));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                             : "=r"(bar) : "r"(dev::smem_u32(bars + turn)), "r"(lane & 15));
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+                             ::"r"(to), "r"(__float_as_uint(v)), "r"(bar) : "memory");
             }
-            cluster_barrier();
         }
-        a = b = 0.0f;
-        for (int i = lane; i < cluster * warps; i += 32) {
-            a += half[i].x;
-            b += half[i].y;
-        }
-        return make_float2(dev::warp_sum(a), dev::warp_sum(b));
+    }
+    // `lost`: a wait gave up, here or earlier; then nothing is waited for.
+    __device__ __forceinline__ float2 get(bool& lost) {
+        const int n = cluster * (blockDim.x >> 5), lane = threadIdx.x & 31;
+        if (!lost)
+            lost = !(cluster == 1 ? dev::mbar_wait_bounded(bars + turn, parity)
+                                  : cluster_wait_bounded(bars + turn, parity));
+        const float* half = slots[turn][lane >= 16];
+        parity ^= turn;
+        turn ^= 1;
+        float v = 0.0f;
+        for (int i = lane & 15; i < n; i += 16) v += half[i];
+        v = half_sum(v);
+        return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
     }
 
-    // Every block of the cluster has begun and set up its shared memory.
-    static __device__ __forceinline__ void start(int cluster) {
+    // Every block of the cluster has begun and set up its shared memory, or is
+    // done with the others'.
+    __device__ __forceinline__ void meet() const {
         if (cluster == 1)
             __syncthreads();
         else
-            cluster_barrier();
-    }
-    static __device__ __forceinline__ void cluster_barrier() {
-        asm volatile("barrier.cluster.arrive.release;\n\t"
-                     "barrier.cluster.wait.acquire;" ::: "memory");
+            asm volatile("barrier.cluster.arrive.release;\n\t"
+                         "barrier.cluster.wait.acquire;" ::: "memory");
     }
 };
+__device__ __forceinline__ float lanes_sum(uint64_t v) {
+    float lo, hi;
+    halves(v, lo, hi);
+    return lo + hi;
+}
 
-// The ring: stage s holds one row's slices of up to four tensors, one after
-// the other.  Thread 0 issues the copies; everyone waits on full[s].
+// ---- rows ------------------------------------------------------------------
+// A ring of stages that hold one row's slices of one or two tensors, one after
+// the other.  Thread 0 issues the copies; everyone waits on the stage's
+// barrier.  Without VEC a slice is copied as the aligned 16-byte blocks that
+// cover it, and lies (address mod 16) bytes into its place.
+//
+// A launch has two: the leading ring for what a row's first sum needs, which
+// is taken two rows ahead, and the trailing ring for the rest; the leading one
+// is longer by about that much.
 struct Ring {
     uint64_t* full;
     uint8_t* base;
     uint32_t stage_bytes;
     int stages;
-    bool lost;          // a wait gave up: no more waiting, the error is reported
-
-    __device__ __forceinline__ uint8_t* at(int stage) const { return base + stage * stage_bytes; }
-    __device__ __forceinline__ void wait(int stage, uint32_t parity) {
-        if (!lost && !dev::mbar_wait_bounded(full + stage, parity)) lost = true;
-    }
-    __device__ __forceinline__ void copy(int stage, uint32_t offset, const void* src,
-                                         uint32_t bytes) const {
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-            ::"r"(dev::smem_u32(at(stage)) + offset), "l"(src), "r"(bytes),
-            "r"(dev::smem_u32(full + stage)) : "memory");
-    }
-};
-
-// A position in the ring.
-struct Turn {
     int stage = 0;
     uint32_t parity = 0;
-    __device__ __forceinline__ void next(int stages) {
+
+    __device__ __forceinline__ void next() {
         if (++stage == stages) {
             stage = 0;
             parity ^= 1;
         }
     }
+    __device__ __forceinline__ void init() const {
+        for (int i = 0; i < stages; ++i) dev::mbar_init(full + i, 1);
+    }
+    // `lost`: a wait gave up, here or earlier; then nothing is waited for.
+    __device__ __forceinline__ void wait(bool& lost) const {
+        if (!lost) lost = !dev::mbar_wait_bounded(full + stage, parity);
+    }
+    __device__ __forceinline__ const uint8_t* at() const { return base + stage * stage_bytes; }
+    static __device__ __forceinline__ uint32_t blocks_bytes(const void* src, uint32_t bytes) {
+        return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 15) + bytes + 15) & ~15u;
+    }
+    __device__ __forceinline__ void copy(int to, uint32_t offset, const void* src, uint32_t bytes) const {
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+            ::"r"(dev::smem_u32(base) + to * stage_bytes + offset),
+            "l"(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15)), "r"(blocks_bytes(src, bytes)),
+            "r"(dev::smem_u32(full + to)) : "memory");
+    }
+    // Stage `to` becomes the slices at p and q (either may be null).
+    __device__ __forceinline__ void fetch(int to, const void* p, uint32_t p_bytes, uint32_t q_place,
+                                          const void* q, uint32_t q_bytes) const {
+        dev::mbar_arrive_expect_tx(full + to, (p ? blocks_bytes(p, p_bytes) : 0) +
+                                                  (q ? blocks_bytes(q, q_bytes) : 0));
+        if (p) copy(to, 0, p, p_bytes);
+        if (q) copy(to, q_place, q, q_bytes);
+    }
 };
+
+// Bytes of a tensor's place in a stage.
+template <bool VEC, typename T>
+__host__ __device__ constexpr uint32_t place_bytes(int width) {
+    return width * sizeof(T) + (VEC ? 0 : 32);
+}
 
 // Eight FP8 codes of y * scale.
 template <bool VEC>
@@ -207,137 +342,196 @@ __device__ __forceinline__ void store_fp8(uint8_t* row, const dev::Cols<VEC>& c,
 }
 
 
+// Without VEC the 16-byte blocks that cover a row's slice may begin or end up
+// to 15 bytes outside it: rows that near to the tensors' ends are read from
+// global memory instead.
+template <bool VEC>
+__device__ __forceinline__ bool in_ring(int64_t row, int64_t rows, int H) {
+    return VEC || (row * H >= 8 && (rows - 1 - row) * H >= 8);   // of two bytes at least
+}
+
+// Where a row's slice is read from: its place in a stage, or itself.
+template <bool RING, bool VEC, typename T>
+__device__ __forceinline__ const T* row_at(const uint8_t* stage, uint32_t offset, const T* global, bool staged) {
+    if (!RING || (!VEC && !staged)) return global;
+    stage += offset;
+    if (!VEC) stage += reinterpret_cast<uintptr_t>(global) & 15;
+    return reinterpret_cast<const T*>(stage);
+}
+
+// FULL: u, both norms and (backward) dres_out are there, known to the compiler.
+
 // Forward.  Per row: sum u^2 -> rstd_post; res_out and sum res_out^2 ->
 // rstd_pre; y.
-template <typename T, typename R, bool VEC, bool RING>
-__global__ void __launch_bounds__(kMaxThreads, 1) block_norm_kernel(const NormArgs a,
+template <typename T, typename R, bool VEC, bool RING, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads, 2) block_norm_kernel(const NormArgs a,
                                                                     const NormShape s) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 slots[2][kMaxCluster * kMaxThreads / 32];
-    __shared__ __align__(8) uint64_t full[kMaxStages];
+    __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
+    __shared__ __align__(8) uint64_t full[2 * kMaxStages + 2];
     __shared__ unsigned block_max;
+    const bool has_u = FULL || a.u, post = FULL || a.post, pre = FULL || a.pre;
     const int tid = threadIdx.x, H = a.hidden;
     const int rank = blockIdx.x % s.cluster, run = blockIdx.x / s.cluster;
     const int col0 = rank * s.width, W = min(s.width, H - col0);
-    const dev::Cols<VEC> c(tid, blockDim.x, W);
+    auto cols = [&](int p) { return dev::Cols<VEC>(p * blockDim.x + tid, blockDim.x, W); };
     const int64_t begin = run_begin(a.rows, run, s.clusters), end = run_begin(a.rows, run + 1, s.clusters);
     const T* u = static_cast<const T*>(a.u) + col0;
     const R* res = static_cast<const R*>(a.res) + col0;
-    const uint32_t u_at = s.width * sizeof(R);   // in a stage: res, then u
-    Ring ring{full, smem, static_cast<uint32_t>(s.width * (sizeof(R) + sizeof(T))), s.stages, false};
-    const Own own{reinterpret_cast<float4*>(smem + (RING ? s.stages * ring.stage_bytes : 0)),
-                  static_cast<int>(blockDim.x)};
-    enum { kPost, kPre, kGate };
-    RowSums sums{slots, s.cluster, rank, 0};
+    Ring lead{full, smem, place_bytes<VEC, T>(s.width), s.lead};                  // u
+    Ring trail{full + kMaxStages, smem + lead.stages * lead.stage_bytes,
+               place_bytes<VEC, R>(s.width), s.trail};                                  // res
+    bool lost = false;       // a wait gave up: no more waiting, the error is reported
+    const Own own{reinterpret_cast<float4*>(RING ? trail.base + trail.stages * trail.stage_bytes : smem)};
+    RowSums sums{slots, full + 2 * kMaxStages, s.cluster, rank};
 
     dev::pdl_launch_dependents();
     if (tid == 0) {
         block_max = 0;
+        sums.init();
         if constexpr (RING) {
-            for (int i = 0; i < s.stages; ++i) dev::mbar_init(full + i, 1);
-            dev::fence_barrier_init();
+            lead.init();
+            trail.init();
         }
+        dev::fence_barrier_init();
     }
-    RowSums::start(s.cluster);
+    sums.meet();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    auto fetch = [&](int64_t row, int stage) {
-        dev::mbar_arrive_expect_tx(full + stage, W * (sizeof(R) + (a.u ? sizeof(T) : 0)));
-        ring.copy(stage, 0, res + row * H, W * sizeof(R));
-        if (a.u) ring.copy(stage, u_at, u + row * H, W * sizeof(T));
+    auto fetch_lead = [&](int64_t row, int to) {
+        const bool staged = has_u && in_ring<VEC>(row, a.rows, H);
+        lead.fetch(to, staged ? u + row * H : nullptr, W * sizeof(T), 0, nullptr, 0);
+    };
+    auto fetch_trail = [&](int64_t row, int to) {
+        trail.fetch(to, in_ring<VEC>(row, a.rows, H) ? res + row * H : nullptr, W * sizeof(R), 0, nullptr, 0);
     };
     if constexpr (RING)
         if (tid == 0)
-            for (int i = 0; i < s.stages && begin + i < end; ++i) fetch(begin + i, i);
-    const float alpha = a.branch_scale, beta = a.residual_scale;
+            for (int i = 0; i < lead.stages && begin + i < end; ++i) {   // the longer one
+                fetch_lead(begin + i, i);
+                if (i < trail.stages) fetch_trail(begin + i, i);
+            }
     int64_t gate_row = a.gate ? begin / a.rows_per_gate : 0;
     int64_t gate_end = a.gate ? (gate_row + 1) * a.rows_per_gate : a.rows;
-    {
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
         float f[8];
-        if (a.u) {
-            load_param<T>(a.post ? a.w_post : nullptr, a.param_f32, col0,
-                          a.post ? a.weight_offset : 0.0f, 1.0f, c, f);
-            own.put(kPost, f);
-            load_param<T>(a.gate, a.param_f32, gate_row * H + col0, 0.0f, alpha, c, f);
-            own.put(kGate, f);
+        if (has_u) {
+            branch_factor<T>(a, gate_row, col0, cols(p), f);
+            own.put(kBranch, p, f);
         }
-        if (a.pre) {
-            load_param<T>(a.w_pre, a.param_f32, col0, a.weight_offset, 1.0f, c, f);
-            own.put(kPre, f);
+        if (pre) {
+            load_param<T>(a.w_pre, a.param_f32, col0, a.weight_offset, cols(p), f);
+            own.put(kPre, p, f);
         }
     }
     const float scale = a.scale ? *a.scale : 0.0f;
     const float per_column = 1.0f / H;
+    const uint64_t beta = pair(a.residual_scale, a.residual_scale);
     unsigned most = 0;
 
-    auto sum_u = [&](int64_t row, int stage) {
-        float f[8], sum = 0.0f;
-        dev::load_cols<VEC>(RING ? reinterpret_cast<const T*>(ring.at(stage) + u_at) : u + row * H, c, f);
+    // sum u^2 of the next row of the leading ring
+    auto sum_u = [&](int64_t row) {
+        if (RING) lead.wait(lost);
+        if (!post) {
+            if (RING) lead.next();
+            return 0.0f;
+        }
+        const T* x = row_at<RING, VEC>(lead.at(), 0, u + row * H, in_ring<VEC>(row, a.rows, H));
+        if (RING) lead.next();
+        float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+        for (int p = 0; p < kPer; ++p) {
+            const V8 v = load_v8<VEC>(x, cols(p));
+            uint64_t part = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part = fma2(v.p[j], v.p[j], part);
+            sum += on(cols(p)) ? lanes_sum(part) : 0.0f;
+        }
         return sum;
     };
-    Turn now, ahead;
-    if (RING) ring.wait(now.stage, now.parity);
+    const bool writes_rstd = rank == 0 && tid == 0;
     float rstd_u = 1.0f;
-    if (a.post) {
-        rstd_u = rsqrtf(sums(sum_u(begin, 0), 0.0f).x * per_column + a.eps);
-        if (a.rstd_post && rank == 0 && tid == 0) a.rstd_post[begin] = rstd_u;
+    const float first_sum = sum_u(begin);
+    if (post) {
+        sums.send(first_sum, 0.0f);
+        rstd_u = rsqrtf(sums.get(lost).x * per_column + a.eps);
+        if (a.rstd_post && writes_rstd) a.rstd_post[begin] = rstd_u;
     }
+    float next_u = begin + 1 < end ? sum_u(begin + 1) : 0.0f;
+    int u_stage = 0;        // the stage of this row's u: the leading ring itself is rows ahead
     for (int64_t row = begin; row < end; ++row) {
-        float v[8], sum_v = 0.0f, next_u = 0.0f;
-        dev::load_cols<VEC>(RING ? reinterpret_cast<const R*>(ring.at(now.stage)) : res + row * H, c, v);
-        if (a.u) {
-            if (row == gate_end) {
-                gate_end += a.rows_per_gate;
+        const int64_t at = row * H;
+        const bool staged = in_ring<VEC>(row, a.rows, H);
+        if (has_u && row == gate_end) {
+            gate_end += a.rows_per_gate;
+            ++gate_row;
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) {
                 float f[8];
-                load_param<T>(a.gate, a.param_f32, ++gate_row * H + col0, 0.0f, alpha, c, f);
-                own.put(kGate, f);
+                branch_factor<T>(a, gate_row, col0, cols(p), f);
+                own.put(kBranch, p, f);
             }
-            float x[8], w[8], g[8];
-            dev::load_cols<VEC>(RING ? reinterpret_cast<const T*>(ring.at(now.stage) + u_at) : u + row * H,
-                                c, x);
-            own.get(kPost, w);
-            own.get(kGate, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = beta * v[j] + g[j] * (x[j] * rstd_u * w[j]);
-            dev::store_cols<VEC>(static_cast<R*>(a.res_out) + row * H + col0, c, v);
         }
+        V8 v[kPer];
+        float sum_v = 0.0f;
+        if (RING) trail.wait(lost);
+        const R* r = row_at<RING, VEC>(trail.at(), 0, res + at, staged);
+        const T* x = row_at<RING, VEC>(lead.base + u_stage * lead.stage_bytes, 0, u + at, staged);
+        const uint64_t rstd2 = pair(rstd_u, rstd_u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c.has(j)) sum_v = fmaf(v[j], v[j], sum_v);
-        ahead = now;
-        ahead.next(s.stages);
-        if (row + 1 < end) {
-            if (RING) ring.wait(ahead.stage, ahead.parity);
-            if (a.post) next_u = sum_u(row + 1, ahead.stage);
+        for (int p = 0; p < kPer; ++p) {
+            v[p] = load_v8<VEC>(r, cols(p));
+            if (has_u) {
+                const V8 xv = load_v8<VEC>(x, cols(p)), g = own.get(kBranch, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[p].p[j] = fma2(mul2(xv.p[j], rstd2), g.p[j], mul2(beta, v[p].p[j]));
+                store_v8<VEC>(static_cast<R*>(a.res_out) + at + col0, cols(p), v[p]);
+            }
+            uint64_t part = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part = fma2(v[p].p[j], v[p].p[j], part);
+            sum_v += on(cols(p)) ? lanes_sum(part) : 0.0f;
         }
-        const float2 sum = sums(next_u, sum_v);
-        // everyone has read this row's stage
-        if constexpr (RING)
-            if (tid == 0 && row + s.stages < end) fetch(row + s.stages, now.stage);
-        now = ahead;
-        if (a.post) {
+        sums.send(next_u, sum_v);
+        if (row + 2 < end) next_u = sum_u(row + 2);
+        const float2 sum = sums.get(lost);
+        // everyone has read this row's stages
+        if constexpr (RING) {
+            if (tid == 0) {
+                if (row + lead.stages < end) fetch_lead(row + lead.stages, u_stage);
+                if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
+            }
+            trail.next();
+            if (++u_stage == lead.stages) u_stage = 0;
+        }
+        if (post) {
             rstd_u = rsqrtf(sum.x * per_column + a.eps);
-            if (a.rstd_post && rank == 0 && tid == 0 && row + 1 < end) a.rstd_post[row + 1] = rstd_u;
+            if (a.rstd_post && writes_rstd && row + 1 < end) a.rstd_post[row + 1] = rstd_u;
         }
-        if (!a.pre) continue;
+        if (!pre) continue;
         const float rstd = rsqrtf(sum.y * per_column + a.eps);
-        if (a.rstd_pre && rank == 0 && tid == 0) a.rstd_pre[row] = rstd;
-        float w[8];
-        own.get(kPre, w);
+        if (a.rstd_pre && writes_rstd) a.rstd_pre[row] = rstd;
+        const uint64_t rstd_v = pair(rstd, rstd);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= rstd * w[j];
-        if (a.scale) {
+        for (int p = 0; p < kPer; ++p) {
+            const V8 w = own.get(kPre, p);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c.has(j)) most = max(most, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-            store_fp8<VEC>(static_cast<uint8_t*>(a.y) + row * H + col0, c, v, scale, a.fmt);
-        } else {
-            dev::store_cols<VEC>(static_cast<T*>(a.y) + row * H + col0, c, v);
+            for (int j = 0; j < 4; ++j) v[p].p[j] = mul2(mul2(v[p].p[j], rstd_v), w.p[j]);
+            if (a.scale) {
+                float f[8];
+                floats(v[p], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (on(cols(p))) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+                store_fp8<VEC>(static_cast<uint8_t*>(a.y) + at + col0, cols(p), f, scale, a.fmt);
+            } else {
+                store_v8<VEC>(static_cast<T*>(a.y) + at + col0, cols(p), v[p]);
+            }
         }
     }
-    if (a.scale && a.pre) {
+    if (a.scale && pre) {
         most = __reduce_max_sync(0xFFFFFFFFu, most);
         if ((tid & 31) == 0) atomicMax(&block_max, most);
         __syncthreads();
@@ -346,9 +540,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_kernel(const NormAr
             if (blockIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, scale);
         }
     }
-    if (RING && ring.lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
     // a block's shared memory stays until its peers have sent their last sums
-    if (s.cluster > 1) RowSums::cluster_barrier();
+    if (s.cluster > 1) sums.meet();
 }
 
 // What the workspace holds for the backward pass, [clusters][H] each: partial
@@ -358,196 +552,252 @@ enum { kSumPre, kSumPost, kSumGateFirst, kSumGateLast, kSums };
 
 // Backward.  With xh = res_out rstd_pre, G = dy a_pre, uh = u rstd_post:
 //   D  = dres_out + rstd_pre (G - xh mean(G xh))      dres = beta D
-//   P  = alpha gate D a_post                           du = rstd_post (P - uh mean(P uh))
-//   dw_pre = sum dy xh,  dw_post = sum alpha gate D uh,  dgate = sum alpha D uh a_post
-template <typename T, typename R, bool VEC, bool RING>
+//   P  = alpha gate a_post D                           du = rstd_post (P - uh mean(P uh))
+//   dw_pre = sum dy xh
+//   S  = sum D uh over a gate row's rows: dgate = alpha a_post S, dw_post = sum alpha gate S
+template <typename T, typename R, bool VEC, bool RING, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     block_norm_backward_kernel(const NormBackwardArgs a, const NormShape s) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 slots[2][kMaxCluster * kMaxThreads / 32];
-    __shared__ __align__(8) uint64_t full[kMaxStages];
+    __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
+    __shared__ __align__(8) uint64_t full[2 * kMaxStages + 2];
+    const bool has_u = FULL || a.u, post = FULL || a.post, pre = FULL || a.pre;
+    const bool has_dres = FULL || a.dres_out;
     const int tid = threadIdx.x, H = a.hidden;
     const int rank = blockIdx.x % s.cluster, run = blockIdx.x / s.cluster;
     const int col0 = rank * s.width, W = min(s.width, H - col0);
-    const dev::Cols<VEC> c(tid, blockDim.x, W);
+    auto cols = [&](int p) { return dev::Cols<VEC>(p * blockDim.x + tid, blockDim.x, W); };
     const int64_t begin = run_begin(a.rows, run, s.clusters), end = run_begin(a.rows, run + 1, s.clusters);
-    // in a stage: res_out, dres_out, dy, u
-    const uint32_t dres_at = s.width * sizeof(R), dy_at = 2 * dres_at, u_at = dy_at + s.width * sizeof(T);
-    Ring ring{full, smem, static_cast<uint32_t>(2 * s.width * (sizeof(R) + sizeof(T))), s.stages, false};
-    const Own own{reinterpret_cast<float4*>(smem + (RING ? s.stages * ring.stage_bytes : 0)),
-                  static_cast<int>(blockDim.x)};
-    enum { kPost, kPre, kGate };
-    RowSums sums{slots, s.cluster, rank, 0};
+    constexpr uint32_t kT = sizeof(T), kR = sizeof(R);
+    const uint32_t second = place_bytes<VEC, R>(s.width);    // in a stage: of type R, then of type T
+    const uint32_t stage_bytes = second + place_bytes<VEC, T>(s.width);
+    Ring lead{full, smem, stage_bytes, s.lead};        // res_out, dy
+    Ring trail{full + kMaxStages, smem + lead.stages * stage_bytes, stage_bytes, s.trail};   // dres_out, u
+    bool lost = false;
+    const Own own{reinterpret_cast<float4*>(RING ? trail.base + trail.stages * stage_bytes : smem)};
+    RowSums sums{slots, full + 2 * kMaxStages, s.cluster, rank};
     const R* res_out = static_cast<const R*>(a.res_out) + col0;
     const R* dres_out = static_cast<const R*>(a.dres_out) + col0;
     const T* dy = static_cast<const T*>(a.dy) + col0;
     const T* u = static_cast<const T*>(a.u) + col0;
 
     dev::pdl_launch_dependents();
-    if constexpr (RING) {
-        if (tid == 0) {
-            for (int i = 0; i < s.stages; ++i) dev::mbar_init(full + i, 1);
-            dev::fence_barrier_init();
+    if (tid == 0) {
+        sums.init();
+        if constexpr (RING) {
+            lead.init();
+            trail.init();
         }
+        dev::fence_barrier_init();
     }
-    RowSums::start(s.cluster);
+    sums.meet();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    auto fetch = [&](int64_t row, int stage) {
-        const uint32_t rb = W * sizeof(R), tb = W * sizeof(T);
-        const int64_t at = row * H;
-        dev::mbar_arrive_expect_tx(full + stage, (a.pre ? rb + tb : 0) + (a.dres_out ? rb : 0) + (a.u ? tb : 0));
-        if (a.pre) {
-            ring.copy(stage, 0, res_out + at, rb);
-            ring.copy(stage, dy_at, dy + at, tb);
-        }
-        if (a.dres_out) ring.copy(stage, dres_at, dres_out + at, rb);
-        if (a.u) ring.copy(stage, u_at, u + at, tb);
+    auto fetch_lead = [&](int64_t row, int to) {
+        const bool staged = pre && in_ring<VEC>(row, a.rows, H);
+        lead.fetch(to, staged ? res_out + row * H : nullptr, W * kR, second, staged ? dy + row * H : nullptr, W * kT);
+    };
+    auto fetch_trail = [&](int64_t row, int to) {
+        const bool staged = in_ring<VEC>(row, a.rows, H);
+        trail.fetch(to, staged && has_dres ? dres_out + row * H : nullptr, W * kR, second,
+                    staged && has_u ? u + row * H : nullptr, W * kT);
     };
     if constexpr (RING)
         if (tid == 0)
-            for (int i = 0; i < s.stages && begin + i < end; ++i) fetch(begin + i, i);
-    const float alpha = a.branch_scale, beta = a.u ? a.residual_scale : 1.0f;
+            for (int i = 0; i < lead.stages && begin + i < end; ++i) {   // the longer one
+                fetch_lead(begin + i, i);
+                if (i < trail.stages) fetch_trail(begin + i, i);
+            }
+    const float beta1 = has_u ? a.residual_scale : 1.0f;
+    const uint64_t beta = pair(beta1, beta1);
     const int64_t first_gate = a.gate ? begin / a.rows_per_gate : 0;
     int64_t gate_row = first_gate;
     int64_t gate_end = a.gate ? (gate_row + 1) * a.rows_per_gate : a.rows;
-    {
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
         float f[8];
-        if (a.u) {
-            load_param<T>(a.post ? a.w_post : nullptr, a.param_f32, col0,
-                          a.post ? a.weight_offset : 0.0f, 1.0f, c, f);
-            own.put(kPost, f);
-            load_param<T>(a.gate, a.param_f32, gate_row * H + col0, 0.0f, alpha, c, f);
-            own.put(kGate, f);
+        if (has_u) {
+            branch_factor<T>(a, gate_row, col0, cols(p), f);
+            own.put(kBranch, p, f);
         }
-        if (a.pre) {
-            load_param<T>(a.w_pre, a.param_f32, col0, a.weight_offset, 1.0f, c, f);
-            own.put(kPre, f);
+        if (pre) {
+            load_param<T>(a.w_pre, a.param_f32, col0, a.weight_offset, cols(p), f);
+            own.put(kPre, p, f);
         }
     }
     const float per_column = 1.0f / H;
-    float dw_pre[8] = {}, dw_post[8] = {}, dgate[8] = {};
+    V8 dw_pre[kPer] = {}, dots[kPer] = {};   // sums of dy xh, and S
 
-    // sum of G xh over the row, and the row's part of dw_pre
-    auto first_sum = [&](int64_t row, int stage, float rstd) {
-        float g[8], x[8], w[8], sum = 0.0f;
-        dev::load_cols<VEC>(RING ? reinterpret_cast<const T*>(ring.at(stage) + dy_at) : dy + row * H, c, g);
-        dev::load_cols<VEC>(RING ? reinterpret_cast<const R*>(ring.at(stage)) : res_out + row * H, c, x);
-        own.get(kPre, w);
+    // sum of G xh over the next row of the leading ring, and its part of dw_pre
+    auto first_sum = [&](int64_t row, float rstd) {
+        if (RING) lead.wait(lost);
+        const uint8_t* stage = lead.at();
+        if (RING) lead.next();
+        if (!pre) return 0.0f;
+        const bool staged = in_ring<VEC>(row, a.rows, H);
+        const T* g = row_at<RING, VEC>(stage, second, dy + row * H, staged);
+        const R* x = row_at<RING, VEC>(stage, 0, res_out + row * H, staged);
+        const uint64_t rstd2 = pair(rstd, rstd);
+        float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float t = g[j] * (x[j] * rstd);
-            dw_pre[j] += t;
-            sum = fmaf(t, w[j], sum);
+        for (int p = 0; p < kPer; ++p) {
+            uint64_t part = 0;
+            const V8 gv = load_v8<VEC>(g, cols(p)), xv = load_v8<VEC>(x, cols(p)), w = own.get(kPre, p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t t = mul2(gv.p[j], xv.p[j]);
+                dw_pre[p].p[j] = fma2(t, rstd2, dw_pre[p].p[j]);
+                part = fma2(t, w.p[j], part);
+            }
+            sum += on(cols(p)) ? lanes_sum(part) : 0.0f;
         }
-        return sum;
+        return sum * rstd;
     };
-    // the gate row's sums: whole ones go to dgate, others to the workspace
-    auto flush_gate = [&](bool to_the_end) {
-        if (a.dgate) {
-            const bool whole = gate_row * a.rows_per_gate >= begin && (to_the_end ? min(gate_end, a.rows) <= end : true);
-            float* part = a.workspace + (int64_t(gate_row == first_gate ? kSumGateFirst : kSumGateLast) * s.clusters + run) * H + col0;
+    // Ends a gate row: its part of dw_post joins the run's, which this thread
+    // alone touches in the workspace; dgate goes out where all its rows are
+    // this run's, else to the workspace.
+    auto end_gate = [&] {
+        const bool whole = gate_row * a.rows_per_gate >= begin && min(gate_end, a.rows) <= end;
+        float* post_sums = a.workspace + (int64_t(kSumPost) * s.clusters + run) * H + col0;
+        float* gate_sums = a.workspace +
+            (int64_t(gate_row == first_gate ? kSumGateFirst : kSumGateLast) * s.clusters + run) * H + col0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (!c.has(j)) continue;
-                const float v = alpha * dgate[j];
-                if (whole)
-                    set_param<T>(a.dgate, a.param_f32, gate_row * H + col0 + c.at(j), v);
+        for (int p = 0; p < kPer; ++p) {
+            const dev::Cols<VEC> c = cols(p);
+            float f[8], w[8];
+            floats(dots[p], f);
+            dots[p] = V8{};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= a.branch_scale;
+            if (a.dw_post) {
+                float sum[8] = {};
+                if (gate_row != first_gate) dev::load_cols<VEC>(post_sums, c, sum);
+                load_param<T>(a.gate, a.param_f32, gate_row * H + col0, 0.0f, c, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] = fmaf(w[j], f[j], sum[j]);
+                dev::store_cols<VEC>(post_sums, c, sum);
+            }
+            if (a.dgate) {
+                load_param<T>(post ? a.w_post : nullptr, a.param_f32, col0, a.weight_offset, c, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] *= w[j];
+                const int64_t at = gate_row * H + col0;
+                if (!whole)
+                    dev::store_cols<VEC>(gate_sums, c, f);
+                else if (a.param_f32)
+                    dev::store_cols<VEC>(static_cast<float*>(a.dgate) + at, c, f);
                 else
-                    part[c.at(j)] = v;
+                    dev::store_cols<VEC>(static_cast<T*>(a.dgate) + at, c, f);
             }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dgate[j] = 0.0f;
     };
 
-    Turn now, ahead;
-    float rstd_x = a.pre ? a.rstd_pre[begin] : 0.0f, rstd_u = a.post ? a.rstd_post[begin] : 1.0f;
-    if (RING) ring.wait(now.stage, now.parity);
+    // rstd of this row and the next two
+    auto rstd_at = [&](bool norm, const float* rstd, int64_t row, float none) {
+        return norm && row < end ? rstd[row] : none;
+    };
+    float rstd_x = rstd_at(pre, a.rstd_pre, begin, 0.0f), rstd_u = rstd_at(post, a.rstd_post, begin, 1.0f);
+    float next_x = rstd_at(pre, a.rstd_pre, begin + 1, 0.0f);
     float mean_x = 0.0f;
-    if (a.pre) mean_x = sums(first_sum(begin, 0, rstd_x), 0.0f).x * per_column;
+    {
+        const float sum = first_sum(begin, rstd_x);
+        if (pre) {
+            sums.send(sum, 0.0f);
+            mean_x = sums.get(lost).x * per_column;
+        }
+    }
+    float sum_x = begin + 1 < end ? first_sum(begin + 1, next_x) : 0.0f;
+    int x_stage = 0;        // the stage of this row's res_out: the leading ring itself is rows ahead
     for (int64_t row = begin; row < end; ++row) {
-        const bool more = row + 1 < end;
-        const float next_x = a.pre && more ? a.rstd_pre[row + 1] : 0.0f;
-        const float next_u = a.post && more ? a.rstd_post[row + 1] : 1.0f;
-        float d[8], p[8], hat[8], sum_p = 0.0f, sum_x = 0.0f;
-        if (a.dres_out) {
-            dev::load_cols<VEC>(RING ? reinterpret_cast<const R*>(ring.at(now.stage) + dres_at)
-                                     : dres_out + row * H, c, d);
-        } else {
+        const int64_t at = row * H;
+        const bool staged = in_ring<VEC>(row, a.rows, H);
+        const float far_x = rstd_at(pre, a.rstd_pre, row + 2, 0.0f);
+        const float next_u = rstd_at(post, a.rstd_post, row + 1, 1.0f);
+        if (has_u && row == gate_end) {
+            end_gate();
+            gate_end += a.rows_per_gate;
+            ++gate_row;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = 0.0f;
-        }
-        if (a.pre) {
-            float g[8], x[8], w[8];
-            dev::load_cols<VEC>(RING ? reinterpret_cast<const T*>(ring.at(now.stage) + dy_at) : dy + row * H,
-                                c, g);
-            dev::load_cols<VEC>(RING ? reinterpret_cast<const R*>(ring.at(now.stage)) : res_out + row * H, c, x);
-            own.get(kPre, w);
-            const float back = rstd_x * rstd_x * mean_x;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] += rstd_x * (g[j] * w[j]) - x[j] * back;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = beta * d[j];
-        dev::store_cols<VEC>(static_cast<R*>(a.dres) + row * H + col0, c, p);
-        if (a.u) {
-            if (row == gate_end) {
-                flush_gate(false);
-                gate_end += a.rows_per_gate;
+            for (int p = 0; p < kPer; ++p) {
                 float f[8];
-                load_param<T>(a.gate, a.param_f32, ++gate_row * H + col0, 0.0f, alpha, c, f);
-                own.put(kGate, f);
-            }
-            float w[8];
-            dev::load_cols<VEC>(RING ? reinterpret_cast<const T*>(ring.at(now.stage) + u_at) : u + row * H,
-                                c, hat);
-            own.get(kPost, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                hat[j] *= rstd_u;
-                dgate[j] = fmaf(d[j] * hat[j], w[j], dgate[j]);
-            }
-            own.get(kGate, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                p[j] *= d[j];
-                dw_post[j] = fmaf(p[j], hat[j], dw_post[j]);
-                p[j] *= w[j];
-                sum_p = fmaf(p[j], hat[j], sum_p);
+                branch_factor<T>(a, gate_row, col0, cols(p), f);
+                own.put(kBranch, p, f);
             }
         }
-        ahead = now;
-        ahead.next(s.stages);
-        if (more) {
-            if (RING) ring.wait(ahead.stage, ahead.parity);
-            if (a.pre) sum_x = first_sum(row + 1, ahead.stage, next_x);
-        }
-        const float2 sum = sums(sum_x, sum_p);
-        // everyone has read this row's stage
-        if constexpr (RING)
-            if (tid == 0 && row + s.stages < end) fetch(row + s.stages, now.stage);
-        if (a.u) {
-            const float mean = a.post ? sum.y * per_column : 0.0f;
+        V8 branch[kPer], hat[kPer];          // P, uh
+        float sum_p = 0.0f;
+        if (RING) trail.wait(lost);
+        const uint8_t* stage = lead.base + x_stage * stage_bytes;
+        const R* x = row_at<RING, VEC>(stage, 0, res_out + at, staged);
+        const T* g = row_at<RING, VEC>(stage, second, dy + at, staged);
+        const R* r = row_at<RING, VEC>(trail.at(), 0, dres_out + at, staged);
+        const T* y = row_at<RING, VEC>(trail.at(), second, u + at, staged);
+        const float back1 = -rstd_x * rstd_x * mean_x;
+        const uint64_t back = pair(back1, back1), rx2 = pair(rstd_x, rstd_x), ru2 = pair(rstd_u, rstd_u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = rstd_u * (p[j] - hat[j] * mean);
-            dev::store_cols<VEC>(static_cast<T*>(a.du) + row * H + col0, c, p);
+        for (int p = 0; p < kPer; ++p) {
+            V8 d = {};
+            if (has_dres) d = load_v8<VEC>(r, cols(p));
+            if (pre) {
+                const V8 gv = load_v8<VEC>(g, cols(p)), xv = load_v8<VEC>(x, cols(p)), w = own.get(kPre, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    d.p[j] = fma2(xv.p[j], back, fma2(mul2(gv.p[j], rx2), w.p[j], d.p[j]));
+            }
+            V8 out;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out.p[j] = mul2(beta, d.p[j]);
+            store_v8<VEC>(static_cast<R*>(a.dres) + at + col0, cols(p), out);
+            if (has_u) {
+                hat[p] = load_v8<VEC>(y, cols(p));
+                branch[p] = own.get(kBranch, p);
+                uint64_t part = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    hat[p].p[j] = mul2(hat[p].p[j], ru2);
+                    dots[p].p[j] = fma2(d.p[j], hat[p].p[j], dots[p].p[j]);
+                    branch[p].p[j] = mul2(branch[p].p[j], d.p[j]);
+                    part = fma2(branch[p].p[j], hat[p].p[j], part);
+                }
+                sum_p += on(cols(p)) ? lanes_sum(part) : 0.0f;
+            }
+        }
+        sums.send(sum_x, sum_p);
+        if (row + 2 < end) sum_x = first_sum(row + 2, far_x);
+        const float2 sum = sums.get(lost);
+        // everyone has read this row's stages
+        if constexpr (RING) {
+            if (tid == 0) {
+                if (row + lead.stages < end) fetch_lead(row + lead.stages, x_stage);
+                if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
+            }
+            trail.next();
+            if (++x_stage == lead.stages) x_stage = 0;
+        }
+        if (has_u) {
+            const float mean = post ? -sum.y * per_column : 0.0f;
+            const uint64_t mean2 = pair(mean, mean);
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    branch[p].p[j] = mul2(ru2, fma2(hat[p].p[j], mean2, branch[p].p[j]));
+                store_v8<VEC>(static_cast<T*>(a.du) + at + col0, cols(p), branch[p]);
+            }
         }
         mean_x = sum.x * per_column;
         rstd_x = next_x;
+        next_x = far_x;
         rstd_u = next_u;
-        now = ahead;
     }
-    flush_gate(true);
-    float* part = a.workspace + int64_t(run) * H + col0;
+    if (has_u) end_gate();
+    if (a.dw_pre) {
+        float* part = a.workspace + (int64_t(kSumPre) * s.clusters + run) * H + col0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (!c.has(j)) continue;
-        if (a.dw_pre) part[int64_t(kSumPre) * s.clusters * H + c.at(j)] = dw_pre[j];
-        if (a.dw_post) part[int64_t(kSumPost) * s.clusters * H + c.at(j)] = dw_post[j];
+        for (int p = 0; p < kPer; ++p) store_v8<VEC>(part, cols(p), dw_pre[p]);
     }
-    if (RING && ring.lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
-    if (s.cluster > 1) RowSums::cluster_barrier();
+    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (s.cluster > 1) sums.meet();
 }
 
 // Joins the runs' column sums, in run order.  blockIdx.y 0, 1: dw_pre, dw_post;
@@ -643,42 +893,55 @@ int sm_count() {
 }
 
 int round_up(int v, int to) { return (v + to - 1) / to * to; }
-int threads_of(int width) { return round_up((width + 7) / 8, 32); }
-
-// Blocks of `width` columns that an SM's registers hold.
-int blocks_per_sm(int width) { return kMaxThreads / threads_of(width); }
-
-// The most runs of rows a launch makes: the workspace has room for them.
-int64_t max_clusters(int64_t rows, int64_t hidden) {
-    int cluster = 1;
-    while (round_up(static_cast<int>((hidden + cluster - 1) / cluster), 8) > kMaxSlice) cluster *= 2;
-    const int width = round_up(static_cast<int>((hidden + cluster - 1) / cluster), 8);
-    return std::min<int64_t>(rows, int64_t(sm_count()) * blocks_per_sm(width) / cluster);
+int threads_of(int width) { return std::max(32, round_up((width + 8 * kPer - 1) / (8 * kPer), 32)); }
+int slice(int64_t hidden, int cluster) {
+    return std::max(8, round_up(static_cast<int>((hidden + cluster - 1) / cluster), 8));
 }
 
-// column_bytes: of one column in a stage.  Picks the fewest blocks per row
-// whose ring has two stages, then as many blocks per SM as the registers and
-// then the ring allow.
-NormShape shape_of(int64_t rows, int hidden, int column_bytes, bool vec, size_t* smem) {
+// Threads that an SM's registers hold.
+constexpr int kForwardThreads = 2 * kMaxThreads, kBackwardThreads = kMaxThreads;
+
+// The most runs of rows a backward launch makes: the workspace has room for them.
+int64_t max_clusters(int64_t rows, int64_t hidden) {
+    int cluster = 1;
+    while (slice(hidden, cluster) > kMaxSlice) cluster *= 2;
+    return std::min<int64_t>(rows, int64_t(sm_count()) * (kBackwardThreads / threads_of(slice(hidden, cluster))) / cluster);
+}
+
+// Picks the fewest blocks per row whose rings hold enough, then as many blocks
+// per SM as the registers and then the rings allow.  lead_bytes, trail_bytes:
+// of one column in a stage, of `tensors` tensors.
+NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, int tensors, bool vec,
+                   int sm_threads, size_t* smem) {
     NormShape s = {};
+    const int pad = vec ? 0 : 32 * tensors;
+    auto own = [&] { return kOwnBytes * threads_of(s.width); };
+    auto rings = [&](int lead, int trail) {
+        return lead * (s.width * lead_bytes + pad) + trail * (s.width * trail_bytes + pad);
+    };
+    // Stages for `per_sm` blocks; false with fewer than rows i, i+1 and i+2 in
+    // the leading ring and i and i+1 in the trailing one.
+    auto fill = [&](int per_sm) {
+        const int room = kSmemPerSm / per_sm - kSmemFixed - own();
+        s.lead = 3;
+        s.trail = 2;
+        if (rings(s.lead, s.trail) > room) return false;
+        for (;;) {
+            if (s.lead < kMaxStages && rings(s.lead + 1, s.trail) <= room) ++s.lead;
+            else return true;
+            if (s.trail < kMaxStages && rings(s.lead, s.trail + 1) <= room) ++s.trail;
+        }
+    };
     for (s.cluster = 1;; s.cluster *= 2) {
-        s.width = round_up((hidden + s.cluster - 1) / s.cluster, 8);
-        if (s.width > kMaxSlice) continue;
-        if (s.cluster == kMaxCluster || !vec ||
-            s.width * (2 * column_bytes + 12) + kSmemFixed <= kSmemPerSm)
-            break;
+        s.width = slice(hidden, s.cluster);
+        if (s.width <= kMaxSlice && (s.cluster == kMaxCluster || fill(1))) break;
     }
-    const int threads = threads_of(s.width);
-    const int own = 3 * 32 * threads;     // three parameters of eight columns
-    int per_sm = blocks_per_sm(s.width);
-    const int stage = s.width * column_bytes;
-    auto stages = [&] { return (kSmemPerSm / per_sm - kSmemFixed - own) / std::max(stage, 1); };
-    while (per_sm > 1 && vec && stages() < 2) --per_sm;
+    int per_sm = std::min(sm_threads / threads_of(s.width), 32);
+    while (per_sm > 1 && !fill(per_sm)) --per_sm;
     s.clusters = static_cast<int>(std::min<int64_t>(rows, std::max(1, sm_count() * per_sm / s.cluster)));
-    // the ring pays for itself once runs are longer than a row
-    s.stages = vec && rows > s.clusters ? std::min(kMaxStages, stages()) : 0;
-    if (s.stages < 2) s.stages = 0;
-    *smem = size_t(own) + size_t(s.stages) * stage;
+    // the rings pay for themselves once runs are longer than a row
+    if (rows <= s.clusters || !fill(per_sm)) s.lead = s.trail = 0;
+    *smem = size_t(own()) + rings(s.lead, s.trail);
     return s;
 }
 
@@ -723,10 +986,13 @@ cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaS
         using T = decltype(t);
         using R = decltype(r);
         size_t smem;
-        const NormShape s = shape_of(a.rows, a.hidden, sizeof(T) + sizeof(R), vec, &smem);
-        auto* kernel = s.stages ? block_norm_kernel<T, R, true, true>
-                       : vec    ? block_norm_kernel<T, R, true, false>
-                                : block_norm_kernel<T, R, false, false>;
+        const NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, vec, kForwardThreads, &smem);
+        const bool full = a.u && a.post && a.pre;
+        auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, true, true, true>
+                                               : block_norm_kernel<T, R, true, true, false>)
+                                       : block_norm_kernel<T, R, false, true, false>)
+                                : (vec ? block_norm_kernel<T, R, true, false, false>
+                                       : block_norm_kernel<T, R, false, false, false>);
         return launch_rows(kernel, a, s, smem, stream);
     });
 }
@@ -739,17 +1005,21 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
                                        cudaStream_t stream) {
     const bool vec = a.hidden % 8 == 0 &&
                      all_aligned(a.dy, a.dres_out, a.u, a.res_out, a.w_post, a.w_pre, a.gate, a.du,
-                                 a.dres);
+                                 a.dres, a.dgate);
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
         size_t smem;
-        NormShape s = shape_of(a.rows, a.hidden, 2 * (sizeof(T) + sizeof(R)), vec, &smem);
+        NormShape s = shape_of(a.rows, a.hidden, sizeof(T) + sizeof(R), sizeof(T) + sizeof(R), 2, vec,
+                               kBackwardThreads, &smem);
         s.clusters = static_cast<int>(std::min<int64_t>(s.clusters, max_clusters(a.rows, a.hidden)));
         if (a.rows > 0) {
-            auto* kernel = s.stages ? block_norm_backward_kernel<T, R, true, true>
-                           : vec    ? block_norm_backward_kernel<T, R, true, false>
-                                    : block_norm_backward_kernel<T, R, false, false>;
+            const bool full = a.u && a.post && a.pre && a.dres_out;
+            auto* kernel = s.lead ? (vec ? (full ? block_norm_backward_kernel<T, R, true, true, true>
+                                                   : block_norm_backward_kernel<T, R, true, true, false>)
+                                           : block_norm_backward_kernel<T, R, false, true, false>)
+                                    : (vec ? block_norm_backward_kernel<T, R, true, false, false>
+                                           : block_norm_backward_kernel<T, R, false, false, false>);
             const cudaError_t e = launch_rows(kernel, a, s, smem, stream);
             if (e != cudaSuccess) return e;
         }
