@@ -17,8 +17,8 @@
 //   - the first sum of row i+1 and the second sum of row i are exchanged
 //     together, and the first sum of row i+2 is taken while they travel;
 //   - arithmetic on pairs of columns (f32x2).
-// Rows of up to kMaxSlice columns take one block; longer ones a cluster of 2,
-// 4 or 8 that exchange partial sums through distributed shared memory.  Rows
+// Rows of up to 16 columns a thread take one block; longer ones a cluster of
+// 2, 4 or 8 that exchange partial sums through distributed shared memory.  Rows
 // that are not whole 16-byte blocks take the same path, copied as the aligned
 // blocks that cover them; launches of few rows read global memory directly.
 #include "ct_device.cuh"
@@ -26,13 +26,19 @@
 #include "ct_types.cuh"
 
 #include <algorithm>
+#include <mutex>
+#include <vector>
 
 namespace ct {
 namespace {
 
 constexpr int kPer = 2;               // groups of eight columns per thread
-constexpr int kMaxThreads = 512;      // 128 registers a thread, 64 forward
-constexpr int kMaxSlice = 8 * kPer * kMaxThreads;
+// Threads of a block and registers of a thread: forward, two blocks of 512 with
+// 64; backward, 384 with 168, which its column sums and the compiler's room to
+// interleave columns need (8192x6144 bf16, 512 with 128: 109 us, so: 106;
+// 12288x4096: 131, so: 119).
+constexpr int kForwardThreads = 512, kBackwardThreads = 384;
+constexpr int kMaxThreads = kForwardThreads;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxStages = 6;         // of either ring
@@ -359,12 +365,16 @@ __device__ __forceinline__ const T* row_at(const uint8_t* stage, uint32_t offset
     return reinterpret_cast<const T*>(stage);
 }
 
+// The next kernel of the stream is let in when a block's rows are done, not
+// at once: blocks of it that came to wait beside these would take the room of
+// the last of them, which would then run as a second wave.
+//
 // FULL: u, both norms and (backward) dres_out are there, known to the compiler.
 
 // Forward.  Per row: sum u^2 -> rstd_post; res_out and sum res_out^2 ->
 // rstd_pre; y.
 template <typename T, typename R, bool VEC, bool RING, bool FULL>
-__global__ void __launch_bounds__(kMaxThreads, 2) block_norm_kernel(const NormArgs a,
+__global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const NormArgs a,
                                                                     const NormShape s) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
@@ -385,7 +395,6 @@ __global__ void __launch_bounds__(kMaxThreads, 2) block_norm_kernel(const NormAr
     const Own own{reinterpret_cast<float4*>(RING ? trail.base + trail.stages * trail.stage_bytes : smem)};
     RowSums sums{slots, full + 2 * kMaxStages, s.cluster, rank};
 
-    dev::pdl_launch_dependents();
     if (tid == 0) {
         block_max = 0;
         sums.init();
@@ -531,6 +540,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) block_norm_kernel(const NormAr
             }
         }
     }
+    dev::pdl_launch_dependents();
     if (a.scale && pre) {
         most = __reduce_max_sync(0xFFFFFFFFu, most);
         if ((tid & 31) == 0) atomicMax(&block_max, most);
@@ -556,7 +566,7 @@ enum { kSumPre, kSumPost, kSumGateFirst, kSumGateLast, kSums };
 //   dw_pre = sum dy xh
 //   S  = sum D uh over a gate row's rows: dgate = alpha a_post S, dw_post = sum alpha gate S
 template <typename T, typename R, bool VEC, bool RING, bool FULL>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+__global__ void __launch_bounds__(kBackwardThreads, 1)
     block_norm_backward_kernel(const NormBackwardArgs a, const NormShape s) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
@@ -581,7 +591,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const T* dy = static_cast<const T*>(a.dy) + col0;
     const T* u = static_cast<const T*>(a.u) + col0;
 
-    dev::pdl_launch_dependents();
     if (tid == 0) {
         sums.init();
         if constexpr (RING) {
@@ -790,6 +799,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         next_x = far_x;
         rstd_u = next_u;
     }
+    dev::pdl_launch_dependents();
     if (has_u) end_gate();
     if (a.dw_pre) {
         float* part = a.workspace + (int64_t(kSumPre) * s.clusters + run) * H + col0;
@@ -803,7 +813,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 // Joins the runs' column sums, in run order.  blockIdx.y 0, 1: dw_pre, dw_post;
 // from 2 on the gate rows that more than one run has rows of, by gate row
 // (few of them, perhaps of many runs), else by the run they begin in.
-constexpr int kJoinCols = 32, kJoinRuns = 8;
+constexpr int kJoinCols = 32, kJoinRuns = 32;   // threads: columns x at most so many shares of the runs
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinCols * kJoinRuns)
@@ -813,6 +823,7 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRuns)
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     const int H = a.hidden, x = threadIdx.x % kJoinCols, y = threadIdx.x / kJoinCols;
+    const int shares = blockDim.x / kJoinCols;
     const int which = blockIdx.y;
     int64_t first = 0, last = runs - 1, at = 0;   // the runs to add up
     int col = blockIdx.x * kJoinCols + x;
@@ -824,9 +835,9 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRuns)
             gate_row = which - 2;
             first = run_of(a.rows, gate_row * a.rows_per_gate, runs);
         } else {
-            // a block of kJoinCols * kJoinRuns columns of the gate row that run
+            // blockDim.x columns of the gate row that run
             // `which - 2` ends in, if it begins there
-            col = blockIdx.x * (kJoinCols * kJoinRuns) + threadIdx.x;
+            col = blockIdx.x * blockDim.x + threadIdx.x;
             first = which - 2;
             gate_row = (run_begin(a.rows, first + 1, runs) - 1) / a.rows_per_gate;
             if (gate_row * a.rows_per_gate < run_begin(a.rows, first, runs)) return;
@@ -853,13 +864,12 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRuns)
     }
     if (col < H) {
 #pragma unroll 8
-        for (int64_t r = first + y; r <= last; r += kJoinRuns) sum += part(r);
+        for (int64_t r = first + y; r <= last; r += shares) sum += part(r);
     }
     parts[y][x] = sum;
     __syncthreads();
     if (y == 0 && col < H) {
-#pragma unroll
-        for (int i = 1; i < kJoinRuns; ++i) sum += parts[i][x];
+        for (int i = 1; i < shares; ++i) sum += parts[i][x];
         set_param<T>(out, a.param_f32, at + col, sum);
     }
 }
@@ -898,21 +908,19 @@ int slice(int64_t hidden, int cluster) {
     return std::max(8, round_up(static_cast<int>((hidden + cluster - 1) / cluster), 8));
 }
 
-// Threads that an SM's registers hold.
-constexpr int kForwardThreads = 2 * kMaxThreads, kBackwardThreads = kMaxThreads;
-
 // The most runs of rows a backward launch makes: the workspace has room for them.
 int64_t max_clusters(int64_t rows, int64_t hidden) {
     int cluster = 1;
-    while (slice(hidden, cluster) > kMaxSlice) cluster *= 2;
+    while (threads_of(slice(hidden, cluster)) > kBackwardThreads) cluster *= 2;
     return std::min<int64_t>(rows, int64_t(sm_count()) * (kBackwardThreads / threads_of(slice(hidden, cluster))) / cluster);
 }
 
 // Picks the fewest blocks per row whose rings hold enough, then as many blocks
 // per SM as the registers and then the rings allow.  lead_bytes, trail_bytes:
-// of one column in a stage, of `tensors` tensors.
+// of one column in a stage, of `tensors` tensors; max_threads, sm_threads: of
+// a block, and of those that an SM's registers hold.
 NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, int tensors, bool vec,
-                   int sm_threads, size_t* smem) {
+                   int max_threads, int sm_threads, size_t* smem) {
     NormShape s = {};
     const int pad = vec ? 0 : 32 * tensors;
     auto own = [&] { return kOwnBytes * threads_of(s.width); };
@@ -934,7 +942,7 @@ NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, in
     };
     for (s.cluster = 1;; s.cluster *= 2) {
         s.width = slice(hidden, s.cluster);
-        if (s.width <= kMaxSlice && (s.cluster == kMaxCluster || fill(1))) break;
+        if (threads_of(s.width) <= max_threads && (s.cluster == kMaxCluster || fill(1))) break;
     }
     int per_sm = std::min(sm_threads / threads_of(s.width), 32);
     while (per_sm > 1 && !fill(per_sm)) --per_sm;
@@ -945,21 +953,13 @@ NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, in
     return s;
 }
 
-template <typename Args>
-cudaError_t launch_rows(void (*kernel)(const Args, const NormShape), const Args& a, const NormShape& s,
-                        size_t smem, cudaStream_t stream) {
-    if (smem > 40 * 1024) {   // 48 KB with the static part
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kSmemPerSm - kSmemFixed);
-        if (e != cudaSuccess) return e;
-    }
+// The launch configuration of a shape; `attr` has to live as long as it.
+cudaLaunchConfig_t config_of(const NormShape& s, size_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.clusters * s.cluster));
     cfg.blockDim = dim3(static_cast<unsigned>(threads_of(s.width)));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -967,6 +967,57 @@ cudaError_t launch_rows(void (*kernel)(const Args, const NormShape), const Args&
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = s.cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
+// Before a kernel's first launch on a device with this much shared memory:
+// allows it, and asks for as much shared memory as the SM has.  Limits the
+// runs to the clusters that can be resident: those of 4 or 8 blocks do not
+// fill every SM, and a second wave of runs would double the time.
+cudaError_t prepare(const void* kernel, NormShape& s, size_t smem) {
+    struct Known {
+        const void* kernel;
+        int device, cluster, threads;
+        size_t smem;
+        int most;
+    };
+    static std::mutex mutex;
+    static std::vector<Known> known;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mutex);
+    for (const Known& k : known)
+        if (k.kernel == kernel && k.device == device && k.cluster == s.cluster &&
+            k.threads == threads_of(s.width) && k.smem == smem) {
+            s.clusters = std::min(s.clusters, k.most);
+            return cudaSuccess;
+        }
+    Known k = {kernel, device, s.cluster, threads_of(s.width), smem, s.clusters};
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - kSmemFixed);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    k.most = 1 << 30;
+    if (s.cluster > 1) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = config_of(s, smem, nullptr, attr);
+        int most = 0;
+        e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        k.most = std::max(most, 1);
+    }
+    known.push_back(k);
+    s.clusters = std::min(s.clusters, k.most);
+    return cudaSuccess;
+}
+
+template <typename Args>
+cudaError_t launch_rows(void (*kernel)(const Args, const NormShape), const Args& a, const NormShape& s,
+                        size_t smem, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config_of(s, smem, stream, attr);
     return cudaLaunchKernelEx(&cfg, kernel, a, s);
 }
 
@@ -986,14 +1037,16 @@ cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaS
         using T = decltype(t);
         using R = decltype(r);
         size_t smem;
-        const NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, vec, kForwardThreads, &smem);
+        NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, vec, kForwardThreads,
+                                     2 * kForwardThreads, &smem);
         const bool full = a.u && a.post && a.pre;
         auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, true, true, true>
                                                : block_norm_kernel<T, R, true, true, false>)
                                        : block_norm_kernel<T, R, false, true, false>)
                                 : (vec ? block_norm_kernel<T, R, true, false, false>
                                        : block_norm_kernel<T, R, false, false, false>);
-        return launch_rows(kernel, a, s, smem, stream);
+        const cudaError_t e = prepare(reinterpret_cast<const void*>(kernel), s, smem);
+        return e != cudaSuccess ? e : launch_rows(kernel, a, s, smem, stream);
     });
 }
 
@@ -1011,7 +1064,7 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
         using R = decltype(r);
         size_t smem;
         NormShape s = shape_of(a.rows, a.hidden, sizeof(T) + sizeof(R), sizeof(T) + sizeof(R), 2, vec,
-                               kBackwardThreads, &smem);
+                               kBackwardThreads, kBackwardThreads, &smem);
         s.clusters = static_cast<int>(std::min<int64_t>(s.clusters, max_clusters(a.rows, a.hidden)));
         if (a.rows > 0) {
             const bool full = a.u && a.post && a.pre && a.dres_out;
@@ -1020,7 +1073,8 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
                                            : block_norm_backward_kernel<T, R, false, true, false>)
                                     : (vec ? block_norm_backward_kernel<T, R, true, false, false>
                                            : block_norm_backward_kernel<T, R, false, false, false>);
-            const cudaError_t e = launch_rows(kernel, a, s, smem, stream);
+            cudaError_t e = prepare(reinterpret_cast<const void*>(kernel), s, smem);
+            if (e == cudaSuccess) e = launch_rows(kernel, a, s, smem, stream);
             if (e != cudaSuccess) return e;
         }
         if (!a.dw_pre && !a.dw_post && !a.dgate) return cudaSuccess;
@@ -1029,7 +1083,10 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
         const int64_t joins = !a.dgate ? 0 : by_gate_row ? gates : s.clusters - 1;
         return launch_pdl(block_norm_join_kernel<T>,
                           dim3((a.hidden + kJoinCols - 1) / kJoinCols, static_cast<unsigned>(2 + joins)),
-                          dim3(kJoinCols * kJoinRuns), 0, stream, a, int64_t(s.clusters),
+                          // many runs: shorter sums (912 runs of 777 columns, 8
+                          // shares: 18.7 us, 32: under 5), few: smaller blocks
+                          dim3(kJoinCols * (s.clusters > 256 ? kJoinRuns : 8)), 0, stream, a,
+                          int64_t(s.clusters),
                           by_gate_row ? 1 : 0);
     });
 }
