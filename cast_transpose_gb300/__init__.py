@@ -63,6 +63,8 @@ class _Desc(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """Load libct_gb300.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -166,8 +168,25 @@ _U8 = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """The stream's handle; None: the current one's, without the Stream object
+    around it (0.2 us a call against 2.8)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
+def _ptr(t, name, dtype, shape) -> int:
+    """As _dev, for a tensor of this dtype (or one of a tuple) and shape: one
+    pass of cheap tests, and the reason only where they fail."""
+    if type(t) in _TENSORS and t.is_cuda and t.shape == shape and t.is_contiguous() and (
+            t.dtype in dtype if type(dtype) is tuple else t.dtype == dtype):
+        return t.data_ptr()
+    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _dev(t, name, dtype)
+
+
+_TENSORS = (torch.Tensor, torch.nn.Parameter)
 
 
 def _rc(x: torch.Tensor):

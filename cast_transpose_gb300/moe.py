@@ -19,10 +19,11 @@ from __future__ import annotations
 
 import torch
 
-from . import E4M3, _check, _dev, _opt, _stream, _U8, lib
+from . import E4M3, _check, _dev, _opt, _ptr, _stream, _U8, lib
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_I32 = torch.int32
+_I32, _F32 = torch.int32, torch.float32
+_INDEX = (torch.int32, torch.int64)
 
 
 def moe_sorted_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int:
@@ -49,70 +50,60 @@ class MoePlan:
         self.tokens, self.topk, self.experts, self.align, self.rows = (tokens, topk, experts,
                                                                        align, rows)
 
-        def buffer(t, name, *shape):
-            if t is None:
-                return torch.empty(*shape, dtype=_I32, device=device)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-            return t
+        def buffer(t, shape):
+            return torch.empty(shape, dtype=_I32, device=device) if t is None else t
 
-        self.row_of = buffer(row_of, "row_of", tokens, topk)
-        self.src = buffer(src, "src", rows)
-        self.offsets = buffer(offsets, "offsets", experts + 1)
-        self.counts = buffer(counts, "counts", experts)
+        self.row_of = buffer(row_of, (tokens, topk))
+        self.src = buffer(src, (rows,))
+        self.offsets = buffer(offsets, (experts + 1,))
+        self.counts = buffer(counts, (experts,))
         size = int(lib().moe_sort_workspace_size(tokens, topk, experts))
         self.workspace = torch.empty(size, dtype=torch.uint8, device=self.row_of.device)
+        self.slots = (tokens, topk)
         # these buffers stay the plan's: checked once, here
-        self._row_of = _dev(self.row_of, "row_of", _I32)
-        self._src = _dev(self.src, "src", _I32)
-        self._offsets = _dev(self.offsets, "offsets", _I32)
-        self._counts = _dev(self.counts, "counts", _I32)
-        self._workspace = self.workspace.data_ptr()
+        self._row_of = _ptr(self.row_of, "row_of", _I32, (tokens, topk))
+        self._src = _ptr(self.src, "src", _I32, (rows,))
+        self._offsets = _ptr(self.offsets, "offsets", _I32, (experts + 1,))
+        self._counts = _ptr(self.counts, "counts", _I32, (experts,))
+        self._workspace, self._workspace_size = self.workspace.data_ptr(), size
 
 
-def _matrix(t, name, rows, dtypes=_DTYPES, hidden=None):
+def _rows_of(t, name):
+    """The columns of a matrix of a floating type, and the type."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D matrix")
-    if t.shape[0] != rows or hidden not in (None, t.shape[1]):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"({rows}, {'hidden' if hidden is None else hidden})")
-    return _dev(t, name, tuple(dtypes))
-
-
-def _weights(t, name, plan):
-    if tuple(t.shape) != (plan.tokens, plan.topk):
-        raise ValueError(f"{name} must be [tokens, topk]")
-    return _dev(t, name, torch.float32)
+    dtype = t.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name} has dtype {dtype}, expected bfloat16, float16 or float32")
+    return t.shape[1], dtype
 
 
 def moe_sort(expert_idx, plan: MoePlan, noop_flag=None, stream=None) -> None:
     """Fill the plan from expert_idx [T, K] (int32 or int64).  The sort is
     stable; an index outside [0, E), -1 say, drops the slot."""
-    if tuple(expert_idx.shape) != (plan.tokens, plan.topk):
-        raise ValueError("expert_idx must be [tokens, topk]")
-    idx = _dev(expert_idx, "expert_idx", (torch.int32, torch.int64))
-    _check(lib().moe_sort(idx, expert_idx.element_size(), plan.tokens, plan.topk, plan.experts,
-                          plan.align, plan.rows, plan._row_of, plan._src, plan._offsets,
-                          plan._counts, plan._workspace, plan.workspace.numel(),
+    idx = _ptr(expert_idx, "expert_idx", _INDEX, plan.slots)
+    _check(lib().moe_sort(idx, 4 if expert_idx.dtype == _I32 else 8, plan.tokens, plan.topk,
+                          plan.experts, plan.align, plan.rows, plan._row_of, plan._src,
+                          plan._offsets, plan._counts, plan._workspace, plan._workspace_size,
                           _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
 def moe_dispatch(x, plan: MoePlan, out, noop_flag=None, stream=None) -> None:
     """x [T, hidden] -> out [rows, hidden] of the same type."""
-    px = _matrix(x, "x", plan.tokens)
-    hidden = x.shape[1]
-    po = _matrix(out, "out", plan.rows, (x.dtype,), hidden)
-    _check(lib().moe_dispatch(px, plan.tokens, plan.topk, hidden, _DTYPES[x.dtype], plan._row_of,
+    hidden, dtype = _rows_of(x, "x")
+    px = _ptr(x, "x", dtype, (plan.tokens, hidden))
+    po = _ptr(out, "out", dtype, (plan.rows, hidden))
+    _check(lib().moe_dispatch(px, plan.tokens, plan.topk, hidden, _DTYPES[dtype], plan._row_of,
                               plan._src, plan.rows, po, _opt(noop_flag, "noop_flag"),
                               _stream(stream)))
 
 
 def moe_dispatch_backward(dout, plan: MoePlan, dx, noop_flag=None, stream=None) -> None:
     """dout [rows, hidden] -> dx [T, hidden] of the same type."""
-    pd = _matrix(dout, "dout", plan.rows)
-    hidden = dout.shape[1]
-    px = _matrix(dx, "dx", plan.tokens, (dout.dtype,), hidden)
-    _check(lib().moe_dispatch_backward(pd, plan.tokens, plan.topk, hidden, _DTYPES[dout.dtype],
+    hidden, dtype = _rows_of(dout, "dout")
+    pd = _ptr(dout, "dout", dtype, (plan.rows, hidden))
+    px = _ptr(dx, "dx", dtype, (plan.tokens, hidden))
+    _check(lib().moe_dispatch_backward(pd, plan.tokens, plan.topk, hidden, _DTYPES[dtype],
                                        plan._row_of, plan.rows, px, _opt(noop_flag, "noop_flag"),
                                        _stream(stream)))
 
@@ -122,25 +113,24 @@ def fp8_moe_dispatch(x, plan: MoePlan, scale, amax, scale_inv, out, out_t=None, 
     """bf16 x [T, hidden] -> FP8 out [rows, hidden] and, unless None, out_t
     [hidden, rows].  weights: fp32 [T, K], multiplied in before the amax and
     the cast; with dy for x, FP8 gradients for the experts' outputs."""
-    px = _matrix(x, "x", plan.tokens, (torch.bfloat16,))
-    hidden = x.shape[1]
-    po = _matrix(out, "out", plan.rows, _U8, hidden)
-    pt = None if out_t is None else _matrix(out_t, "out_t", hidden, _U8, plan.rows)
-    pw = None if weights is None else _weights(weights, "weights", plan)
+    hidden, _ = _rows_of(x, "x")
+    px = _ptr(x, "x", torch.bfloat16, (plan.tokens, hidden))
+    po = _ptr(out, "out", _U8, (plan.rows, hidden))
+    pt = None if out_t is None else _ptr(out_t, "out_t", _U8, (hidden, plan.rows))
+    pw = None if weights is None else _ptr(weights, "weights", _F32, plan.slots)
     _check(lib().fp8_moe_dispatch(px, plan.tokens, plan.topk, hidden, plan._src, plan.rows, pw,
-                                  _dev(scale, "scale", torch.float32, 1),
-                                  _dev(amax, "amax", torch.float32, 1),
-                                  _dev(scale_inv, "scale_inv", torch.float32, 1), po, pt, fmt,
+                                  _dev(scale, "scale", _F32, 1), _dev(amax, "amax", _F32, 1),
+                                  _dev(scale_inv, "scale_inv", _F32, 1), po, pt, fmt,
                                   _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
 def moe_combine(ys, plan: MoePlan, weights, out, noop_flag=None, stream=None) -> None:
     """ys [rows, hidden], weights fp32 [T, K] -> out [T, hidden] of ys' type."""
-    py = _matrix(ys, "ys", plan.rows)
-    hidden = ys.shape[1]
-    po = _matrix(out, "out", plan.tokens, (ys.dtype,), hidden)
-    _check(lib().moe_combine(py, plan.tokens, plan.topk, hidden, _DTYPES[ys.dtype], plan._row_of,
-                             _weights(weights, "weights", plan), plan.rows, po,
+    hidden, dtype = _rows_of(ys, "ys")
+    py = _ptr(ys, "ys", dtype, (plan.rows, hidden))
+    po = _ptr(out, "out", dtype, (plan.tokens, hidden))
+    _check(lib().moe_combine(py, plan.tokens, plan.topk, hidden, _DTYPES[dtype], plan._row_of,
+                             _ptr(weights, "weights", _F32, plan.slots), plan.rows, po,
                              _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
@@ -148,12 +138,12 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
                          noop_flag=None, stream=None) -> None:
     """dout [T, hidden] -> dys [rows, hidden] and dweights fp32 [T, K]; either
     may be None (ys is read for dweights only)."""
-    pd = _matrix(dout, "dout", plan.tokens)
-    hidden, dtype = dout.shape[1], (dout.dtype,)
-    py = None if ys is None else _matrix(ys, "ys", plan.rows, dtype, hidden)
-    ps = None if dys is None else _matrix(dys, "dys", plan.rows, dtype, hidden)
-    pw = None if dweights is None else _weights(dweights, "dweights", plan)
-    _check(lib().moe_combine_backward(pd, py, plan.tokens, plan.topk, hidden, _DTYPES[dout.dtype],
+    hidden, dtype = _rows_of(dout, "dout")
+    pd = _ptr(dout, "dout", dtype, (plan.tokens, hidden))
+    py = None if ys is None else _ptr(ys, "ys", dtype, (plan.rows, hidden))
+    ps = None if dys is None else _ptr(dys, "dys", dtype, (plan.rows, hidden))
+    pw = None if dweights is None else _ptr(dweights, "dweights", _F32, plan.slots)
+    _check(lib().moe_combine_backward(pd, py, plan.tokens, plan.topk, hidden, _DTYPES[dtype],
                                       plan._row_of, plan._src,
-                                      _weights(weights, "weights", plan), plan.rows, ps, pw,
+                                      _ptr(weights, "weights", _F32, plan.slots), plan.rows, ps, pw,
                                       _opt(noop_flag, "noop_flag"), _stream(stream)))

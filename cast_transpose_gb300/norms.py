@@ -15,7 +15,7 @@ import ctypes
 
 import torch
 
-from . import E4M3, _check, _dev, _opt, _stream, _U8, lib
+from . import E4M3, _check, _dev, _opt, _ptr, _stream, _U8, lib
 from .moe import _DTYPES
 
 _F32 = torch.float32
@@ -31,31 +31,27 @@ class _Config(ctypes.Structure):
                 ("flags", ctypes.c_int)]
 
 
-def _typed(t, name, shape, dtypes):
-    if t is None:
-        return None
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return _dev(t, name, dtypes)
+def _given(t, name, dtype, shape):
+    return None if t is None else _ptr(t, name, dtype, shape)
 
 
-def _config(res, dtype, w_post, w_pre, gate, rows_per_gate, eps, branch_scale, residual_scale,
-            weight_offset, post_norm, pre_norm):
-    """The call's config, the types of its parameters and its gate's shape."""
-    rows, hidden = res.shape
-    params = [t for t in (w_post, w_pre, gate) if t is not None]
-    ptype = params[0].dtype if params else dtype
+def _config(shape, res_dtype, dtype, w_post, w_pre, gate, rows_per_gate, eps, branch_scale,
+            residual_scale, weight_offset, post_norm, pre_norm):
+    """The call's config, the type of its parameters and its gate's shape."""
+    rows, hidden = shape
+    first = w_post if w_post is not None else w_pre if w_pre is not None else gate
+    ptype = dtype if first is None else first.dtype
     if rows_per_gate is None:
         rows_per_gate = max(rows, 1)
     groups = (-(-rows // rows_per_gate) if rows_per_gate > 0 else 0, hidden)
-    for t, name in ((dtype, "u and y"), (res.dtype, "res"), (ptype, "the parameters")):
-        if t not in _DTYPES:
-            raise TypeError(f"{name}: dtype {t} is not bfloat16, float16 or float32")
-    cfg = _Config(rows, hidden, rows_per_gate, _typed(w_post, "w_post", (hidden,), ptype),
-                  _typed(w_pre, "w_pre", (hidden,), ptype), _typed(gate, "gate", groups, ptype),
-                  eps, branch_scale, residual_scale, weight_offset, _DTYPES[dtype],
-                  _DTYPES[res.dtype], _DTYPES[ptype], (1 if post_norm else 0) |
-                  (2 if pre_norm else 0))
+    try:
+        types = _DTYPES[dtype], _DTYPES[res_dtype], _DTYPES[ptype]
+    except KeyError as e:
+        raise TypeError(f"dtype {e} is not bfloat16, float16 or float32") from None
+    cfg = _Config(rows, hidden, rows_per_gate, _given(w_post, "w_post", ptype, (hidden,)),
+                  _given(w_pre, "w_pre", ptype, (hidden,)), _given(gate, "gate", ptype, groups),
+                  eps, branch_scale, residual_scale, weight_offset, *types,
+                  (1 if post_norm else 0) | (2 if pre_norm else 0))
     return cfg, ptype, groups
 
 
@@ -72,18 +68,19 @@ def block_norm(u, res, res_out=None, y=None, w_post=None, w_pre=None, gate=None,
     (fp32 scalars) y is FP8 of format fmt, cast as fp8_cast does."""
     if res.dim() != 2:
         raise ValueError("res must be a 2-D matrix")
-    shape = rows, hidden = tuple(res.shape)
+    shape, rtype = tuple(res.shape), res.dtype
+    rows = shape[:1]
     if u is not None:
         dtype = u.dtype
     else:
-        dtype = y.dtype if y is not None and scale is None else res.dtype
-    cfg, _, _ = _config(res, dtype, w_post, w_pre, gate, rows_per_gate, eps, branch_scale,
+        dtype = y.dtype if y is not None and scale is None else rtype
+    cfg, _, _ = _config(shape, rtype, dtype, w_post, w_pre, gate, rows_per_gate, eps, branch_scale,
                         residual_scale, weight_offset, post_norm, pre_norm)
     _check(lib().block_norm(
-        ctypes.byref(cfg), _typed(u, "u", shape, dtype), _typed(res, "res", shape, res.dtype),
-        _typed(res_out, "res_out", shape, res.dtype),
-        _typed(y, "y", shape, dtype if scale is None else _U8),
-        _typed(rstd_post, "rstd_post", (rows,), _F32), _typed(rstd_pre, "rstd_pre", (rows,), _F32),
+        ctypes.byref(cfg), _given(u, "u", dtype, shape), _ptr(res, "res", rtype, shape),
+        _given(res_out, "res_out", rtype, shape),
+        _given(y, "y", dtype if scale is None else _U8, shape),
+        _given(rstd_post, "rstd_post", _F32, rows), _given(rstd_pre, "rstd_pre", _F32, rows),
         _opt(scale, "scale"), _opt(amax, "amax"), _opt(scale_inv, "scale_inv"), fmt,
         _opt(noop_flag, "noop_flag"), _stream(stream)))
 
@@ -104,21 +101,21 @@ def block_norm_backward(dy, dres_out, u, res_out, rstd_post, rstd_pre, du=None, 
     block_norm_backward_workspace_size(rows, hidden) bytes."""
     if dres.dim() != 2:
         raise ValueError("dres must be a 2-D matrix")
-    shape = rows, hidden = tuple(dres.shape)
+    shape, rtype = tuple(dres.shape), dres.dtype
+    rows, columns = shape[:1], shape[1:]
     dtype = u.dtype if u is not None else dy.dtype
-    cfg, ptype, groups = _config(dres, dtype, w_post, w_pre, gate, rows_per_gate, 0.0,
+    cfg, ptype, groups = _config(shape, rtype, dtype, w_post, w_pre, gate, rows_per_gate, 0.0,
                                  branch_scale, residual_scale, weight_offset, post_norm, pre_norm)
-    grads = [t for t in (dw_post, dw_pre, dgate) if t is not None]
-    if w_post is None and w_pre is None and gate is None and grads:
+    if w_post is None and w_pre is None and gate is None and not (
+            dw_post is None and dw_pre is None and dgate is None):
         raise ValueError("a gradient of a weight that is not given")
     _check(lib().block_norm_backward(
-        ctypes.byref(cfg), _typed(dy, "dy", shape, dtype),
-        _typed(dres_out, "dres_out", shape, dres.dtype), _typed(u, "u", shape, dtype),
-        _typed(res_out, "res_out", shape, dres.dtype),
-        _typed(rstd_post, "rstd_post", (rows,), _F32), _typed(rstd_pre, "rstd_pre", (rows,), _F32),
-        _typed(du, "du", shape, dtype), _typed(dres, "dres", shape, dres.dtype),
-        _typed(dw_post, "dw_post", (hidden,), ptype), _typed(dw_pre, "dw_pre", (hidden,), ptype),
-        _typed(dgate, "dgate", groups, ptype),
+        ctypes.byref(cfg), _given(dy, "dy", dtype, shape), _given(dres_out, "dres_out", rtype, shape),
+        _given(u, "u", dtype, shape), _given(res_out, "res_out", rtype, shape),
+        _given(rstd_post, "rstd_post", _F32, rows), _given(rstd_pre, "rstd_pre", _F32, rows),
+        _given(du, "du", dtype, shape), _ptr(dres, "dres", rtype, shape),
+        _given(dw_post, "dw_post", ptype, columns), _given(dw_pre, "dw_pre", ptype, columns),
+        _given(dgate, "dgate", ptype, groups),
         None if workspace is None else _dev(workspace, "workspace", torch.uint8),
         0 if workspace is None else workspace.numel(), _opt(noop_flag, "noop_flag"),
         _stream(stream)))
