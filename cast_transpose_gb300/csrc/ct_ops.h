@@ -17,6 +17,7 @@ struct SortArgs {
     int* counts;           // [experts]
     const float* noop;
     int experts, align, index64;
+    int expert_bits;       // experts <= 2^expert_bits
 };
 size_t sort_workspace(int64_t n, int experts);
 cudaError_t launch_moe_sort(const SortArgs& a, void* workspace, cudaStream_t stream);

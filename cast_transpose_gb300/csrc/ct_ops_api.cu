@@ -106,6 +106,7 @@ int moe_sort(const void* expert_idx, int index_bytes, int64_t tokens, int topk, 
     a.experts = experts;
     a.align = align;
     a.index64 = index_bytes == 8;
+    for (a.expert_bits = 0; (1 << a.expert_bits) < experts;) ++a.expert_bits;
     return cuda_status(ct::launch_moe_sort(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
