@@ -295,14 +295,38 @@ __device__ void clear_padding(const MoveArgs& a, int64_t words) {
     }
 }
 
+// What the first blocks of a dispatch ask to have in L2 while they wait for the
+// kernel before, as a rule the sort, which leaves HBM idle for its 4 to 15 us:
+// the rows of x that are moved first.  A hint: whatever is written to x
+// meanwhile is written in L2 too.  A call with a noop flag does not ask.
+//   8191x4x6144 with its sort: 89.3 us without, 85.3 with 24 MB, 85.8 with 48.
+constexpr int64_t kPrefetchBytes = int64_t(24) << 20;
+constexpr int kPrefetchBlocks = 608;
+
+struct Prefetch {
+    const uint8_t* from;
+    int64_t bytes;          // a multiple of 16
+    int blocks;
+    static constexpr uint32_t kPiece = 4096;
+
+    __device__ __forceinline__ void issue() const {
+        if (blockIdx.x >= blocks) return;
+        for (int64_t at = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * kPiece; at < bytes;
+             at += int64_t(blocks) * blockDim.x * kPiece)
+            dev::prefetch_l2_bulk(from + at, static_cast<uint32_t>(min(int64_t(kPiece), bytes - at)));
+    }
+};
+
 // W: the word that rows are moved in.  kMoveWords loads of a thread are in
 // flight at a time.
 constexpr int kMoveWords = 4;
 
 template <typename W>
-__global__ void __launch_bounds__(kMoveThreads) moe_dispatch_kernel(MoveArgs a, int pad_blocks) {
+__global__ void __launch_bounds__(kMoveThreads)
+    moe_dispatch_kernel(MoveArgs a, int pad_blocks, Prefetch ahead) {
     __shared__ int rows[kMaxSlots];
     pdl_launch_dependents();
+    ahead.issue();
     pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     const int words = static_cast<int>(a.hidden * a.elem_bytes / sizeof(W));
@@ -551,10 +575,14 @@ cudaError_t launch_moe_sort(const SortArgs& a, void* workspace, cudaStream_t str
 
 cudaError_t launch_moe_dispatch(const MoveArgs& a, cudaStream_t stream) {
     const int pad = pad_blocks(a);
+    const int64_t bytes = a.tokens * a.hidden * a.elem_bytes;
+    const Prefetch ahead = {static_cast<const uint8_t*>(a.x), std::min(bytes, kPrefetchBytes),
+                            vectors(a) && !a.noop ? kPrefetchBlocks : 0};
     auto go = [&](auto w) {
         using W = decltype(w);
         return launch_pdl(moe_dispatch_kernel<W>, dim3(static_cast<unsigned>(a.tokens + pad)),
-                          move_threads(a.hidden * a.elem_bytes / int64_t(sizeof(W)), 3), 0, stream, a, pad);
+                          move_threads(a.hidden * a.elem_bytes / int64_t(sizeof(W)), 3), 0, stream, a, pad,
+                          ahead);
     };
     if (vectors(a)) return go(uint4{});
     return a.elem_bytes == 4 ? go(uint32_t{}) : go(uint16_t{});

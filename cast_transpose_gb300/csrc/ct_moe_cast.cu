@@ -3,6 +3,8 @@
 #include "ct_device.cuh"
 #include "ct_ops.h"
 
+#include <type_traits>
+
 namespace ct {
 namespace {
 
@@ -52,30 +54,39 @@ __global__ void __launch_bounds__(kCastThreads, 4)
         if (WEIGHTED) weight[tid] = w;
     }
     const float scale = *a.scale;
-    __syncthreads();
+    // no padding and no end among the block's rows: most blocks
+    const bool whole_rows = __syncthreads_and(tid >= 128 || token[tid & 127] >= 0);
 
+    unsigned most = 0;
+    uint4 v[8];
     // columns 8c .. 8c+7 of rows rg + 16 i: all eight loads in flight at once
     const int c = tid & 15, rg = tid >> 4;
-    uint4 v[8];
-    auto load = [&](int64_t col0) {
-        const int64_t col = col0 + 8 * c;
-        const uint16_t* x = a.x + col;
+    // rows 16b .. 16b+15 of the four columns of word w
+    const int b = lane & 7, w4 = warp * 4 + (lane >> 3);
+    const uint16_t* x = a.x + 8 * c;
+    uint8_t* const q0 = a.out + (row0 + rg) * a.hidden + 8 * c;
+    uint8_t* const t0 = TRANSPOSE ? a.out_t + int64_t(4 * w4) * a.rows + row0 + 16 * b : nullptr;
+    const int64_t q_step = 16 * a.hidden;
+
+    // WHOLE: every row and column of the tile is there.
+    auto load = [&](auto whole, int64_t col0) {
+        constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int t = token[rg + 16 * i];
-            v[i] = col < a.hidden && t >= 0 ? __ldg(reinterpret_cast<const uint4*>(x + t * a.hidden))
-                                            : make_uint4(0u, 0u, 0u, 0u);
+            const uint4* p = reinterpret_cast<const uint4*>(x + t * a.hidden + col0);
+            if (WHOLE)
+                v[i] = __ldcg(p);
+            else
+                v[i] = col0 + 8 * c < a.hidden && t >= 0 ? __ldcg(p) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
-    unsigned most = 0;
-    const int first = strip * kStripTiles, last = min(first + kStripTiles, tile_cols);
-    load(int64_t(first) * 128);
-    for (int ct = first; ct < last; ++ct) {
-        const int64_t col0 = int64_t(ct) * 128;
-        const bool col_ok = col0 + 8 * c < a.hidden;
-        uint8_t* q = a.out + row0 * a.hidden + col0 + 8 * c;
+    auto cast = [&](auto whole, int64_t col0) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const bool col_ok = WHOLE || col0 + 8 * c < a.hidden;
+        uint8_t* q = q0 + col0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; ++i, q += q_step) {
             const int r = rg + 16 * i;
             uint2 q8;
             if constexpr (WEIGHTED) {
@@ -101,42 +112,51 @@ __global__ void __launch_bounds__(kCastThreads, 4)
                 most = dev::absmax_pair(most, v[i].w);
                 q8 = dev::cast8<FMT>(v[i], scale);
             }
-            if (col_ok && row0 + r < a.rows) __stcs(reinterpret_cast<uint2*>(q + r * a.hidden), q8);
+            if (WHOLE || (col_ok && row0 + r < a.rows)) __stcs(reinterpret_cast<uint2*>(q), q8);
             if constexpr (TRANSPOSE)
                 *reinterpret_cast<uint2*>(sq + r * 128 + ((2 * c) ^ dev::swz(r)) * 4) = q8;
         }
-        const bool more = ct + 1 < last;
+    };
+    auto is_whole = [&](int ct) { return whole_rows && int64_t(ct + 1) * 128 <= a.hidden; };
+    auto load_tile = [&](int ct) {
+        if (is_whole(ct))
+            load(std::true_type{}, int64_t(ct) * 128);
+        else
+            load(std::false_type{}, int64_t(ct) * 128);
+    };
+    const int first = strip * kStripTiles, last = min(first + kStripTiles, tile_cols);
+    load_tile(first);
+    for (int ct = first; ct < last; ++ct) {
+        const int64_t col0 = int64_t(ct) * 128;
+        const bool whole = is_whole(ct), more = ct + 1 < last;
+        if (whole)
+            cast(std::true_type{}, col0);
+        else
+            cast(std::false_type{}, col0);
         if constexpr (!TRANSPOSE) {
-            if (more) load(col0 + 128);
+            if (more) load_tile(ct + 1);
         } else {
             __syncthreads();
-            // rows 16b .. 16b+15 of the four columns of word w
-            const int b = lane & 7, w = warp * 4 + (lane >> 3);
             const uint32_t* sq32 = reinterpret_cast<const uint32_t*>(sq);
             uint32_t in[16], o[4][4];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const int r = 16 * b + j;
-                in[j] = sq32[r * 32 + (w ^ dev::swz(r))];
+                in[j] = sq32[r * 32 + (w4 ^ dev::swz(r))];
             }
             if (more) {
-                load(col0 + 128);
+                load_tile(ct + 1);
                 __syncthreads();   // the copy has been read: the next tile may overwrite it
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 dev::transpose4x4(in[4 * g], in[4 * g + 1], in[4 * g + 2], in[4 * g + 3], o[0][g],
                                   o[1][g], o[2][g], o[3][g]);
-            const int64_t row = row0 + 16 * b;
-            if (row < a.rows) {
+            uint8_t* t = t0 + col0 * a.rows;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int64_t col = col0 + 4 * w + k;
-                    if (col < a.hidden)
-                        __stcs(reinterpret_cast<uint4*>(a.out_t + col * a.rows + row),
-                               make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]));
-                }
-            }
+            for (int k = 0; k < 4; ++k, t += a.rows)
+                if (whole || (row0 + 16 * b < a.rows && col0 + 4 * w4 + k < a.hidden))
+                    __stcs(reinterpret_cast<uint4*>(t), make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]));
         }
     }
     most = __reduce_max_sync(0xFFFFFFFFu, WEIGHTED ? most : dev::pair_to_f32_bits(most));
