@@ -360,16 +360,16 @@ __global__ void __launch_bounds__(kMoveThreads)
 constexpr int kSlotGroup = 4;
 
 // Calls f(cols) for the block's threads' groups of eight columns.
-template <bool VEC, typename F>
+template <int G, typename F>
 __device__ __forceinline__ void each_cols(int H, F&& f) {
-    const int threads = blockDim.x;
-    for (int v = threadIdx.x; v / threads * threads * 8 < H; v += threads) {
-        const dev::Cols<VEC> cols(v, threads, H);
-        if (cols.any()) f(cols);
+    for (int v = threadIdx.x;; v += blockDim.x) {
+        const dev::Cols<G> cols(v, H);
+        if (!cols.any()) break;      // later items begin later
+        f(cols);
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, int G>
 __global__ void __launch_bounds__(kMoveThreads) moe_combine_kernel(MoveArgs a) {
     __shared__ int rows[kMaxSlots];
     pdl_launch_dependents();
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kMoveThreads) moe_combine_kernel(MoveArgs a) {
     const T* ys = static_cast<const T*>(a.ys);
     const float* weights = a.weights ? a.weights + t * a.topk : nullptr;
     token_rows(a, t, rows);
-    each_cols<VEC>(static_cast<int>(a.hidden), [&](const dev::Cols<VEC>& cols) {
+    each_cols<G>(static_cast<int>(a.hidden), [&](const dev::Cols<G>& cols) {
         float sum[8] = {};
         for (int k0 = 0; k0 < a.topk; k0 += kSlotGroup) {
             float f[kSlotGroup][8], w[kSlotGroup];
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kMoveThreads) moe_combine_kernel(MoveArgs a) {
                 // a slot that is dropped takes no part, whatever its weight
                 w[i] = r >= 0 ? (weights ? weights[k0 + i] : 1.0f) : 0.0f;
                 if (r >= 0) {
-                    dev::load_cols<VEC>(ys + r * a.hidden, cols, f[i]);
+                    dev::load_cols<G>(ys + r * a.hidden, cols, f[i]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
@@ -400,11 +400,11 @@ __global__ void __launch_bounds__(kMoveThreads) moe_combine_kernel(MoveArgs a) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] = fmaf(w[i], f[i][j], sum[j]);
         }
-        dev::store_cols<VEC>(static_cast<T*>(a.out) + t * a.hidden, cols, sum);
+        dev::store_cols<G>(static_cast<T*>(a.out) + t * a.hidden, cols, sum);
     });
 }
 
-template <typename T, bool VEC>
+template <typename T, int G>
 __global__ void __launch_bounds__(kMoveThreads) moe_combine_backward_kernel(MoveArgs a, int pad_blocks) {
     __shared__ int rows[kMaxSlots];
     __shared__ float4 slots[2][kMoveThreads / 32];
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kMoveThreads) moe_combine_backward_kernel(Move
     if (a.noop && *a.noop != 0.0f) return;
     const int H = static_cast<int>(a.hidden);
     if (blockIdx.x < pad_blocks) {
-        if (VEC)
+        if constexpr (G == 8)
             clear_padding<uint4>(a, a.hidden * sizeof(T) / 16);
         else
             clear_padding<T>(a, H);
@@ -434,14 +434,14 @@ __global__ void __launch_bounds__(kMoveThreads) moe_combine_backward_kernel(Move
             r[i] = k0 + i < a.topk ? rows[k0 + i] : -1;
             w[i] = dys && r[i] >= 0 ? a.weights[t * a.topk + k0 + i] : 0.0f;
         }
-        each_cols<VEC>(H, [&](const dev::Cols<VEC>& cols) {
+        each_cols<G>(H, [&](const dev::Cols<G>& cols) {
             float g[8], f[kSlotGroup][8];
-            dev::load_cols<VEC>(dout, cols, g);
+            dev::load_cols<G>(dout, cols, g);
             if (a.dweights) {
 #pragma unroll
                 for (int i = 0; i < kSlotGroup; ++i) {
                     if (r[i] >= 0) {
-                        dev::load_cols<VEC>(ys + r[i] * a.hidden, cols, f[i]);
+                        dev::load_cols<G>(ys + r[i] * a.hidden, cols, f[i]);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kMoveThreads) moe_combine_backward_kernel(Move
                     float d[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) d[j] = w[i] * g[j];
-                    dev::store_cols<VEC>(dys + r[i] * a.hidden, cols, d);
+                    dev::store_cols<G>(dys + r[i] * a.hidden, cols, d);
                 }
             }
         });
@@ -479,12 +479,17 @@ __global__ void __launch_bounds__(kMoveThreads) moe_combine_backward_kernel(Move
     }
 }
 
-// Rows whose bytes and buffers allow 16-byte vectors.
-bool vectors(const MoveArgs& a) {
-    auto ok = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    return a.hidden * a.elem_bytes % 16 == 0 && a.hidden % 8 == 0 && ok(a.x) && ok(a.ys) &&
-           ok(a.sorted) && ok(a.out);
+// Whether rows and buffers allow accesses of `bytes`.
+bool allow(const MoveArgs& a, int bytes) {
+    auto ok = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    return a.hidden * a.elem_bytes % bytes == 0 && ok(a.x) && ok(a.ys) && ok(a.sorted) && ok(a.out);
 }
+
+bool vectors(const MoveArgs& a) { return a.hidden % 8 == 0 && allow(a, 16); }
+
+// The kernel for the widest groups of columns that rows and buffers allow.
+#define CT_BY_GROUP(kernel, T) \
+    (vectors(a) ? kernel<T, 8> : allow(a, 2 * sizeof(T)) ? kernel<T, 2> : kernel<T, 1>)
 
 int pad_blocks(const MoveArgs& a) {
     return static_cast<int>(a.sorted ? (a.rows + kPadRows - 1) / kPadRows : 0);
@@ -585,13 +590,14 @@ cudaError_t launch_moe_dispatch(const MoveArgs& a, cudaStream_t stream) {
                           ahead);
     };
     if (vectors(a)) return go(uint4{});
-    return a.elem_bytes == 4 ? go(uint32_t{}) : go(uint16_t{});
+    if (allow(a, 8)) return go(uint2{});
+    return allow(a, 4) ? go(uint32_t{}) : go(uint16_t{});
 }
 
 cudaError_t launch_moe_combine(const MoveArgs& a, int dtype, cudaStream_t stream) {
     return by_type(dtype, [&](auto z) {
         using T = decltype(z);
-        auto* kernel = vectors(a) ? moe_combine_kernel<T, true> : moe_combine_kernel<T, false>;
+        auto* kernel = CT_BY_GROUP(moe_combine_kernel, T);
         return launch_pdl(kernel, dim3(static_cast<unsigned>(a.tokens)),
                           move_threads((a.hidden + 7) / 8, 1), 0, stream, a);
     });
@@ -601,8 +607,7 @@ cudaError_t launch_moe_combine_backward(const MoveArgs& a, int dtype, cudaStream
     const int pad = pad_blocks(a);
     return by_type(dtype, [&](auto z) {
         using T = decltype(z);
-        auto* kernel = vectors(a) ? moe_combine_backward_kernel<T, true>
-                                  : moe_combine_backward_kernel<T, false>;
+        auto* kernel = CT_BY_GROUP(moe_combine_backward_kernel, T);
         return launch_pdl(kernel, dim3(static_cast<unsigned>(a.tokens + pad)),
                           move_threads((a.hidden + 7) / 8, 1), 0, stream, a, pad);
     });

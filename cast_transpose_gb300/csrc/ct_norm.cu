@@ -98,24 +98,24 @@ __device__ __forceinline__ void floats(const V8& v, float (&f)[8]) {
 // Columns past the row's end: a vector is read from column 0 instead, so that
 // no load is conditional; what it adds to a sum is dropped by on(), and it is
 // not stored.
-template <bool VEC>
-__device__ __forceinline__ bool on(const dev::Cols<VEC>& c) {
-    return !VEC || c.any();
+template <int G>
+__device__ __forceinline__ bool on(const dev::Cols<G>& c) {
+    return G != 8 || c.any();
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ V8 load_v8(const T* row, const dev::Cols<VEC>& c) {
+template <int G, typename T>
+__device__ __forceinline__ V8 load_v8(const T* row, const dev::Cols<G>& c) {
     float f[8];
-    if constexpr (VEC)
+    if constexpr (G == 8)
         dev::unpack8(dev::load8(row + (c.any() ? c.first : 0)), f);
     else
-        dev::load_cols<VEC>(row, c, f);
+        dev::load_cols<G>(row, c, f);
     return pairs(f);
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_v8(T* row, const dev::Cols<VEC>& c, const V8& v) {
+template <int G, typename T>
+__device__ __forceinline__ void store_v8(T* row, const dev::Cols<G>& c, const V8& v) {
     float f[8];
     floats(v, f);
-    dev::store_cols<VEC>(row, c, f);
+    dev::store_cols<G>(row, c, f);
 }
 
 // ---- parameters ------------------------------------------------------------
@@ -128,26 +128,26 @@ __device__ __forceinline__ void set_param(void* p, int f32, int64_t i, float v) 
 }
 
 // offset + w of the thread's columns; 1 without a weight.
-template <typename T, bool VEC>
+template <typename T, int G>
 __device__ __forceinline__ void load_param(const void* p, int f32, int64_t at, float offset,
-                                           const dev::Cols<VEC>& c, float (&f)[8]) {
+                                           const dev::Cols<G>& c, float (&f)[8]) {
     if (!p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = 1.0f;
         return;
     }
     if (f32)
-        dev::load_cols<VEC>(static_cast<const float*>(p) + at, c, f);
+        dev::load_cols<G>(static_cast<const float*>(p) + at, c, f);
     else
-        dev::load_cols<VEC>(static_cast<const T*>(p) + at, c, f);
+        dev::load_cols<G>(static_cast<const T*>(p) + at, c, f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] += offset;
 }
 
 // alpha * gate * a(w_post): what the normed u is multiplied by.
-template <typename T, bool VEC, typename Args>
+template <typename T, int G, typename Args>
 __device__ __forceinline__ void branch_factor(const Args& a, int64_t gate_row, int col0,
-                                              const dev::Cols<VEC>& c, float (&f)[8]) {
+                                              const dev::Cols<G>& c, float (&f)[8]) {
     float w[8];
     load_param<T>(a.gate, a.param_f32, gate_row * a.hidden + col0, 0.0f, c, f);
     load_param<T>(a.post ? a.w_post : nullptr, a.param_f32, col0, a.weight_offset, c, w);
@@ -272,7 +272,7 @@ __device__ __forceinline__ float lanes_sum(uint64_t v) {
 // ---- rows ------------------------------------------------------------------
 // A ring of stages that hold one row's slices of one or two tensors, one after
 // the other.  Thread 0 issues the copies; everyone waits on the stage's
-// barrier.  Without VEC a slice is copied as the aligned 16-byte blocks that
+// barrier.  With G = 1 a slice is copied as the aligned 16-byte blocks that
 // cover it, and lies (address mod 16) bytes into its place.
 //
 // A launch has two: the leading ring for what a row's first sum needs, which
@@ -321,14 +321,14 @@ struct Ring {
 };
 
 // Bytes of a tensor's place in a stage.
-template <bool VEC, typename T>
+template <int G, typename T>
 __host__ __device__ constexpr uint32_t place_bytes(int width) {
-    return width * sizeof(T) + (VEC ? 0 : 32);
+    return width * sizeof(T) + (G == 8 ? 0 : 32);
 }
 
 // Eight FP8 codes of y * scale.
-template <bool VEC>
-__device__ __forceinline__ void store_fp8(uint8_t* row, const dev::Cols<VEC>& c,
+template <int G>
+__device__ __forceinline__ void store_fp8(uint8_t* row, const dev::Cols<G>& c,
                                           const float (&y)[8], float scale, int fmt) {
     uint32_t h[4];
 #pragma unroll
@@ -336,7 +336,7 @@ __device__ __forceinline__ void store_fp8(uint8_t* row, const dev::Cols<VEC>& c,
         const float lo = __fmul_rn(y[2 * j], scale), hi = __fmul_rn(y[2 * j + 1], scale);
         h[j] = fmt == 0 ? dev::cvt_fp8x2<0>(lo, hi) : dev::cvt_fp8x2<1>(lo, hi);
     }
-    if constexpr (VEC) {
+    if constexpr (G == 8) {
         if (c.any())
             *reinterpret_cast<uint2*>(row + c.first) =
                 make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
@@ -348,20 +348,20 @@ __device__ __forceinline__ void store_fp8(uint8_t* row, const dev::Cols<VEC>& c,
 }
 
 
-// Without VEC the 16-byte blocks that cover a row's slice may begin or end up
+// With G = 1 the 16-byte blocks that cover a row's slice may begin or end up
 // to 15 bytes outside it: rows that near to the tensors' ends are read from
 // global memory instead.
-template <bool VEC>
+template <int G>
 __device__ __forceinline__ bool in_ring(int64_t row, int64_t rows, int H) {
-    return VEC || (row * H >= 8 && (rows - 1 - row) * H >= 8);   // of two bytes at least
+    return G == 8 || (row * H >= 8 && (rows - 1 - row) * H >= 8);   // of two bytes at least
 }
 
 // Where a row's slice is read from: its place in a stage, or itself.
-template <bool RING, bool VEC, typename T>
+template <bool RING, int G, typename T>
 __device__ __forceinline__ const T* row_at(const uint8_t* stage, uint32_t offset, const T* global, bool staged) {
-    if (!RING || (!VEC && !staged)) return global;
+    if (!RING || (G != 8 && !staged)) return global;
     stage += offset;
-    if (!VEC) stage += reinterpret_cast<uintptr_t>(global) & 15;
+    if (G != 8) stage += reinterpret_cast<uintptr_t>(global) & 15;
     return reinterpret_cast<const T*>(stage);
 }
 
@@ -373,7 +373,7 @@ __device__ __forceinline__ const T* row_at(const uint8_t* stage, uint32_t offset
 
 // Forward.  Per row: sum u^2 -> rstd_post; res_out and sum res_out^2 ->
 // rstd_pre; y.
-template <typename T, typename R, bool VEC, bool RING, bool FULL>
+template <typename T, typename R, int G, bool RING, bool FULL>
 __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const NormArgs a,
                                                                     const NormShape s) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -384,13 +384,13 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     const int tid = threadIdx.x, H = a.hidden;
     const int rank = blockIdx.x % s.cluster, run = blockIdx.x / s.cluster;
     const int col0 = rank * s.width, W = min(s.width, H - col0);
-    auto cols = [&](int p) { return dev::Cols<VEC>(p * blockDim.x + tid, blockDim.x, W); };
+    auto cols = [&](int p) { return dev::Cols<G>(p * blockDim.x + tid, W); };
     const int64_t begin = run_begin(a.rows, run, s.clusters), end = run_begin(a.rows, run + 1, s.clusters);
     const T* u = static_cast<const T*>(a.u) + col0;
     const R* res = static_cast<const R*>(a.res) + col0;
-    Ring lead{full, smem, place_bytes<VEC, T>(s.width), s.lead};                  // u
+    Ring lead{full, smem, place_bytes<G, T>(s.width), s.lead};                  // u
     Ring trail{full + kMaxStages, smem + lead.stages * lead.stage_bytes,
-               place_bytes<VEC, R>(s.width), s.trail};                                  // res
+               place_bytes<G, R>(s.width), s.trail};                                  // res
     bool lost = false;       // a wait gave up: no more waiting, the error is reported
     const Own own{reinterpret_cast<float4*>(RING ? trail.base + trail.stages * trail.stage_bytes : smem)};
     RowSums sums{slots, full + 2 * kMaxStages, s.cluster, rank};
@@ -408,11 +408,11 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     auto fetch_lead = [&](int64_t row, int to) {
-        const bool staged = has_u && in_ring<VEC>(row, a.rows, H);
+        const bool staged = has_u && in_ring<G>(row, a.rows, H);
         lead.fetch(to, staged ? u + row * H : nullptr, W * sizeof(T), 0, nullptr, 0);
     };
     auto fetch_trail = [&](int64_t row, int to) {
-        trail.fetch(to, in_ring<VEC>(row, a.rows, H) ? res + row * H : nullptr, W * sizeof(R), 0, nullptr, 0);
+        trail.fetch(to, in_ring<G>(row, a.rows, H) ? res + row * H : nullptr, W * sizeof(R), 0, nullptr, 0);
     };
     if constexpr (RING)
         if (tid == 0)
@@ -446,12 +446,12 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
             if (RING) lead.next();
             return 0.0f;
         }
-        const T* x = row_at<RING, VEC>(lead.at(), 0, u + row * H, in_ring<VEC>(row, a.rows, H));
+        const T* x = row_at<RING, G>(lead.at(), 0, u + row * H, in_ring<G>(row, a.rows, H));
         if (RING) lead.next();
         float sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const V8 v = load_v8<VEC>(x, cols(p));
+            const V8 v = load_v8<G>(x, cols(p));
             uint64_t part = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) part = fma2(v.p[j], v.p[j], part);
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     int u_stage = 0;        // the stage of this row's u: the leading ring itself is rows ahead
     for (int64_t row = begin; row < end; ++row) {
         const int64_t at = row * H;
-        const bool staged = in_ring<VEC>(row, a.rows, H);
+        const bool staged = in_ring<G>(row, a.rows, H);
         if (has_u && row == gate_end) {
             gate_end += a.rows_per_gate;
             ++gate_row;
@@ -485,18 +485,18 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         V8 v[kPer];
         float sum_v = 0.0f;
         if (RING) trail.wait(lost);
-        const R* r = row_at<RING, VEC>(trail.at(), 0, res + at, staged);
-        const T* x = row_at<RING, VEC>(lead.base + u_stage * lead.stage_bytes, 0, u + at, staged);
+        const R* r = row_at<RING, G>(trail.at(), 0, res + at, staged);
+        const T* x = row_at<RING, G>(lead.base + u_stage * lead.stage_bytes, 0, u + at, staged);
         const uint64_t rstd2 = pair(rstd_u, rstd_u);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            v[p] = load_v8<VEC>(r, cols(p));
+            v[p] = load_v8<G>(r, cols(p));
             if (has_u) {
-                const V8 xv = load_v8<VEC>(x, cols(p)), g = own.get(kBranch, p);
+                const V8 xv = load_v8<G>(x, cols(p)), g = own.get(kBranch, p);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     v[p].p[j] = fma2(mul2(xv.p[j], rstd2), g.p[j], mul2(beta, v[p].p[j]));
-                store_v8<VEC>(static_cast<R*>(a.res_out) + at + col0, cols(p), v[p]);
+                store_v8<G>(static_cast<R*>(a.res_out) + at + col0, cols(p), v[p]);
             }
             uint64_t part = 0;
 #pragma unroll
@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (on(cols(p))) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-                store_fp8<VEC>(static_cast<uint8_t*>(a.y) + at + col0, cols(p), f, scale, a.fmt);
+                store_fp8<G>(static_cast<uint8_t*>(a.y) + at + col0, cols(p), f, scale, a.fmt);
             } else {
-                store_v8<VEC>(static_cast<T*>(a.y) + at + col0, cols(p), v[p]);
+                store_v8<G>(static_cast<T*>(a.y) + at + col0, cols(p), v[p]);
             }
         }
     }
@@ -565,7 +565,7 @@ enum { kSumPre, kSumPost, kSumGateFirst, kSumGateLast, kSums };
 //   P  = alpha gate a_post D                           du = rstd_post (P - uh mean(P uh))
 //   dw_pre = sum dy xh
 //   S  = sum D uh over a gate row's rows: dgate = alpha a_post S, dw_post = sum alpha gate S
-template <typename T, typename R, bool VEC, bool RING, bool FULL>
+template <typename T, typename R, int G, bool RING, bool FULL>
 __global__ void __launch_bounds__(kBackwardThreads, 1)
     block_norm_backward_kernel(const NormBackwardArgs a, const NormShape s) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -576,11 +576,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     const int tid = threadIdx.x, H = a.hidden;
     const int rank = blockIdx.x % s.cluster, run = blockIdx.x / s.cluster;
     const int col0 = rank * s.width, W = min(s.width, H - col0);
-    auto cols = [&](int p) { return dev::Cols<VEC>(p * blockDim.x + tid, blockDim.x, W); };
+    auto cols = [&](int p) { return dev::Cols<G>(p * blockDim.x + tid, W); };
     const int64_t begin = run_begin(a.rows, run, s.clusters), end = run_begin(a.rows, run + 1, s.clusters);
     constexpr uint32_t kT = sizeof(T), kR = sizeof(R);
-    const uint32_t second = place_bytes<VEC, R>(s.width);    // in a stage: of type R, then of type T
-    const uint32_t stage_bytes = second + place_bytes<VEC, T>(s.width);
+    const uint32_t second = place_bytes<G, R>(s.width);    // in a stage: of type R, then of type T
+    const uint32_t stage_bytes = second + place_bytes<G, T>(s.width);
     Ring lead{full, smem, stage_bytes, s.lead};        // res_out, dy
     Ring trail{full + kMaxStages, smem + lead.stages * stage_bytes, stage_bytes, s.trail};   // dres_out, u
     bool lost = false;
@@ -603,11 +603,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     auto fetch_lead = [&](int64_t row, int to) {
-        const bool staged = pre && in_ring<VEC>(row, a.rows, H);
+        const bool staged = pre && in_ring<G>(row, a.rows, H);
         lead.fetch(to, staged ? res_out + row * H : nullptr, W * kR, second, staged ? dy + row * H : nullptr, W * kT);
     };
     auto fetch_trail = [&](int64_t row, int to) {
-        const bool staged = in_ring<VEC>(row, a.rows, H);
+        const bool staged = in_ring<G>(row, a.rows, H);
         trail.fetch(to, staged && has_dres ? dres_out + row * H : nullptr, W * kR, second,
                     staged && has_u ? u + row * H : nullptr, W * kT);
     };
@@ -643,15 +643,15 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         const uint8_t* stage = lead.at();
         if (RING) lead.next();
         if (!pre) return 0.0f;
-        const bool staged = in_ring<VEC>(row, a.rows, H);
-        const T* g = row_at<RING, VEC>(stage, second, dy + row * H, staged);
-        const R* x = row_at<RING, VEC>(stage, 0, res_out + row * H, staged);
+        const bool staged = in_ring<G>(row, a.rows, H);
+        const T* g = row_at<RING, G>(stage, second, dy + row * H, staged);
+        const R* x = row_at<RING, G>(stage, 0, res_out + row * H, staged);
         const uint64_t rstd2 = pair(rstd, rstd);
         float sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
             uint64_t part = 0;
-            const V8 gv = load_v8<VEC>(g, cols(p)), xv = load_v8<VEC>(x, cols(p)), w = own.get(kPre, p);
+            const V8 gv = load_v8<G>(g, cols(p)), xv = load_v8<G>(x, cols(p)), w = own.get(kPre, p);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint64_t t = mul2(gv.p[j], xv.p[j]);
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             (int64_t(gate_row == first_gate ? kSumGateFirst : kSumGateLast) * s.clusters + run) * H + col0;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const dev::Cols<VEC> c = cols(p);
+            const dev::Cols<G> c = cols(p);
             float f[8], w[8];
             floats(dots[p], f);
             dots[p] = V8{};
@@ -680,11 +680,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             for (int j = 0; j < 8; ++j) f[j] *= a.branch_scale;
             if (a.dw_post) {
                 float sum[8] = {};
-                if (gate_row != first_gate) dev::load_cols<VEC>(post_sums, c, sum);
+                if (gate_row != first_gate) dev::load_cols<G>(post_sums, c, sum);
                 load_param<T>(a.gate, a.param_f32, gate_row * H + col0, 0.0f, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] = fmaf(w[j], f[j], sum[j]);
-                dev::store_cols<VEC>(post_sums, c, sum);
+                dev::store_cols<G>(post_sums, c, sum);
             }
             if (a.dgate) {
                 load_param<T>(post ? a.w_post : nullptr, a.param_f32, col0, a.weight_offset, c, w);
@@ -692,11 +692,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
                 for (int j = 0; j < 8; ++j) f[j] *= w[j];
                 const int64_t at = gate_row * H + col0;
                 if (!whole)
-                    dev::store_cols<VEC>(gate_sums, c, f);
+                    dev::store_cols<G>(gate_sums, c, f);
                 else if (a.param_f32)
-                    dev::store_cols<VEC>(static_cast<float*>(a.dgate) + at, c, f);
+                    dev::store_cols<G>(static_cast<float*>(a.dgate) + at, c, f);
                 else
-                    dev::store_cols<VEC>(static_cast<T*>(a.dgate) + at, c, f);
+                    dev::store_cols<G>(static_cast<T*>(a.dgate) + at, c, f);
             }
         }
     };
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     int x_stage = 0;        // the stage of this row's res_out: the leading ring itself is rows ahead
     for (int64_t row = begin; row < end; ++row) {
         const int64_t at = row * H;
-        const bool staged = in_ring<VEC>(row, a.rows, H);
+        const bool staged = in_ring<G>(row, a.rows, H);
         const float far_x = rstd_at(pre, a.rstd_pre, row + 2, 0.0f);
         const float next_u = rstd_at(post, a.rstd_post, row + 1, 1.0f);
         if (has_u && row == gate_end) {
@@ -737,18 +737,18 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         float sum_p = 0.0f;
         if (RING) trail.wait(lost);
         const uint8_t* stage = lead.base + x_stage * stage_bytes;
-        const R* x = row_at<RING, VEC>(stage, 0, res_out + at, staged);
-        const T* g = row_at<RING, VEC>(stage, second, dy + at, staged);
-        const R* r = row_at<RING, VEC>(trail.at(), 0, dres_out + at, staged);
-        const T* y = row_at<RING, VEC>(trail.at(), second, u + at, staged);
+        const R* x = row_at<RING, G>(stage, 0, res_out + at, staged);
+        const T* g = row_at<RING, G>(stage, second, dy + at, staged);
+        const R* r = row_at<RING, G>(trail.at(), 0, dres_out + at, staged);
+        const T* y = row_at<RING, G>(trail.at(), second, u + at, staged);
         const float back1 = -rstd_x * rstd_x * mean_x;
         const uint64_t back = pair(back1, back1), rx2 = pair(rstd_x, rstd_x), ru2 = pair(rstd_u, rstd_u);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
             V8 d = {};
-            if (has_dres) d = load_v8<VEC>(r, cols(p));
+            if (has_dres) d = load_v8<G>(r, cols(p));
             if (pre) {
-                const V8 gv = load_v8<VEC>(g, cols(p)), xv = load_v8<VEC>(x, cols(p)), w = own.get(kPre, p);
+                const V8 gv = load_v8<G>(g, cols(p)), xv = load_v8<G>(x, cols(p)), w = own.get(kPre, p);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     d.p[j] = fma2(xv.p[j], back, fma2(mul2(gv.p[j], rx2), w.p[j], d.p[j]));
@@ -756,9 +756,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             V8 out;
 #pragma unroll
             for (int j = 0; j < 4; ++j) out.p[j] = mul2(beta, d.p[j]);
-            store_v8<VEC>(static_cast<R*>(a.dres) + at + col0, cols(p), out);
+            store_v8<G>(static_cast<R*>(a.dres) + at + col0, cols(p), out);
             if (has_u) {
-                hat[p] = load_v8<VEC>(y, cols(p));
+                hat[p] = load_v8<G>(y, cols(p));
                 branch[p] = own.get(kBranch, p);
                 uint64_t part = 0;
 #pragma unroll
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     branch[p].p[j] = mul2(ru2, fma2(hat[p].p[j], mean2, branch[p].p[j]));
-                store_v8<VEC>(static_cast<T*>(a.du) + at + col0, cols(p), branch[p]);
+                store_v8<G>(static_cast<T*>(a.du) + at + col0, cols(p), branch[p]);
             }
         }
         mean_x = sum.x * per_column;
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     if (a.dw_pre) {
         float* part = a.workspace + (int64_t(kSumPre) * s.clusters + run) * H + col0;
 #pragma unroll
-        for (int p = 0; p < kPer; ++p) store_v8<VEC>(part, cols(p), dw_pre[p]);
+        for (int p = 0; p < kPer; ++p) store_v8<G>(part, cols(p), dw_pre[p]);
     }
     if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
     if (s.cluster > 1) sums.meet();
@@ -1040,11 +1040,11 @@ cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaS
         NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, vec, kForwardThreads,
                                      2 * kForwardThreads, &smem);
         const bool full = a.u && a.post && a.pre;
-        auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, true, true, true>
-                                               : block_norm_kernel<T, R, true, true, false>)
-                                       : block_norm_kernel<T, R, false, true, false>)
-                                : (vec ? block_norm_kernel<T, R, true, false, false>
-                                       : block_norm_kernel<T, R, false, false, false>);
+        auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, 8, true, true>
+                                               : block_norm_kernel<T, R, 8, true, false>)
+                                       : block_norm_kernel<T, R, 1, true, false>)
+                                : (vec ? block_norm_kernel<T, R, 8, false, false>
+                                       : block_norm_kernel<T, R, 1, false, false>);
         const cudaError_t e = prepare(reinterpret_cast<const void*>(kernel), s, smem);
         return e != cudaSuccess ? e : launch_rows(kernel, a, s, smem, stream);
     });
@@ -1068,11 +1068,11 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
         s.clusters = static_cast<int>(std::min<int64_t>(s.clusters, max_clusters(a.rows, a.hidden)));
         if (a.rows > 0) {
             const bool full = a.u && a.post && a.pre && a.dres_out;
-            auto* kernel = s.lead ? (vec ? (full ? block_norm_backward_kernel<T, R, true, true, true>
-                                                   : block_norm_backward_kernel<T, R, true, true, false>)
-                                           : block_norm_backward_kernel<T, R, false, true, false>)
-                                    : (vec ? block_norm_backward_kernel<T, R, true, false, false>
-                                           : block_norm_backward_kernel<T, R, false, false, false>);
+            auto* kernel = s.lead ? (vec ? (full ? block_norm_backward_kernel<T, R, 8, true, true>
+                                                   : block_norm_backward_kernel<T, R, 8, true, false>)
+                                           : block_norm_backward_kernel<T, R, 1, true, false>)
+                                    : (vec ? block_norm_backward_kernel<T, R, 8, false, false>
+                                           : block_norm_backward_kernel<T, R, 1, false, false>);
             cudaError_t e = prepare(reinterpret_cast<const void*>(kernel), s, smem);
             if (e == cudaSuccess) e = launch_rows(kernel, a, s, smem, stream);
             if (e != cudaSuccess) return e;

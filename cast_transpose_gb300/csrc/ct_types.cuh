@@ -94,50 +94,86 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
     for (int i = 0; i < int(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
 }
 
-// The eight columns a thread holds of a row of H.  VEC: the consecutive ones
-// of vector `vi` (H % 8 == 0, rows 16-byte aligned).  Otherwise, for any H and
-// alignment, eight columns `step` apart, so that a warp's threads stay on
-// neighbouring elements.
-template <bool VEC>
+// The eight columns of item `vi` of a row of H, in groups of G neighbours.
+// G = 8: one 16-byte vector of two-byte elements (H % 8 == 0, rows 16-byte
+// aligned).  Otherwise 32 items, a warp's, share 256 columns, each group 32 * G
+// columns after the one before: a warp's accesses are consecutive and their
+// offsets constants.  G = 2: pairs (H even, rows aligned for them); G = 1: any
+// H and alignment.
+template <int G>
 struct Cols {
-    int first, step, H;
-    __device__ __forceinline__ Cols(int vi, int threads, int H_) : H(H_) {
-        if (VEC) {
-            first = vi * 8;
-            step = 1;
-        } else {
-            first = (vi / threads) * threads * 8 + vi % threads;
-            step = threads;
-        }
+    static constexpr int kStep = 32 * G;
+    int first, H;
+    __device__ __forceinline__ Cols(int vi, int H_) : H(H_) {
+        first = G == 8 ? vi * 8 : (vi >> 5) * 256 + (vi & 31) * G;
     }
-    __device__ __forceinline__ int at(int j) const { return first + j * step; }
+    __device__ __forceinline__ int at(int j) const { return G == 8 ? first + j : first + j / G * kStep + j % G; }
     __device__ __forceinline__ bool any() const { return first < H; }
-    __device__ __forceinline__ bool has(int j) const { return VEC ? first < H : at(j) < H; }
+    __device__ __forceinline__ bool has(int j) const { return G == 8 ? first < H : at(j) < H; }
+    __device__ __forceinline__ bool all() const { return G == 8 ? first < H : at(7) < H; }
 };
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_cols(const T* row, const Cols<VEC>& c, float (&f)[8]) {
-    if constexpr (VEC) {
+template <typename T>
+struct Pair {
+    T x, y;
+};
+template <>
+struct __align__(4) Pair<__nv_bfloat16> {
+    __nv_bfloat16 x, y;
+};
+template <>
+struct __align__(4) Pair<__half> {
+    __half x, y;
+};
+template <>
+struct __align__(8) Pair<float> {
+    float x, y;
+};
+
+template <int G, typename T>
+__device__ __forceinline__ void load_cols(const T* row, const Cols<G>& c, float (&f)[8]) {
+    if constexpr (G == 8) {
         if (c.any()) {
             unpack8(load8(row + c.first), f);
             return;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    } else {
+    } else if constexpr (G == 2) {
+        const Pair<T>* p = reinterpret_cast<const Pair<T>*>(row + c.first);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = c.has(j) ? to_f32(row[c.at(j)]) : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            const bool some = c.has(2 * j);
+            Pair<T> v;
+            if (some) v = p[32 * j];
+            f[2 * j] = some ? to_f32(v.x) : 0.0f;
+            f[2 * j + 1] = some ? to_f32(v.y) : 0.0f;
+        }
+    } else {
+        const T* p = row + c.first;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = c.has(j) ? to_f32(p[32 * j]) : 0.0f;
     }
 }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_cols(T* row, const Cols<VEC>& c, const float (&f)[8]) {
-    if constexpr (VEC) {
+template <int G, typename T>
+__device__ __forceinline__ void store_cols(T* row, const Cols<G>& c, const float (&f)[8]) {
+    if constexpr (G == 8) {
         if (c.any()) store8(row + c.first, f);
+    } else if constexpr (G == 2) {
+        Pair<T>* p = reinterpret_cast<Pair<T>*>(row + c.first);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            Pair<T> v;
+            from_f32(v.x, f[2 * j]);
+            from_f32(v.y, f[2 * j + 1]);
+            if (c.has(2 * j)) p[32 * j] = v;
+        }
     } else {
+        T* p = row + c.first;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (c.has(j)) from_f32(row[c.at(j)], f[j]);
+            if (c.has(j)) from_f32(p[32 * j], f[j]);
     }
 }
 
