@@ -2,6 +2,7 @@
 // transposed in one pass: q[r] = fp8(w[s] * x[s / K] * scale), s = src[r].
 #include "ct_device.cuh"
 #include "ct_ops.h"
+#include "ct_types.cuh"
 
 #include <type_traits>
 
@@ -170,9 +171,9 @@ __global__ void __launch_bounds__(kCastThreads, 4)
     }
 }
 
-// Any shape and alignment, element by element, without the transpose: one
-// block per sorted row.
-template <int FMT>
+// Any shape and alignment, without the transpose: one block per sorted row.
+// G = 2: columns in pairs (hidden even, x 4-byte and out 2-byte aligned).
+template <int FMT, int G>
 __global__ void __launch_bounds__(kCastThreads) sorted_cast_any_kernel(const SortedCastArgs a) {
     __shared__ unsigned warp_max[kCastThreads / 32];
     dev::pdl_launch_dependents();
@@ -184,15 +185,32 @@ __global__ void __launch_bounds__(kCastThreads) sorted_cast_any_kernel(const Sor
     float w;
     const int t = token_of(a, row, w);
     unsigned most = 0;
-    for (int c = tid; c < a.hidden; c += kCastThreads) {
-        float v = 0.0f;
+    for (int item = tid;; item += kCastThreads) {
+        const dev::Cols<G> c(item, static_cast<int>(a.hidden));
+        if (!c.any()) break;
+        float f[8];
         if (t >= 0) {
-            v = __uint_as_float(uint32_t(a.x[t * a.hidden + c]) << 16);
-            if (a.weights) v = __fmul_rn(w, v);
-            most = max_bits(most, v);
+            dev::load_cols<G>(reinterpret_cast<const __nv_bfloat16*>(a.x) + t * a.hidden, c, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (a.weights) f[j] = __fmul_rn(w, f[j]);
+                if (c.has(j)) most = max_bits(most, f[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
         }
-        a.out[row * a.hidden + c] =
-            static_cast<uint8_t>(dev::cvt_fp8x2<FMT>(__fmul_rn(v, scale), 0.0f));
+        uint8_t* q = a.out + row * a.hidden;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const uint32_t two = dev::cvt_fp8x2<FMT>(__fmul_rn(f[j], scale), __fmul_rn(f[j + 1], scale));
+            if constexpr (G == 2) {
+                if (c.has(j)) *reinterpret_cast<uint16_t*>(q + c.at(j)) = static_cast<uint16_t>(two);
+            } else {
+                if (c.has(j)) q[c.at(j)] = static_cast<uint8_t>(two);
+                if (c.has(j + 1)) q[c.at(j + 1)] = static_cast<uint8_t>(two >> 8);
+            }
+        }
     }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if ((tid & 31) == 0) warp_max[tid >> 5] = most;
@@ -223,8 +241,10 @@ cudaError_t launch_fmt(const SortedCastArgs& a, cudaStream_t stream) {
                                              : sorted_cast_kernel<FMT, false, false>);
         e = launch_pdl(kernel, grid, dim3(kCastThreads), 0, stream, a, tile_rows, tile_cols);
     } else {
-        e = launch_pdl(sorted_cast_any_kernel<FMT>, dim3(static_cast<unsigned>(a.rows)),
-                       dim3(kCastThreads), 0, stream, a);
+        const bool pairs = a.hidden % 2 == 0 && reinterpret_cast<uintptr_t>(a.x) % 4 == 0 &&
+                           reinterpret_cast<uintptr_t>(a.out) % 2 == 0;
+        e = launch_pdl(pairs ? sorted_cast_any_kernel<FMT, 2> : sorted_cast_any_kernel<FMT, 1>,
+                       dim3(static_cast<unsigned>(a.rows)), dim3(kCastThreads), 0, stream, a);
     }
     if (e != cudaSuccess || !a.out_t || together) return e;
     // rows that are no multiple of 16, or odd alignments: the byte transpose of
