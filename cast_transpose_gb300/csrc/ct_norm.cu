@@ -37,7 +37,7 @@ constexpr int kPer = 2;               // groups of eight columns per thread
 // 64; backward, 384 with 168, which its column sums and the compiler's room to
 // interleave columns need (8192x6144 bf16, 512 with 128: 109 us, so: 106;
 // 12288x4096: 131, so: 119).
-constexpr int kForwardThreads = 512, kBackwardThreads = 384;
+constexpr int kForwardThreads = 384, kBackwardThreads = 384;
 constexpr int kMaxThreads = kForwardThreads;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = kMaxThreads / 32;
@@ -109,6 +109,12 @@ __device__ __forceinline__ V8 load_v8(const T* row, const dev::Cols<G>& c) {
         dev::unpack8(dev::load8(row + (c.any() ? c.first : 0)), f);
     else
         dev::load_cols<G>(row, c, f);
+    return pairs(f);
+}
+template <typename T>
+__device__ __forceinline__ V8 unpacked(const dev::Raw8<T>& r) {
+    float f[8];
+    dev::unpack8(r, f);
     return pairs(f);
 }
 template <int G, typename T>
@@ -373,9 +379,16 @@ __device__ __forceinline__ const T* row_at(const uint8_t* stage, uint32_t offset
 
 // Forward.  Per row: sum u^2 -> rstd_post; res_out and sum res_out^2 ->
 // rstd_pre; y.
+//
+// KEEP: a row's u stays in registers between its two uses, two rows apart, so
+// that its stage is free for a row on its way (two-byte types: 16 registers).
 template <typename T, typename R, int G, bool RING, bool FULL>
 __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const NormArgs a,
                                                                     const NormShape s) {
+    constexpr bool KEEP = RING && FULL && G == 8 && sizeof(T) == 2;
+    struct Kept {
+        dev::Raw8<T> v[KEEP ? kPer : 1];
+    };
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
     __shared__ __align__(8) uint64_t full[2 * kMaxStages + 2];
@@ -416,8 +429,8 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     };
     if constexpr (RING)
         if (tid == 0)
-            for (int i = 0; i < lead.stages && begin + i < end; ++i) {   // the longer one
-                fetch_lead(begin + i, i);
+            for (int i = 0; i < max(lead.stages, trail.stages) && begin + i < end; ++i) {
+                if (i < lead.stages) fetch_lead(begin + i, i);
                 if (i < trail.stages) fetch_trail(begin + i, i);
             }
     int64_t gate_row = a.gate ? begin / a.rows_per_gate : 0;
@@ -439,8 +452,8 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     const uint64_t beta = pair(a.residual_scale, a.residual_scale);
     unsigned most = 0;
 
-    // sum u^2 of the next row of the leading ring
-    auto sum_u = [&](int64_t row) {
+    // sum u^2 of the next row of the leading ring; KEEP: with the row itself
+    auto sum_u = [&](int64_t row, Kept& kept) {
         if (RING) lead.wait(lost);
         if (!post) {
             if (RING) lead.next();
@@ -451,7 +464,13 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         float sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const V8 v = load_v8<G>(x, cols(p));
+            V8 v;
+            if constexpr (KEEP) {
+                kept.v[p] = dev::load8(x + (cols(p).any() ? cols(p).first : 0));
+                v = unpacked(kept.v[p]);
+            } else {
+                v = load_v8<G>(x, cols(p));
+            }
             uint64_t part = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) part = fma2(v.p[j], v.p[j], part);
@@ -461,14 +480,19 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     };
     const bool writes_rstd = rank == 0 && tid == 0;
     float rstd_u = 1.0f;
-    const float first_sum = sum_u(begin);
+    Kept u_now, u_next;
+    const float first_sum = sum_u(begin, u_now);
+    int u_stage = 0;        // the leading stage that is done with next: this row's, KEEP: the next one's
     if (post) {
         sums.send(first_sum, 0.0f);
         rstd_u = rsqrtf(sums.get(lost).x * per_column + a.eps);
         if (a.rstd_post && writes_rstd) a.rstd_post[begin] = rstd_u;
+        if (KEEP) {
+            if (tid == 0 && begin + lead.stages < end) fetch_lead(begin + lead.stages, u_stage);
+            ++u_stage;
+        }
     }
-    float next_u = begin + 1 < end ? sum_u(begin + 1) : 0.0f;
-    int u_stage = 0;        // the stage of this row's u: the leading ring itself is rows ahead
+    float next_u = begin + 1 < end ? sum_u(begin + 1, u_next) : 0.0f;
     for (int64_t row = begin; row < end; ++row) {
         const int64_t at = row * H;
         const bool staged = in_ring<G>(row, a.rows, H);
@@ -492,7 +516,12 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         for (int p = 0; p < kPer; ++p) {
             v[p] = load_v8<G>(r, cols(p));
             if (has_u) {
-                const V8 xv = load_v8<G>(x, cols(p)), g = own.get(kBranch, p);
+                V8 xv;
+                if constexpr (KEEP)
+                    xv = unpacked(u_now.v[p]);
+                else
+                    xv = load_v8<G>(x, cols(p));
+                const V8 g = own.get(kBranch, p);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     v[p].p[j] = fma2(mul2(xv.p[j], rstd2), g.p[j], mul2(beta, v[p].p[j]));
@@ -504,12 +533,14 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
             sum_v += on(cols(p)) ? lanes_sum(part) : 0.0f;
         }
         sums.send(next_u, sum_v);
-        if (row + 2 < end) next_u = sum_u(row + 2);
+        if constexpr (KEEP) u_now = u_next;
+        if (row + 2 < end) next_u = sum_u(row + 2, u_next);
         const float2 sum = sums.get(lost);
-        // everyone has read this row's stages
+        // everyone has read this row's stages; KEEP: of u, the next row's
         if constexpr (RING) {
             if (tid == 0) {
-                if (row + lead.stages < end) fetch_lead(row + lead.stages, u_stage);
+                const int64_t far = row + lead.stages + (KEEP ? 1 : 0);
+                if (far < end) fetch_lead(far, u_stage);
                 if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
             }
             trail.next();
@@ -613,8 +644,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     };
     if constexpr (RING)
         if (tid == 0)
-            for (int i = 0; i < lead.stages && begin + i < end; ++i) {   // the longer one
-                fetch_lead(begin + i, i);
+            for (int i = 0; i < max(lead.stages, trail.stages) && begin + i < end; ++i) {
+                if (i < lead.stages) fetch_lead(begin + i, i);
                 if (i < trail.stages) fetch_trail(begin + i, i);
             }
     const float beta1 = has_u ? a.residual_scale : 1.0f;
@@ -917,21 +948,22 @@ int64_t max_clusters(int64_t rows, int64_t hidden) {
 
 // Picks the fewest blocks per row whose rings hold enough, then as many blocks
 // per SM as the registers and then the rings allow.  lead_bytes, trail_bytes:
-// of one column in a stage, of `tensors` tensors; max_threads, sm_threads: of
+// of one column in a stage, of `tensors` tensors; min_lead: rows that hold a
+// leading stage at a time; max_threads, sm_threads: of
 // a block, and of those that an SM's registers hold.
-NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, int tensors, bool vec,
-                   int max_threads, int sm_threads, size_t* smem) {
+NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, int tensors, int min_lead,
+                   bool vec, int max_threads, int sm_threads, size_t* smem) {
     NormShape s = {};
     const int pad = vec ? 0 : 32 * tensors;
     auto own = [&] { return kOwnBytes * threads_of(s.width); };
     auto rings = [&](int lead, int trail) {
         return lead * (s.width * lead_bytes + pad) + trail * (s.width * trail_bytes + pad);
     };
-    // Stages for `per_sm` blocks; false with fewer than rows i, i+1 and i+2 in
-    // the leading ring and i and i+1 in the trailing one.
+    // Stages for `per_sm` blocks; false with fewer than the rows that are in use
+    // at a time in the leading ring and two in the trailing one.
     auto fill = [&](int per_sm) {
         const int room = kSmemPerSm / per_sm - kSmemFixed - own();
-        s.lead = 3;
+        s.lead = min_lead;
         s.trail = 2;
         if (rings(s.lead, s.trail) > room) return false;
         for (;;) {
@@ -1037,9 +1069,10 @@ cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaS
         using T = decltype(t);
         using R = decltype(r);
         size_t smem;
-        NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, vec, kForwardThreads,
-                                     2 * kForwardThreads, &smem);
         const bool full = a.u && a.post && a.pre;
+        const int min_lead = full && vec && sizeof(T) == 2 ? 2 : 3;   // rows i+1, i+2, and i unless it is kept
+        NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, min_lead, vec, kForwardThreads,
+                               2 * kForwardThreads, &smem);
         auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, 8, true, true>
                                                : block_norm_kernel<T, R, 8, true, false>)
                                        : block_norm_kernel<T, R, 1, true, false>)
@@ -1063,7 +1096,7 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
         using T = decltype(t);
         using R = decltype(r);
         size_t smem;
-        NormShape s = shape_of(a.rows, a.hidden, sizeof(T) + sizeof(R), sizeof(T) + sizeof(R), 2, vec,
+        NormShape s = shape_of(a.rows, a.hidden, sizeof(T) + sizeof(R), sizeof(T) + sizeof(R), 2, 3, vec,
                                kBackwardThreads, kBackwardThreads, &smem);
         s.clusters = static_cast<int>(std::min<int64_t>(s.clusters, max_clusters(a.rows, a.hidden)));
         if (a.rows > 0) {
