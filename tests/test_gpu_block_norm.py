@@ -331,3 +331,11 @@ def test_offsets_past_32_bits():
     for t, k in ((du[-64:], "du"), (dres[-64:], "dres"), (dw[0], "dw_post"), (dw[1], "dw_pre")):
         ref.close(t, want[k][0], ref.rounded(want[k][0], want[k][1], BF), k)
     assert not du[:-64].any()
+
+
+def test_no_wait_gave_up():
+    """The kernels' bounded waits set a bit of the diagnostic word when they run out."""
+    c = Case(2000, 6144, BF, BF, BF, per_gate=300)
+    c.check_backward()
+    torch.cuda.synchronize()
+    assert ct.device_error() & 1 == 0
