@@ -844,30 +844,33 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
 // Joins the runs' column sums, in run order.  blockIdx.y 0, 1: dw_pre, dw_post;
 // from 2 on the gate rows that more than one run has rows of, by gate row
 // (few of them, perhaps of many runs), else by the run they begin in.
-constexpr int kJoinCols = 32, kJoinRuns = 32;   // threads: columns x at most so many shares of the runs
+//
+// A block takes `cols` columns (32, or 8, one sector, of short rows) and gives each blockDim / cols threads, which add up every so many-th run.
+constexpr int kJoinThreads = 512;      // at most
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinCols * kJoinRuns)
-    block_norm_join_kernel(const NormBackwardArgs a, int64_t runs, int by_gate_row) {
-    __shared__ float parts[kJoinRuns][kJoinCols];
+__global__ void __launch_bounds__(kJoinThreads)
+    block_norm_join_kernel(const NormBackwardArgs a, int64_t runs, int cols, int by_gate_row) {
+    __shared__ float parts[kJoinThreads];
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    const int H = a.hidden, x = threadIdx.x % kJoinCols, y = threadIdx.x / kJoinCols;
-    const int shares = blockDim.x / kJoinCols;
-    const int which = blockIdx.y;
+    const int H = a.hidden, x = threadIdx.x % cols, y = threadIdx.x / cols;
+    const int shares = blockDim.x / cols, which = blockIdx.y;
     int64_t first = 0, last = runs - 1, at = 0;   // the runs to add up
-    int col = blockIdx.x * kJoinCols + x;
+    int col = blockIdx.x * cols + x;
     void* out = which == 0 ? a.dw_pre : which == 1 ? a.dw_post : a.dgate;
-    bool gate_first_is_last = false;
+    if (!out) return;
+    // where the first run's sums are, and the others'
+    int kind_first = which == 0 ? kSumPre : kSumPost, kind = kind_first;
     if (which >= 2) {
         int64_t gate_row;
         if (by_gate_row) {
             gate_row = which - 2;
             first = run_of(a.rows, gate_row * a.rows_per_gate, runs);
         } else {
-            // blockDim.x columns of the gate row that run
-            // `which - 2` ends in, if it begins there
+            // blockDim.x columns of the gate row that run `which - 2` ends in,
+            // if it begins there
             col = blockIdx.x * blockDim.x + threadIdx.x;
             first = which - 2;
             gate_row = (run_begin(a.rows, first + 1, runs) - 1) / a.rows_per_gate;
@@ -876,33 +879,35 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRuns)
         last = run_of(a.rows, min((gate_row + 1) * a.rows_per_gate, a.rows) - 1, runs);
         if (first == last) return;                // written by its run
         at = gate_row * H;
-        gate_first_is_last = run_begin(a.rows, first, runs) / a.rows_per_gate != gate_row;
+        // a gate row is the last one of its first run, unless it is that run's
+        // first one too, and the first one of the others
+        kind = kSumGateFirst;
+        kind_first = run_begin(a.rows, first, runs) / a.rows_per_gate == gate_row ? kSumGateFirst : kSumGateLast;
     }
-    if (!out) return;
-    // the sums of run r: a gate row is the last one of the first run unless it
-    // is its first one too, and the first one of the others
-    auto part = [&](int64_t r) {
-        const int kind = which < 2 ? (which == 0 ? kSumPre : kSumPost)
-                         : r == first && gate_first_is_last ? kSumGateLast : kSumGateFirst;
-        return a.workspace[(int64_t(kind) * runs + r) * H + col];
-    };
+    const float* sums = a.workspace + int64_t(kind) * runs * H + col;
+    const float* sums_first = a.workspace + (int64_t(kind_first) * runs + first) * H + col;
     float sum = 0.0f;
     if (which >= 2 && !by_gate_row) {
         if (col >= H) return;
-        for (int64_t r = first; r <= last; ++r) sum += part(r);
+        sum = *sums_first;
+        for (int64_t r = first + 1; r <= last; ++r) sum += sums[r * H];
         set_param<T>(out, a.param_f32, at + col, sum);
         return;
     }
-    if (col < H) {
+    if (col < H && first <= last) {
+        if (y == 0) sum = *sums_first;
+        const int64_t step = int64_t(shares) * H;
+        const float* p = sums + (first + (y == 0 ? shares : y)) * H;
+        int left = static_cast<int>((last - first - (y == 0 ? shares : y) + shares) / shares);
 #pragma unroll 8
-        for (int64_t r = first + y; r <= last; r += shares) sum += part(r);
+        for (; left > 0; --left, p += step) sum += *p;
     }
-    parts[y][x] = sum;
-    __syncthreads();
-    if (y == 0 && col < H) {
-        for (int i = 1; i < shares; ++i) sum += parts[i][x];
-        set_param<T>(out, a.param_f32, at + col, sum);
+    parts[threadIdx.x] = sum;
+    for (int n = shares / 2; n > 0; n /= 2) {
+        __syncthreads();
+        if (y < n) parts[threadIdx.x] += parts[threadIdx.x + n * cols];
     }
+    if (y == 0 && col < H) set_param<T>(out, a.param_f32, at + col, parts[x]);
 }
 
 // The types of u and y, and of the residual stream.
@@ -1114,13 +1119,15 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
         const int64_t gates = a.dgate ? (a.rows + a.rows_per_gate - 1) / a.rows_per_gate : 0;
         const bool by_gate_row = gates <= s.clusters / 2;
         const int64_t joins = !a.dgate ? 0 : by_gate_row ? gates : s.clusters - 1;
+        // Shorter sums where runs are many, smaller blocks where they are few; the
+        // whole backward pass, us, with 128 / 256 / 512 threads: 76 runs of 12288
+        // columns 189.4 / 191.5 / -, 152 of 6144 103.3 / 102.6 / -, 912 of 1024
+        // - / 105.1 / 102.9.
+        const int cols = s.clusters > 256 && a.hidden < 1024 ? 8 : 32;
+        const int threads = s.clusters > 256 ? kJoinThreads : s.clusters > 100 ? 256 : 128;
         return launch_pdl(block_norm_join_kernel<T>,
-                          dim3((a.hidden + kJoinCols - 1) / kJoinCols, static_cast<unsigned>(2 + joins)),
-                          // many runs: shorter sums (912 runs of 777 columns, 8
-                          // shares: 18.7 us, 32: under 5), few: smaller blocks
-                          dim3(kJoinCols * (s.clusters > 256 ? kJoinRuns : 8)), 0, stream, a,
-                          int64_t(s.clusters),
-                          by_gate_row ? 1 : 0);
+                          dim3((a.hidden + cols - 1) / cols, static_cast<unsigned>(2 + joins)),
+                          dim3(threads), 0, stream, a, int64_t(s.clusters), cols, by_gate_row ? 1 : 0);
     });
 }
 
