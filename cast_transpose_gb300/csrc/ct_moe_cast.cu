@@ -39,7 +39,7 @@ __device__ __forceinline__ unsigned max_bits(unsigned m, float v) {
 template <int FMT, bool WEIGHTED, bool TRANSPOSE>
 __global__ void __launch_bounds__(kCastThreads, 4)
     sorted_cast_kernel(const SortedCastArgs a, int tile_rows, int tile_cols) {
-    __shared__ __align__(16) uint8_t sq[TRANSPOSE ? 128 * 128 : 16];
+    __shared__ __align__(16) uint8_t sq2[2][TRANSPOSE ? 128 * 128 : 16];   // FP8 copies, in turn
     __shared__ int token[128];
     __shared__ float weight[WEIGHTED ? 128 : 1];
     __shared__ unsigned warp_max[kCastThreads / 32];
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kCastThreads, 4)
                 v[i] = col0 + 8 * c < a.hidden && t >= 0 ? __ldcg(p) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
-    auto cast = [&](auto whole, int64_t col0) {
+    auto cast = [&](auto whole, int64_t col0, uint8_t* sq) {
         constexpr bool WHOLE = decltype(whole)::value;
         const bool col_ok = WHOLE || col0 + 8 * c < a.hidden;
         uint8_t* q = q0 + col0;
@@ -130,13 +130,15 @@ __global__ void __launch_bounds__(kCastThreads, 4)
     for (int ct = first; ct < last; ++ct) {
         const int64_t col0 = int64_t(ct) * 128;
         const bool whole = is_whole(ct), more = ct + 1 < last;
+        uint8_t* sq = sq2[ct & 1];
         if (whole)
-            cast(std::true_type{}, col0);
+            cast(std::true_type{}, col0, sq);
         else
-            cast(std::false_type{}, col0);
-        if constexpr (!TRANSPOSE) {
-            if (more) load_tile(ct + 1);
-        } else {
+            cast(std::false_type{}, col0, sq);
+        if (more) load_tile(ct + 1);
+        if constexpr (TRANSPOSE) {
+            // once a tile: whoever overwrites this copy, two tiles on, has
+            // passed the next tile's barrier, and so has everyone's reading
             __syncthreads();
             const uint32_t* sq32 = reinterpret_cast<const uint32_t*>(sq);
             uint32_t in[16], o[4][4];
@@ -144,10 +146,6 @@ __global__ void __launch_bounds__(kCastThreads, 4)
             for (int j = 0; j < 16; ++j) {
                 const int r = 16 * b + j;
                 in[j] = sq32[r * 32 + (w4 ^ dev::swz(r))];
-            }
-            if (more) {
-                load_tile(ct + 1);
-                __syncthreads();   // the copy has been read: the next tile may overwrite it
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g)
