@@ -21,6 +21,13 @@
 // 2, 4 or 8 that exchange partial sums through distributed shared memory.  Rows
 // that are not whole 16-byte blocks take the same path, copied as the aligned
 // blocks that cover them; launches of few rows read global memory directly.
+//
+// Measured, bf16, of the measured copy rate: forward 8191x6144 68.8 us (403 MB,
+// 0.86), backward with its join 8192x6144 102.6 us (604 MB, 0.87), 8192x12288
+// 189.8 us (1208 MB, 0.94).  What is left is the chain of a row (two sums, each
+// over the block, around 16 columns' arithmetic a thread), of which only as
+// many fit an SM as its registers (backward) and the parameters' shared memory
+// (forward) allow.
 #include "ct_device.cuh"
 #include "ct_ops.h"
 #include "ct_types.cuh"
