@@ -932,19 +932,6 @@ bool all_aligned(P... p) {
     return ((reinterpret_cast<uintptr_t>(p) % 16 == 0) && ...);
 }
 
-int sm_count() {
-    static const int count = [] {
-        int device = 0, n = 0;
-        if (cudaGetDevice(&device) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            return 152;
-        }
-        return n;
-    }();
-    return count;
-}
-
 int round_up(int v, int to) { return (v + to - 1) / to * to; }
 int threads_of(int width) { return std::max(32, round_up((width + 8 * kPer - 1) / (8 * kPer), 32)); }
 int slice(int64_t hidden, int cluster) {

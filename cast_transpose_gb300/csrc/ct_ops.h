@@ -8,6 +8,20 @@
 
 namespace ct {
 
+// SMs of the device of the first call (152 without one).
+inline int sm_count() {
+    static const int count = [] {
+        int device = 0, n = 0;
+        if (cudaGetDevice(&device) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            return 152;
+        }
+        return n;
+    }();
+    return count;
+}
+
 struct SortArgs {
     const void* idx;       // [n] int32, or int64 (index64)
     int64_t n, rows;

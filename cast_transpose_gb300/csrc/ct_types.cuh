@@ -1,5 +1,5 @@
-// ct_types.cuh -- eight columns at a time of bf16, fp16 or fp32 rows, and
-// the block-wide sum, for the norm and expert-movement kernels.
+// ct_types.cuh -- eight columns at a time of bf16, fp16 or fp32 rows, for the
+// norm and expert-movement kernels.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -110,7 +110,6 @@ struct Cols {
     __device__ __forceinline__ int at(int j) const { return G == 8 ? first + j : first + j / G * kStep + j % G; }
     __device__ __forceinline__ bool any() const { return first < H; }
     __device__ __forceinline__ bool has(int j) const { return G == 8 ? first < H : at(j) < H; }
-    __device__ __forceinline__ bool all() const { return G == 8 ? first < H : at(7) < H; }
 };
 
 template <typename T>
@@ -181,18 +180,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
-}
-
-// Sum over the block, the same in every thread, in a fixed order.  `slots`
-// has one float per warp; it may be used again after another __syncthreads
-// (callers that sum twice in a row alternate between two).
-__device__ __forceinline__ float block_sum(float v, float* slots) {
-    v = warp_sum(v);
-    const int warps = (blockDim.x + 31) >> 5, lane = threadIdx.x & 31;
-    if (warps == 1) return v;
-    if (lane == 0) slots[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return warp_sum(lane < warps ? slots[lane] : 0.0f);
 }
 
 }  // namespace dev
