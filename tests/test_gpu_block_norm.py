@@ -138,6 +138,17 @@ def test_many_rows_and_gates(rows, hidden, per_gate):
     c.check_backward()
 
 
+@pytest.mark.parametrize("rows,hidden,dtype", [(400, 8192, BF), (500, 16384, BF), (200, 24580, BF),
+                                               (170, 32768, BF), (170, 32767, HF), (200, 12288, F32),
+                                               (90, 32768, F32), (300, 1, BF), (700, 5, HF), (900, 30, BF)])
+def test_long_runs_of_long_and_short_rows(rows, hidden, dtype):
+    """Rows over clusters of 2, 4 and 8 blocks, whole and odd, and rows of a
+    few elements, in runs of more than one row."""
+    c = Case(rows, hidden, dtype, dtype, F32, per_gate=rows // 2, seed=9)
+    c.check_forward(c.forward())
+    c.check_backward()
+
+
 @pytest.mark.parametrize("post,pre,u,weights", [(True, False, True, True), (False, True, True, True),
                                                 (False, False, True, True), (True, True, False, True),
                                                 (True, True, True, False), (False, True, False, False)])

@@ -100,7 +100,7 @@ def test_sort_no_tokens_and_int64_and_repeats():
 
 
 SHAPES = [(1, 1, 1, 1, 8), (1, 8, 64, 1, 4096), (5, 4, 16, 16, 1), (67, 2, 8, 16, 777),
-          (130, 3, 9, 1, 1000), (300, 8, 32, 16, 520), (64, 5, 6, 32, 12288), (513, 4, 16, 16, 257)]
+          (130, 3, 9, 1, 1000), (90, 3, 8, 16, 1002), (40, 2, 4, 4, 30), (300, 8, 32, 16, 520), (64, 5, 6, 32, 12288), (513, 4, 16, 16, 257)]
 
 
 def data(shape, dtype, seed, std=1.0):
@@ -317,6 +317,28 @@ def test_fp8_dispatch_unaligned_outputs(offset):
         qt.check()
         outs.append((q.t.clone(), qt.t.clone()))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("hidden", [1000, 24])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_fp8_dispatch_many_tiles(hidden, weighted):
+    """More tiles than a wave of blocks: strips of tiles, then single ones."""
+    tokens, topk, experts = 31000, 4, 32
+    idx = routing(tokens, topk, experts, 87)
+    plan = sorted_plan(idx, experts, 16)
+    x = data((tokens, hidden), torch.bfloat16, 88).cuda()
+    weights = data((tokens, topk), torch.float32, 89).cuda()
+    scale, amax, sinv = scalar(70.0), scalar(0.0), scalar(0.0)
+    q = torch.empty(plan.rows, hidden, dtype=torch.uint8, device="cuda")
+    qt = torch.empty(hidden, plan.rows, dtype=torch.uint8, device="cuda")
+    ct.fp8_moe_dispatch(x, plan, scale, amax, sinv, q, qt, weights=weights if weighted else None)
+    slot = torch.as_tensor(ref.sort(idx, experts, 16, plan.rows)[1]).cuda().long()
+    v = torch.where((slot >= 0)[:, None], x[slot.clamp(min=0) // topk].float(), 0.0)
+    if weighted:
+        v = torch.where((slot >= 0)[:, None], v * weights.reshape(-1)[slot.clamp(min=0)][:, None], 0.0)
+    want = (v * scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(q, want) and torch.equal(qt, want.t())
+    assert f32_bits(amax.item()) == f32_bits(v.abs().max().item())
 
 
 # ---------------------------------------------------------------- gradients and use
