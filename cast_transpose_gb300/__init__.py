@@ -176,17 +176,16 @@ def _stream(stream) -> int:
 
 
 def _ptr(t, name, dtype, shape) -> int:
-    """As _dev, for a tensor of this dtype (or one of a tuple) and shape: one
-    pass of cheap tests, and the reason only where they fail."""
-    if type(t) in _TENSORS and t.is_cuda and t.shape == shape and t.is_contiguous() and (
-            t.dtype in dtype if type(dtype) is tuple else t.dtype == dtype):
-        return t.data_ptr()
-    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
+    """As _dev, for a tensor of this dtype (or one of a tuple) and shape: cheap
+    tests first, the reason only where one of them fails."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return _dev(t, name, dtype)
-
-
-_TENSORS = (torch.Tensor, torch.nn.Parameter)
 
 
 def _rc(x: torch.Tensor):

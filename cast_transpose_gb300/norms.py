@@ -32,7 +32,12 @@ class _Config(ctypes.Structure):
 
 
 def _given(t, name, dtype, shape):
-    return None if t is None else _ptr(t, name, dtype, shape)
+    """_ptr of an optional tensor."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, name, dtype, shape)
 
 
 def _config(shape, res_dtype, dtype, w_post, w_pre, gate, rows_per_gate, eps, branch_scale,
