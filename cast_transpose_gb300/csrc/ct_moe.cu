@@ -193,6 +193,9 @@ __global__ void __launch_bounds__(kSortMaxThreads)
             before[e] = earlier;
             total[e] = all;
         }
+        // done with the other blocks' counts; waited for at the end, so that no
+        // block leaves while another may still read its
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     } else {
         for (int e = tid; e < E; e += threads) before[e] = total[e] = 0;
         __syncthreads();
@@ -259,8 +262,7 @@ __global__ void __launch_bounds__(kSortMaxThreads)
         for (int64_t r = int64_t(first[e]) + total[e] + lane; r < first[e + 1]; r += 32) a.src[r] = -1;
     for (int64_t r = int64_t(end) + b * threads + tid; r < a.rows; r += int64_t(blocks) * threads)
         a.src[r] = -1;
-    // no block leaves while another may still read its counts
-    if constexpr (MODE == kCluster) cooperative_groups::this_cluster().sync();
+    if constexpr (MODE == kCluster) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ---- row movement ----------------------------------------------------------

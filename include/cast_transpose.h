@@ -618,8 +618,8 @@ int block_norm_backward(const ct_block_norm_config* cfg, const void* dy, const v
  * wait on an mbarrier give up after a bounded time (about two seconds)
  * instead of hanging, set a bit here and return early; in a correct run it
  * stays 0.  Reads (synchronously) and optionally clears the word.
- * Bits: 1 = a tile-load wait timed out; 2 = ct_selftest_bounded_wait ran
- * (its wait always times out).
+ * Bits: 1 = a wait for a tile, or in block_norm for a row or its sums, timed
+ * out; 2 = ct_selftest_bounded_wait ran (its wait always times out).
  */
 int ct_device_error(unsigned int* value_out, int clear);
 
