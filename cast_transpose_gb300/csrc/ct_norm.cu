@@ -20,7 +20,8 @@
 // Rows of up to 16 columns a thread take one block; longer ones a cluster of
 // 2, 4 or 8 that exchange partial sums through distributed shared memory.  Rows
 // that are not whole 16-byte blocks take the same path, copied as the aligned
-// blocks that cover them; launches of few rows read global memory directly.
+// blocks that cover them.  Launches of no more rows than clusters fit take a
+// kernel of one row per cluster, without loops and rings.
 //
 // Measured, bf16, of the measured copy rate: forward 8191x6144 68.8 us (403 MB,
 // 0.86), backward with its join 8192x6144 102.6 us (604 MB, 0.87), 8192x12288
@@ -56,7 +57,7 @@ constexpr int kSmemFixed = 3328;      // static shared memory and the system's, 
 struct NormShape {
     int cluster;        // blocks per row
     int width;          // columns per block, a multiple of 8
-    int lead, trail;    // stages of the rings; 0: plain loads, no rings
+    int lead, trail;    // stages of the rings; 0: one row per cluster, no rings
     int clusters;       // runs of rows
 };
 
@@ -361,6 +362,34 @@ __device__ __forceinline__ void store_fp8(uint8_t* row, const dev::Cols<G>& c,
 }
 
 
+// y, as it is or as FP8 with the largest magnitude in `most`.
+template <typename T, int G>
+__device__ __forceinline__ void put_y(const NormArgs& a, int64_t at, const dev::Cols<G>& c, const V8& v,
+                                      float scale, unsigned& most) {
+    if (!a.scale) {
+        store_v8<G>(static_cast<T*>(a.y) + at, c, v);
+        return;
+    }
+    float f[8];
+    floats(v, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (on(c)) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+    store_fp8<G>(static_cast<uint8_t*>(a.y) + at, c, f, scale, a.fmt);
+}
+
+// The block's largest magnitude joins amax; the first block writes scale_inv.
+__device__ __forceinline__ void put_amax(const NormArgs& a, unsigned most, float scale, unsigned* block_max) {
+    if (!a.scale) return;
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if ((threadIdx.x & 31) == 0) atomicMax(block_max, most);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (*block_max) atomicMax(reinterpret_cast<unsigned*>(a.amax), *block_max);
+        if (blockIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, scale);
+    }
+}
+
 // With G = 1 the 16-byte blocks that cover a row's slice may begin or end up
 // to 15 bytes outside it: rows that near to the tensors' ends are read from
 // global memory instead.
@@ -370,9 +399,9 @@ __device__ __forceinline__ bool in_ring(int64_t row, int64_t rows, int H) {
 }
 
 // Where a row's slice is read from: its place in a stage, or itself.
-template <bool RING, int G, typename T>
+template <int G, typename T>
 __device__ __forceinline__ const T* row_at(const uint8_t* stage, uint32_t offset, const T* global, bool staged) {
-    if (!RING || (G != 8 && !staged)) return global;
+    if (G != 8 && !staged) return global;
     stage += offset;
     if (G != 8) stage += reinterpret_cast<uintptr_t>(global) & 15;
     return reinterpret_cast<const T*>(stage);
@@ -389,10 +418,10 @@ __device__ __forceinline__ const T* row_at(const uint8_t* stage, uint32_t offset
 //
 // KEEP: a row's u stays in registers between its two uses, two rows apart, so
 // that its stage is free for a row on its way (two-byte types: 16 registers).
-template <typename T, typename R, int G, bool RING, bool FULL>
+template <typename T, typename R, int G, bool FULL>
 __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const NormArgs a,
                                                                     const NormShape s) {
-    constexpr bool KEEP = RING && FULL && G == 8 && sizeof(T) == 2;
+    constexpr bool KEEP = FULL && G == 8 && sizeof(T) == 2;
     struct Kept {
         dev::Raw8<T> v[KEEP ? kPer : 1];
     };
@@ -412,16 +441,14 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     Ring trail{full + kMaxStages, smem + lead.stages * lead.stage_bytes,
                place_bytes<G, R>(s.width), s.trail};                                  // res
     bool lost = false;       // a wait gave up: no more waiting, the error is reported
-    const Own own{reinterpret_cast<float4*>(RING ? trail.base + trail.stages * trail.stage_bytes : smem)};
+    const Own own{reinterpret_cast<float4*>(trail.base + trail.stages * trail.stage_bytes)};
     RowSums sums{slots, full + 2 * kMaxStages, s.cluster, rank};
 
     if (tid == 0) {
         block_max = 0;
         sums.init();
-        if constexpr (RING) {
-            lead.init();
-            trail.init();
-        }
+        lead.init();
+        trail.init();
         dev::fence_barrier_init();
     }
     sums.meet();
@@ -434,12 +461,11 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     auto fetch_trail = [&](int64_t row, int to) {
         trail.fetch(to, in_ring<G>(row, a.rows, H) ? res + row * H : nullptr, W * sizeof(R), 0, nullptr, 0);
     };
-    if constexpr (RING)
-        if (tid == 0)
-            for (int i = 0; i < max(lead.stages, trail.stages) && begin + i < end; ++i) {
-                if (i < lead.stages) fetch_lead(begin + i, i);
-                if (i < trail.stages) fetch_trail(begin + i, i);
-            }
+    if (tid == 0)
+        for (int i = 0; i < max(lead.stages, trail.stages) && begin + i < end; ++i) {
+            if (i < lead.stages) fetch_lead(begin + i, i);
+            if (i < trail.stages) fetch_trail(begin + i, i);
+        }
     int64_t gate_row = a.gate ? begin / a.rows_per_gate : 0;
     int64_t gate_end = a.gate ? (gate_row + 1) * a.rows_per_gate : a.rows;
 #pragma unroll
@@ -461,13 +487,13 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
 
     // sum u^2 of the next row of the leading ring; KEEP: with the row itself
     auto sum_u = [&](int64_t row, Kept& kept) {
-        if (RING) lead.wait(lost);
+        lead.wait(lost);
         if (!post) {
-            if (RING) lead.next();
+            lead.next();
             return 0.0f;
         }
-        const T* x = row_at<RING, G>(lead.at(), 0, u + row * H, in_ring<G>(row, a.rows, H));
-        if (RING) lead.next();
+        const T* x = row_at<G>(lead.at(), 0, u + row * H, in_ring<G>(row, a.rows, H));
+        lead.next();
         float sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
@@ -515,9 +541,9 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         }
         V8 v[kPer];
         float sum_v = 0.0f;
-        if (RING) trail.wait(lost);
-        const R* r = row_at<RING, G>(trail.at(), 0, res + at, staged);
-        const T* x = row_at<RING, G>(lead.base + u_stage * lead.stage_bytes, 0, u + at, staged);
+        trail.wait(lost);
+        const R* r = row_at<G>(trail.at(), 0, res + at, staged);
+        const T* x = row_at<G>(lead.base + u_stage * lead.stage_bytes, 0, u + at, staged);
         const uint64_t rstd2 = pair(rstd_u, rstd_u);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
@@ -544,15 +570,13 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         if (row + 2 < end) next_u = sum_u(row + 2, u_next);
         const float2 sum = sums.get(lost);
         // everyone has read this row's stages; KEEP: of u, the next row's
-        if constexpr (RING) {
-            if (tid == 0) {
-                const int64_t far = row + lead.stages + (KEEP ? 1 : 0);
-                if (far < end) fetch_lead(far, u_stage);
-                if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
-            }
-            trail.next();
-            if (++u_stage == lead.stages) u_stage = 0;
+        if (tid == 0) {
+            const int64_t far = row + lead.stages + (KEEP ? 1 : 0);
+            if (far < end) fetch_lead(far, u_stage);
+            if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
         }
+        trail.next();
+        if (++u_stage == lead.stages) u_stage = 0;
         if (post) {
             rstd_u = rsqrtf(sum.x * per_column + a.eps);
             if (a.rstd_post && writes_rstd && row + 1 < end) a.rstd_post[row + 1] = rstd_u;
@@ -566,30 +590,98 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
             const V8 w = own.get(kPre, p);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[p].p[j] = mul2(mul2(v[p].p[j], rstd_v), w.p[j]);
-            if (a.scale) {
-                float f[8];
-                floats(v[p], f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (on(cols(p))) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-                store_fp8<G>(static_cast<uint8_t*>(a.y) + at + col0, cols(p), f, scale, a.fmt);
-            } else {
-                store_v8<G>(static_cast<T*>(a.y) + at + col0, cols(p), v[p]);
-            }
+            put_y<T>(a, at + col0, cols(p), v[p], scale, most);
         }
     }
     dev::pdl_launch_dependents();
-    if (a.scale && pre) {
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        if ((tid & 31) == 0) atomicMax(&block_max, most);
-        __syncthreads();
-        if (tid == 0) {
-            if (block_max) atomicMax(reinterpret_cast<unsigned*>(a.amax), block_max);
-            if (blockIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, scale);
-        }
-    }
+    if (pre) put_amax(a, most, scale, &block_max);
     if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
     // a block's shared memory stays until its peers have sent their last sums
+    if (s.cluster > 1) sums.meet();
+}
+
+// Forward, one row per cluster: for launches of no more rows than clusters fit.
+// Everything is loaded at once, then summed twice.
+template <typename T, typename R, int G>
+__global__ void __launch_bounds__(kForwardThreads, 1) block_norm_row_kernel(const NormArgs a,
+                                                                        const NormShape s) {
+    __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
+    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ unsigned block_max;
+    const int tid = threadIdx.x, H = a.hidden;
+    const int rank = blockIdx.x % s.cluster, col0 = rank * s.width, W = min(s.width, H - col0);
+    const int64_t row = blockIdx.x / s.cluster, at = row * H + col0;
+    auto cols = [&](int p) { return dev::Cols<G>(p * blockDim.x + tid, W); };
+    RowSums sums{slots, bars, s.cluster, rank};
+    bool lost = false;
+    dev::pdl_launch_dependents();
+    if (tid == 0) {
+        block_max = 0;
+        sums.init();
+        dev::fence_barrier_init();
+    }
+    sums.meet();
+    dev::pdl_wait();
+    if (a.noop && *a.noop != 0.0f) return;
+    const float scale = a.scale ? *a.scale : 0.0f, per_column = 1.0f / H;
+    const int64_t gate_row = a.gate ? row / a.rows_per_gate : 0;
+    V8 u[kPer], v[kPer], branch[kPer], w[kPer];
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+        float f[8];
+        v[p] = load_v8<G>(static_cast<const R*>(a.res) + at, cols(p));
+        if (a.u) {
+            u[p] = load_v8<G>(static_cast<const T*>(a.u) + at, cols(p));
+            branch_factor<T>(a, gate_row, col0, cols(p), f);
+            branch[p] = pairs(f);
+        }
+        if (a.pre) {
+            load_param<T>(a.w_pre, a.param_f32, col0, a.weight_offset, cols(p), f);
+            w[p] = pairs(f);
+        }
+    }
+    auto sum_squares = [&](const V8 (&x)[kPer]) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            uint64_t part = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part = fma2(x[p].p[j], x[p].p[j], part);
+            sum += on(cols(p)) ? lanes_sum(part) : 0.0f;
+        }
+        return sum;
+    };
+    if (a.u) {
+        float rstd = 1.0f;
+        if (a.post) {
+            sums.send(sum_squares(u), 0.0f);
+            rstd = rsqrtf(sums.get(lost).x * per_column + a.eps);
+            if (a.rstd_post && rank == 0 && tid == 0) a.rstd_post[row] = rstd;
+        }
+        const uint64_t rstd2 = pair(rstd, rstd), beta = pair(a.residual_scale, a.residual_scale);
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[p].p[j] = fma2(mul2(u[p].p[j], rstd2), branch[p].p[j], mul2(beta, v[p].p[j]));
+            store_v8<G>(static_cast<R*>(a.res_out) + at, cols(p), v[p]);
+        }
+    }
+    if (a.pre) {
+        sums.send(0.0f, sum_squares(v));
+        const float rstd = rsqrtf(sums.get(lost).y * per_column + a.eps);
+        if (a.rstd_pre && rank == 0 && tid == 0) a.rstd_pre[row] = rstd;
+        const uint64_t rstd2 = pair(rstd, rstd);
+        unsigned most = 0;
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[p].p[j] = mul2(mul2(v[p].p[j], rstd2), w[p].p[j]);
+            put_y<T>(a, at, cols(p), v[p], scale, most);
+        }
+        put_amax(a, most, scale, &block_max);
+    }
+    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
     if (s.cluster > 1) sums.meet();
 }
 
@@ -603,7 +695,7 @@ enum { kSumPre, kSumPost, kSumGateFirst, kSumGateLast, kSums };
 //   P  = alpha gate a_post D                           du = rstd_post (P - uh mean(P uh))
 //   dw_pre = sum dy xh
 //   S  = sum D uh over a gate row's rows: dgate = alpha a_post S, dw_post = sum alpha gate S
-template <typename T, typename R, int G, bool RING, bool FULL>
+template <typename T, typename R, int G, bool FULL>
 __global__ void __launch_bounds__(kBackwardThreads, 1)
     block_norm_backward_kernel(const NormBackwardArgs a, const NormShape s) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -622,7 +714,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     Ring lead{full, smem, stage_bytes, s.lead};        // res_out, dy
     Ring trail{full + kMaxStages, smem + lead.stages * stage_bytes, stage_bytes, s.trail};   // dres_out, u
     bool lost = false;
-    const Own own{reinterpret_cast<float4*>(RING ? trail.base + trail.stages * stage_bytes : smem)};
+    const Own own{reinterpret_cast<float4*>(trail.base + trail.stages * stage_bytes)};
     RowSums sums{slots, full + 2 * kMaxStages, s.cluster, rank};
     const R* res_out = static_cast<const R*>(a.res_out) + col0;
     const R* dres_out = static_cast<const R*>(a.dres_out) + col0;
@@ -631,10 +723,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
 
     if (tid == 0) {
         sums.init();
-        if constexpr (RING) {
-            lead.init();
-            trail.init();
-        }
+        lead.init();
+        trail.init();
         dev::fence_barrier_init();
     }
     sums.meet();
@@ -649,12 +739,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         trail.fetch(to, staged && has_dres ? dres_out + row * H : nullptr, W * kR, second,
                     staged && has_u ? u + row * H : nullptr, W * kT);
     };
-    if constexpr (RING)
-        if (tid == 0)
-            for (int i = 0; i < max(lead.stages, trail.stages) && begin + i < end; ++i) {
-                if (i < lead.stages) fetch_lead(begin + i, i);
-                if (i < trail.stages) fetch_trail(begin + i, i);
-            }
+    if (tid == 0)
+        for (int i = 0; i < max(lead.stages, trail.stages) && begin + i < end; ++i) {
+            if (i < lead.stages) fetch_lead(begin + i, i);
+            if (i < trail.stages) fetch_trail(begin + i, i);
+        }
     const float beta1 = has_u ? a.residual_scale : 1.0f;
     const uint64_t beta = pair(beta1, beta1);
     const int64_t first_gate = a.gate ? begin / a.rows_per_gate : 0;
@@ -677,13 +766,13 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
 
     // sum of G xh over the next row of the leading ring, and its part of dw_pre
     auto first_sum = [&](int64_t row, float rstd) {
-        if (RING) lead.wait(lost);
+        lead.wait(lost);
         const uint8_t* stage = lead.at();
-        if (RING) lead.next();
+        lead.next();
         if (!pre) return 0.0f;
         const bool staged = in_ring<G>(row, a.rows, H);
-        const T* g = row_at<RING, G>(stage, second, dy + row * H, staged);
-        const R* x = row_at<RING, G>(stage, 0, res_out + row * H, staged);
+        const T* g = row_at<G>(stage, second, dy + row * H, staged);
+        const R* x = row_at<G>(stage, 0, res_out + row * H, staged);
         const uint64_t rstd2 = pair(rstd, rstd);
         float sum = 0.0f;
 #pragma unroll
@@ -773,12 +862,12 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         }
         V8 branch[kPer], hat[kPer];          // P, uh
         float sum_p = 0.0f;
-        if (RING) trail.wait(lost);
+        trail.wait(lost);
         const uint8_t* stage = lead.base + x_stage * stage_bytes;
-        const R* x = row_at<RING, G>(stage, 0, res_out + at, staged);
-        const T* g = row_at<RING, G>(stage, second, dy + at, staged);
-        const R* r = row_at<RING, G>(trail.at(), 0, dres_out + at, staged);
-        const T* y = row_at<RING, G>(trail.at(), second, u + at, staged);
+        const R* x = row_at<G>(stage, 0, res_out + at, staged);
+        const T* g = row_at<G>(stage, second, dy + at, staged);
+        const R* r = row_at<G>(trail.at(), 0, dres_out + at, staged);
+        const T* y = row_at<G>(trail.at(), second, u + at, staged);
         const float back1 = -rstd_x * rstd_x * mean_x;
         const uint64_t back = pair(back1, back1), rx2 = pair(rstd_x, rstd_x), ru2 = pair(rstd_u, rstd_u);
 #pragma unroll
@@ -813,14 +902,12 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         if (row + 2 < end) sum_x = first_sum(row + 2, far_x);
         const float2 sum = sums.get(lost);
         // everyone has read this row's stages
-        if constexpr (RING) {
-            if (tid == 0) {
-                if (row + lead.stages < end) fetch_lead(row + lead.stages, x_stage);
-                if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
-            }
-            trail.next();
-            if (++x_stage == lead.stages) x_stage = 0;
+        if (tid == 0) {
+            if (row + lead.stages < end) fetch_lead(row + lead.stages, x_stage);
+            if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
         }
+        trail.next();
+        if (++x_stage == lead.stages) x_stage = 0;
         if (has_u) {
             const float mean = post ? -sum.y * per_column : 0.0f;
             const uint64_t mean2 = pair(mean, mean);
@@ -843,6 +930,120 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         float* part = a.workspace + (int64_t(kSumPre) * s.clusters + run) * H + col0;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) store_v8<G>(part, cols(p), dw_pre[p]);
+    }
+    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (s.cluster > 1) sums.meet();
+}
+
+// Backward, one row per cluster, likewise: its column sums are the row's terms.
+template <typename T, typename R, int G>
+__global__ void __launch_bounds__(kBackwardThreads, 1)
+    block_norm_backward_row_kernel(const NormBackwardArgs a, const NormShape s) {
+    __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
+    __shared__ __align__(8) uint64_t bars[2];
+    const int tid = threadIdx.x, H = a.hidden;
+    const int rank = blockIdx.x % s.cluster, col0 = rank * s.width, W = min(s.width, H - col0);
+    const int64_t row = blockIdx.x / s.cluster, at = row * H + col0;
+    auto cols = [&](int p) { return dev::Cols<G>(p * blockDim.x + tid, W); };
+    RowSums sums{slots, bars, s.cluster, rank};
+    bool lost = false;
+    dev::pdl_launch_dependents();
+    if (tid == 0) {
+        sums.init();
+        dev::fence_barrier_init();
+    }
+    sums.meet();
+    dev::pdl_wait();
+    if (a.noop && *a.noop != 0.0f) return;
+    const float rstd_x = a.pre ? a.rstd_pre[row] : 0.0f, rstd_u = a.post ? a.rstd_post[row] : 1.0f;
+    const float beta1 = a.u ? a.residual_scale : 1.0f, per_column = 1.0f / H;
+    const uint64_t rx2 = pair(rstd_x, rstd_x), ru2 = pair(rstd_u, rstd_u), beta = pair(beta1, beta1);
+    const int64_t gate_row = a.gate ? row / a.rows_per_gate : 0;
+    auto sums_of = [&](int kind) { return a.workspace + (int64_t(kind) * s.clusters + row) * H + col0; };
+    V8 d[kPer], g[kPer], x[kPer], hat[kPer], gate[kPer], w_post[kPer];
+    float sum = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+        float f[8];
+        d[p] = V8{};
+        if (a.dres_out) d[p] = load_v8<G>(static_cast<const R*>(a.dres_out) + at, cols(p));
+        if (a.u) {
+            hat[p] = load_v8<G>(static_cast<const T*>(a.u) + at, cols(p));
+            load_param<T>(a.gate, a.param_f32, gate_row * H + col0, 0.0f, cols(p), f);
+            gate[p] = pairs(f);
+            load_param<T>(a.post ? a.w_post : nullptr, a.param_f32, col0, a.weight_offset, cols(p), f);
+            w_post[p] = pairs(f);
+        }
+        if (a.pre) {
+            g[p] = load_v8<G>(static_cast<const T*>(a.dy) + at, cols(p));
+            x[p] = load_v8<G>(static_cast<const R*>(a.res_out) + at, cols(p));
+            load_param<T>(a.w_pre, a.param_f32, col0, a.weight_offset, cols(p), f);
+            const V8 w = pairs(f);
+            V8 terms;
+            uint64_t part = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[p].p[j] = mul2(x[p].p[j], rx2);                // xh
+                terms.p[j] = mul2(g[p].p[j], x[p].p[j]);
+                part = fma2(terms.p[j], w.p[j], part);
+                g[p].p[j] = mul2(g[p].p[j], w.p[j]);             // G
+            }
+            sum += on(cols(p)) ? lanes_sum(part) : 0.0f;
+            if (a.dw_pre) store_v8<G>(sums_of(kSumPre), cols(p), terms);
+        }
+    }
+    float mean = 0.0f;
+    if (a.pre) {
+        sums.send(sum, 0.0f);
+        mean = -sums.get(lost).x * per_column;
+    }
+    const uint64_t mean_x = pair(mean, mean), alpha = pair(a.branch_scale, a.branch_scale);
+    sum = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+        V8 out;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (a.pre) d[p].p[j] = fma2(rx2, fma2(x[p].p[j], mean_x, g[p].p[j]), d[p].p[j]);
+            out.p[j] = mul2(beta, d[p].p[j]);
+        }
+        store_v8<G>(static_cast<R*>(a.dres) + at, cols(p), out);
+        if (!a.u) continue;
+        V8 post_terms, gate_terms;
+        uint64_t part = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hat[p].p[j] = mul2(hat[p].p[j], ru2);                // uh
+            const uint64_t dots = mul2(alpha, mul2(d[p].p[j], hat[p].p[j]));
+            post_terms.p[j] = mul2(gate[p].p[j], dots);
+            gate_terms.p[j] = mul2(w_post[p].p[j], dots);
+            d[p].p[j] = mul2(mul2(alpha, mul2(gate[p].p[j], d[p].p[j])), w_post[p].p[j]);   // P
+            part = fma2(d[p].p[j], hat[p].p[j], part);
+        }
+        sum += on(cols(p)) ? lanes_sum(part) : 0.0f;
+        if (a.dw_post) store_v8<G>(sums_of(kSumPost), cols(p), post_terms);
+        if (a.dgate) {
+            if (gate_row * a.rows_per_gate != row || min((gate_row + 1) * a.rows_per_gate, a.rows) != row + 1)
+                store_v8<G>(sums_of(kSumGateFirst), cols(p), gate_terms);
+            else if (a.param_f32)
+                store_v8<G>(static_cast<float*>(a.dgate) + gate_row * H + col0, cols(p), gate_terms);
+            else
+                store_v8<G>(static_cast<T*>(a.dgate) + gate_row * H + col0, cols(p), gate_terms);
+        }
+    }
+    if (a.u) {
+        mean = 0.0f;
+        if (a.post) {
+            sums.send(0.0f, sum);
+            mean = -sums.get(lost).y * per_column;
+        }
+        const uint64_t mean_p = pair(mean, mean);
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[p].p[j] = mul2(ru2, fma2(hat[p].p[j], mean_p, d[p].p[j]));
+            store_v8<G>(static_cast<T*>(a.du) + at, cols(p), d[p]);
+        }
     }
     if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
     if (s.cluster > 1) sums.meet();
@@ -948,10 +1149,10 @@ int64_t max_clusters(int64_t rows, int64_t hidden) {
 // Picks the fewest blocks per row whose rings hold enough, then as many blocks
 // per SM as the registers and then the rings allow.  lead_bytes, trail_bytes:
 // of one column in a stage, of `tensors` tensors; min_lead: rows that hold a
-// leading stage at a time; max_threads, sm_threads: of
-// a block, and of those that an SM's registers hold.
+// leading stage at a time; max_threads, sm_threads: of a block, and those that
+// an SM's registers hold; most: runs of rows, at most.
 NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, int tensors, int min_lead,
-                   bool vec, int max_threads, int sm_threads, size_t* smem) {
+                   bool vec, int max_threads, int sm_threads, int64_t most, size_t* smem) {
     NormShape s = {};
     const int pad = vec ? 0 : 32 * tensors;
     auto own = [&] { return kOwnBytes * threads_of(s.width); };
@@ -977,10 +1178,14 @@ NormShape shape_of(int64_t rows, int hidden, int lead_bytes, int trail_bytes, in
     }
     int per_sm = std::min(sm_threads / threads_of(s.width), 32);
     while (per_sm > 1 && !fill(per_sm)) --per_sm;
-    s.clusters = static_cast<int>(std::min<int64_t>(rows, std::max(1, sm_count() * per_sm / s.cluster)));
-    // the rings pay for themselves once runs are longer than a row
-    if (rows <= s.clusters || !fill(per_sm)) s.lead = s.trail = 0;
+    s.clusters = static_cast<int>(
+        std::min({rows, most, int64_t(std::max(1, sm_count() * per_sm / s.cluster))}));
+    fill(per_sm);
     *smem = size_t(own()) + rings(s.lead, s.trail);
+    if (rows <= s.clusters) {
+        s.lead = s.trail = 0;
+        *smem = 0;
+    }
     return s;
 }
 
@@ -1021,7 +1226,7 @@ cudaError_t prepare(const void* kernel, NormShape& s, size_t smem) {
     for (const Known& k : known)
         if (k.kernel == kernel && k.device == device && k.cluster == s.cluster &&
             k.threads == threads_of(s.width) && k.smem == smem) {
-            s.clusters = std::min(s.clusters, k.most);
+            if (s.lead) s.clusters = std::min(s.clusters, k.most);
             return cudaSuccess;
         }
     Known k = {kernel, device, s.cluster, threads_of(s.width), smem, s.clusters};
@@ -1040,7 +1245,7 @@ cudaError_t prepare(const void* kernel, NormShape& s, size_t smem) {
         k.most = std::max(most, 1);
     }
     known.push_back(k);
-    s.clusters = std::min(s.clusters, k.most);
+    if (s.lead) s.clusters = std::min(s.clusters, k.most);
     return cudaSuccess;
 }
 
@@ -1071,12 +1276,10 @@ cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaS
         const bool full = a.u && a.post && a.pre;
         const int min_lead = full && vec && sizeof(T) == 2 ? 2 : 3;   // rows i+1, i+2, and i unless it is kept
         NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, min_lead, vec, kForwardThreads,
-                               2 * kForwardThreads, &smem);
-        auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, 8, true, true>
-                                               : block_norm_kernel<T, R, 8, true, false>)
-                                       : block_norm_kernel<T, R, 1, true, false>)
-                                : (vec ? block_norm_kernel<T, R, 8, false, false>
-                                       : block_norm_kernel<T, R, 1, false, false>);
+                               2 * kForwardThreads, a.rows, &smem);
+        auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, 8, true> : block_norm_kernel<T, R, 8, false>)
+                                     : block_norm_kernel<T, R, 1, false>)
+                              : (vec ? block_norm_row_kernel<T, R, 8> : block_norm_row_kernel<T, R, 1>);
         const cudaError_t e = prepare(reinterpret_cast<const void*>(kernel), s, smem);
         return e != cudaSuccess ? e : launch_rows(kernel, a, s, smem, stream);
     });
@@ -1096,15 +1299,14 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
         using R = decltype(r);
         size_t smem;
         NormShape s = shape_of(a.rows, a.hidden, sizeof(T) + sizeof(R), sizeof(T) + sizeof(R), 2, 3, vec,
-                               kBackwardThreads, kBackwardThreads, &smem);
-        s.clusters = static_cast<int>(std::min<int64_t>(s.clusters, max_clusters(a.rows, a.hidden)));
+                               kBackwardThreads, kBackwardThreads, max_clusters(a.rows, a.hidden), &smem);
         if (a.rows > 0) {
             const bool full = a.u && a.post && a.pre && a.dres_out;
-            auto* kernel = s.lead ? (vec ? (full ? block_norm_backward_kernel<T, R, 8, true, true>
-                                                   : block_norm_backward_kernel<T, R, 8, true, false>)
-                                           : block_norm_backward_kernel<T, R, 1, true, false>)
-                                    : (vec ? block_norm_backward_kernel<T, R, 8, false, false>
-                                           : block_norm_backward_kernel<T, R, 1, false, false>);
+            auto* kernel = s.lead ? (vec ? (full ? block_norm_backward_kernel<T, R, 8, true>
+                                                 : block_norm_backward_kernel<T, R, 8, false>)
+                                         : block_norm_backward_kernel<T, R, 1, false>)
+                                  : (vec ? block_norm_backward_row_kernel<T, R, 8>
+                                         : block_norm_backward_row_kernel<T, R, 1>);
             cudaError_t e = prepare(reinterpret_cast<const void*>(kernel), s, smem);
             if (e == cudaSuccess) e = launch_rows(kernel, a, s, smem, stream);
             if (e != cudaSuccess) return e;
