@@ -601,7 +601,9 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
 }
 
 // Forward, one row per cluster: for launches of no more rows than clusters fit.
-// Everything is loaded at once, then summed twice.
+// Everything is loaded at once, then summed twice (4x4096 to FP8: 4.6 us, the
+// ring's kernel with plain loads 5.4).  From more rows on the ring is ahead:
+// 1000x4096 12.6 us against 20.6, 1200x6144 16.9 against 46.
 template <typename T, typename R, int G>
 __global__ void __launch_bounds__(kForwardThreads, 1) block_norm_row_kernel(const NormArgs a,
                                                                         const NormShape s) {
@@ -935,7 +937,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     if (s.cluster > 1) sums.meet();
 }
 
-// Backward, one row per cluster, likewise: its column sums are the row's terms.
+// Backward, one row per cluster, likewise: its column sums are the row's terms
+// (500x777 with the join 14.6 us, the ring's kernel with plain loads 20.1).
 template <typename T, typename R, int G>
 __global__ void __launch_bounds__(kBackwardThreads, 1)
     block_norm_backward_row_kernel(const NormBackwardArgs a, const NormShape s) {
