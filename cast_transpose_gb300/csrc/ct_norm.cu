@@ -41,10 +41,10 @@ namespace ct {
 namespace {
 
 constexpr int kPer = 2;               // groups of eight columns per thread
-// Threads of a block and registers of a thread: forward, two blocks of 512 with
-// 64; backward, 384 with 168, which its column sums and the compiler's room to
-// interleave columns need (8192x6144 bf16, 512 with 128: 109 us, so: 106;
-// 12288x4096: 131, so: 119).
+// Threads of a block: forward, two blocks with 80 registers a thread (512 with
+// 64 do not hold a row's u: 8191x6144 72.5 us, so: 68.8); backward, one with
+// 168, which its column sums and the compiler's room to interleave columns need
+// (8192x6144, 512 with 128: 109 us, so: 106; 12288x4096: 131, so: 119).
 constexpr int kForwardThreads = 384, kBackwardThreads = 384;
 constexpr int kMaxThreads = kForwardThreads;
 constexpr int kMaxCluster = 8;

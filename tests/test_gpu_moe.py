@@ -417,6 +417,26 @@ def test_noop_flag_stream_and_graph():
         assert all(torch.equal(b, v) for b, v in zip(bufs, want))
 
 
+def test_dispatch_sees_x_written_by_the_preceding_kernel():
+    """x is asked for in L2 while the kernel before still runs: what that kernel
+    writes is what is moved."""
+    tokens, topk, experts, hidden = 4000, 4, 16, 4096
+    idx = routing(tokens, topk, experts, 97)
+    plan = sorted_plan(idx, experts, 16)
+    kept = plan.src >= 0
+    slot = plan.src.clamp(min=0).long()
+    x = data((tokens, hidden), torch.bfloat16, 98).cuda()
+    out = torch.empty(plan.rows, hidden, dtype=torch.bfloat16, device="cuda")
+    for i in range(20):
+        x.neg_()
+        if i % 2:
+            ct.moe_sort(idx.cuda(), plan)
+            x.neg_()
+        ct.moe_dispatch(x, plan, out)
+        want = torch.where(kept[:, None], x[slot // topk], 0.0)
+        assert torch.equal(out, want)
+
+
 def test_offsets_past_32_bits():
     """Sorted buffers of more than 2^31 elements: the last rows are right."""
     tokens, topk, hidden = 33000, 8, 8192
