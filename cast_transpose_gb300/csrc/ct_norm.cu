@@ -267,6 +267,12 @@ struct RowSums {
         return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
     }
 
+    // After a wait that gave up: what the peers may still be sending for the last
+    // get() has to land, or another limit run out, before the block ends.
+    __device__ __forceinline__ void drain() const {
+        const int last = turn ^ 1;
+        if (cluster > 1) cluster_wait_bounded(bars + last, parity ^ last);
+    }
     // Every block of the cluster has begun and set up its shared memory, or is
     // done with the others'.
     __device__ __forceinline__ void meet() const {
@@ -299,12 +305,21 @@ struct Ring {
     int stages;
     int stage = 0;
     uint32_t parity = 0;
+    int on_the_way = 0;     // thread 0: fetched and not yet passed by next()
 
-    __device__ __forceinline__ void next() {
+    // Stays where a wait gave up: drain() goes on from there.
+    __device__ __forceinline__ void next(bool lost) {
+        if (lost) return;
+        --on_the_way;
         if (++stage == stages) {
             stage = 0;
             parity ^= 1;
         }
+    }
+    // After a wait that gave up (thread 0): the copies on their way have to land,
+    // or another limit run out, before the block ends.
+    __device__ __forceinline__ void drain() {
+        for (; on_the_way > 0; next(false)) dev::mbar_wait_bounded(full + stage, parity);
     }
     __device__ __forceinline__ void init() const {
         for (int i = 0; i < stages; ++i) dev::mbar_init(full + i, 1);
@@ -326,7 +341,8 @@ struct Ring {
     }
     // Stage `to` becomes the slices at p and q (either may be null).
     __device__ __forceinline__ void fetch(int to, const void* p, uint32_t p_bytes, uint32_t q_place,
-                                          const void* q, uint32_t q_bytes) const {
+                                          const void* q, uint32_t q_bytes) {
+        ++on_the_way;
         dev::mbar_arrive_expect_tx(full + to, (p ? blocks_bytes(p, p_bytes) : 0) +
                                                   (q ? blocks_bytes(q, q_bytes) : 0));
         if (p) copy(to, 0, p, p_bytes);
@@ -489,11 +505,11 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     auto sum_u = [&](int64_t row, Kept& kept) {
         lead.wait(lost);
         if (!post) {
-            lead.next();
+            lead.next(lost);
             return 0.0f;
         }
         const T* x = row_at<G>(lead.at(), 0, u + row * H, in_ring<G>(row, a.rows, H));
-        lead.next();
+        lead.next(lost);
         float sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
@@ -521,7 +537,7 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         rstd_u = rsqrtf(sums.get(lost).x * per_column + a.eps);
         if (a.rstd_post && writes_rstd) a.rstd_post[begin] = rstd_u;
         if (KEEP) {
-            if (tid == 0 && begin + lead.stages < end) fetch_lead(begin + lead.stages, u_stage);
+            if (tid == 0 && !lost && begin + lead.stages < end) fetch_lead(begin + lead.stages, u_stage);
             ++u_stage;
         }
     }
@@ -570,12 +586,12 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         if (row + 2 < end) next_u = sum_u(row + 2, u_next);
         const float2 sum = sums.get(lost);
         // everyone has read this row's stages; KEEP: of u, the next row's
-        if (tid == 0) {
+        if (tid == 0 && !lost) {
             const int64_t far = row + lead.stages + (KEEP ? 1 : 0);
             if (far < end) fetch_lead(far, u_stage);
             if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
         }
-        trail.next();
+        trail.next(lost);
         if (++u_stage == lead.stages) u_stage = 0;
         if (post) {
             rstd_u = rsqrtf(sum.x * per_column + a.eps);
@@ -595,7 +611,14 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     }
     dev::pdl_launch_dependents();
     if (pre) put_amax(a, most, scale, &block_max);
-    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (lost) {
+        if (tid == 0) {
+            lead.drain();
+            trail.drain();
+            atomicOr(&g_norm_error, kErrWaitTimeout);
+        }
+        sums.drain();
+    }
     // a block's shared memory stays until its peers have sent their last sums
     if (s.cluster > 1) sums.meet();
 }
@@ -683,7 +706,10 @@ __global__ void __launch_bounds__(kForwardThreads, 1) block_norm_row_kernel(cons
         }
         put_amax(a, most, scale, &block_max);
     }
-    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (lost) {
+        if (tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+        sums.drain();
+    }
     if (s.cluster > 1) sums.meet();
 }
 
@@ -770,7 +796,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     auto first_sum = [&](int64_t row, float rstd) {
         lead.wait(lost);
         const uint8_t* stage = lead.at();
-        lead.next();
+        lead.next(lost);
         if (!pre) return 0.0f;
         const bool staged = in_ring<G>(row, a.rows, H);
         const T* g = row_at<G>(stage, second, dy + row * H, staged);
@@ -904,11 +930,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         if (row + 2 < end) sum_x = first_sum(row + 2, far_x);
         const float2 sum = sums.get(lost);
         // everyone has read this row's stages
-        if (tid == 0) {
+        if (tid == 0 && !lost) {
             if (row + lead.stages < end) fetch_lead(row + lead.stages, x_stage);
             if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
         }
-        trail.next();
+        trail.next(lost);
         if (++x_stage == lead.stages) x_stage = 0;
         if (has_u) {
             const float mean = post ? -sum.y * per_column : 0.0f;
@@ -933,7 +959,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
 #pragma unroll
         for (int p = 0; p < kPer; ++p) store_v8<G>(part, cols(p), dw_pre[p]);
     }
-    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (lost) {
+        if (tid == 0) {
+            lead.drain();
+            trail.drain();
+            atomicOr(&g_norm_error, kErrWaitTimeout);
+        }
+        sums.drain();
+    }
     if (s.cluster > 1) sums.meet();
 }
 
@@ -1048,7 +1081,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             store_v8<G>(static_cast<T*>(a.du) + at, cols(p), d[p]);
         }
     }
-    if (lost && tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (lost) {
+        if (tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
+        sums.drain();
+    }
     if (s.cluster > 1) sums.meet();
 }
 
