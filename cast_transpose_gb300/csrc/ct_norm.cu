@@ -305,21 +305,19 @@ struct Ring {
     int stages;
     int stage = 0;
     uint32_t parity = 0;
-    int on_the_way = 0;     // thread 0: fetched and not yet passed by next()
+    int fetched = 0;        // thread 0: fetches so far, number f to stage f % stages
 
-    // Stays where a wait gave up: drain() goes on from there.
-    __device__ __forceinline__ void next(bool lost) {
-        if (lost) return;
-        --on_the_way;
+    __device__ __forceinline__ void next() {
         if (++stage == stages) {
             stage = 0;
             parity ^= 1;
         }
     }
-    // After a wait that gave up (thread 0): the copies on their way have to land,
-    // or another limit run out, before the block ends.
-    __device__ __forceinline__ void drain() {
-        for (; on_the_way > 0; next(false)) dev::mbar_wait_bounded(full + stage, parity);
+    // After a wait that gave up (thread 0): every stage's last copies have to
+    // land, or another limit run out, before the block ends.
+    __device__ __forceinline__ void drain() const {
+        for (int f = max(0, fetched - stages); f < fetched; ++f)
+            dev::mbar_wait_bounded(full + f % stages, (f / stages) & 1);
     }
     __device__ __forceinline__ void init() const {
         for (int i = 0; i < stages; ++i) dev::mbar_init(full + i, 1);
@@ -342,7 +340,7 @@ struct Ring {
     // Stage `to` becomes the slices at p and q (either may be null).
     __device__ __forceinline__ void fetch(int to, const void* p, uint32_t p_bytes, uint32_t q_place,
                                           const void* q, uint32_t q_bytes) {
-        ++on_the_way;
+        ++fetched;
         dev::mbar_arrive_expect_tx(full + to, (p ? blocks_bytes(p, p_bytes) : 0) +
                                                   (q ? blocks_bytes(q, q_bytes) : 0));
         if (p) copy(to, 0, p, p_bytes);
@@ -505,11 +503,11 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     auto sum_u = [&](int64_t row, Kept& kept) {
         lead.wait(lost);
         if (!post) {
-            lead.next(lost);
+            lead.next();
             return 0.0f;
         }
         const T* x = row_at<G>(lead.at(), 0, u + row * H, in_ring<G>(row, a.rows, H));
-        lead.next(lost);
+        lead.next();
         float sum = 0.0f;
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
@@ -591,7 +589,7 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
             if (far < end) fetch_lead(far, u_stage);
             if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
         }
-        trail.next(lost);
+        trail.next();
         if (++u_stage == lead.stages) u_stage = 0;
         if (post) {
             rstd_u = rsqrtf(sum.x * per_column + a.eps);
@@ -796,7 +794,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     auto first_sum = [&](int64_t row, float rstd) {
         lead.wait(lost);
         const uint8_t* stage = lead.at();
-        lead.next(lost);
+        lead.next();
         if (!pre) return 0.0f;
         const bool staged = in_ring<G>(row, a.rows, H);
         const T* g = row_at<G>(stage, second, dy + row * H, staged);
@@ -934,7 +932,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             if (row + lead.stages < end) fetch_lead(row + lead.stages, x_stage);
             if (row + trail.stages < end) fetch_trail(row + trail.stages, trail.stage);
         }
-        trail.next(lost);
+        trail.next();
         if (++x_stage == lead.stages) x_stage = 0;
         if (has_u) {
             const float mean = post ? -sum.y * per_column : 0.0f;
