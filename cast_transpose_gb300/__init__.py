@@ -100,6 +100,8 @@ def lib() -> ctypes.CDLL:
             L.ct_device_error.argtypes = [c.POINTER(c.c_uint), i32]
             L.ct_selftest_bounded_wait.argtypes = [c.c_uint, vp]
             L.ct_selftest_bounded_wait.restype = i32
+            L.ct_selftest_norm_wait.argtypes = [i32, i32, c.c_uint, vp]
+            L.ct_selftest_norm_wait.restype = i32
             L.ct_fp8_convert_f32.argtypes = [vp, i64, i32, vp, vp]
             L.ct_fp8_convert_f32.restype = i32
             L.moe_sorted_rows.restype = i64
@@ -367,6 +369,13 @@ def selftest_bounded_wait(limit_us: int = 20000, stream=None) -> None:
     """Launch the bounded-wait self-test (its wait times out by design and
     sets bit 2 of the device diagnostic word)."""
     _check(lib().ct_selftest_bounded_wait(limit_us, _stream(stream)))
+
+
+def selftest_norm_wait(blocks: int = 2, thread: int = 0, limit_us: int = 20000,
+                       stream=None) -> None:
+    """Launch the self-test of block_norm's give-up path (sets bit 2 of the
+    device diagnostic word)."""
+    _check(lib().ct_selftest_norm_wait(blocks, thread, limit_us, _stream(stream)))
 
 
 def empty_outputs(x: torch.Tensor):

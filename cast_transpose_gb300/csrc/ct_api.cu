@@ -560,6 +560,14 @@ int ct_selftest_bounded_wait(unsigned int limit_us, void* stream) {
     return cuda_status(ct::launch_wait_selftest(limit_us, static_cast<cudaStream_t>(stream)));
 }
 
+int ct_selftest_norm_wait(int blocks, int thread, unsigned int limit_us, void* stream) {
+    if ((blocks != 1 && blocks != 2 && blocks != 4 && blocks != 8) || thread < 0 || thread >= 64 ||
+        limit_us < 1 || limit_us > 1000000)
+        return CT_ERR_ARG;
+    return cuda_status(ct::launch_norm_wait_selftest(blocks, thread, limit_us,
+                                                     static_cast<cudaStream_t>(stream)));
+}
+
 int ct_device_error(unsigned int* value_out, int clear) {
     if (!value_out) return CT_ERR_NULL;
     unsigned casts = 0, norms = 0;

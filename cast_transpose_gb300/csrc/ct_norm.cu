@@ -191,18 +191,37 @@ struct Own {
 enum { kBranch, kPre, kOwnSlots };    // alpha gate a(w_post), a(w_pre)
 constexpr int kOwnBytes = 32 * kPer * kOwnSlots;   // per thread
 
-// dev::mbar_wait_bounded for a barrier that other blocks of the cluster complete.
-__device__ __forceinline__ bool cluster_wait_bounded(uint64_t* bar, uint32_t parity) {
+// ---- waits -----------------------------------------------------------------
+// Every thread polls a barrier for itself and gives up for itself (`lost`):
+// its neighbours may see the same barrier complete.  A thread that is lost goes
+// through the rest of its rows without waiting, so that it meets the others at
+// every shuffle and block barrier, but from then on it arrives at no barrier,
+// sends nothing and fetches nothing: a phase that it has not seen end must not
+// be entered a second time.  Whoever needs its part gives up in turn, so that
+// all of the cluster gets to RowSums::end, where each lost thread reports.
+
+// CLUSTER: for a barrier that other blocks of the cluster complete.
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+    if constexpr (!CLUSTER) return dev::mbar_try_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(dev::smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+// As dev::mbar_wait_bounded, with a last try after the limit: a block that did
+// not run for that long finds its barriers complete.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    if (try_wait<CLUSTER>(bar, parity)) return true;
     const uint64_t t0 = dev::globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok) : "r"(dev::smem_u32(bar)), "r"(parity) : "memory");
-        if (ok) return true;
-        if ((i & 63u) == 0 && dev::globaltimer_ns() - t0 > dev::kWaitLimitNs) return false;
+        if (try_wait<CLUSTER>(bar, parity)) return true;
+        if ((i & 63u) == 0 && dev::globaltimer_ns() - t0 > limit_ns) return try_wait<CLUSTER>(bar, parity);
     }
 }
 
@@ -216,6 +235,7 @@ struct RowSums {
     float (*slots)[2][kMaxCluster * kMaxWarps];
     uint64_t* bars;
     int cluster, rank;
+    uint64_t limit_ns = dev::kWaitLimitNs;
     int turn = 0;
     uint32_t parity = 0;
 
@@ -229,19 +249,20 @@ struct RowSums {
         for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         return v;
     }
-    __device__ __forceinline__ void send(float a, float b) {
+    // `lost`: a wait gave up earlier; then nothing is sent.
+    __device__ __forceinline__ void send(float a, float b, bool lost) {
         const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const bool upper = lane >= 16;
         float v = upper ? b : a;
         v = half_sum(v + __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16));
         float* slot = slots[turn][upper] + rank * warps + warp;
         if (cluster == 1) {
-            if ((lane & 15) == 0) *slot = v;
+            if ((lane & 15) == 0 && !lost) *slot = v;
             __syncwarp();
-            if (lane == 0) dev::mbar_arrive(bars + turn);
+            if (lane == 0 && !lost) dev::mbar_arrive(bars + turn);
         } else {
-            if (threadIdx.x == 0) dev::mbar_arrive_expect_tx(bars + turn, cluster * warps * 8);
-            if ((lane & 15) < cluster) {
+            if (threadIdx.x == 0 && !lost) dev::mbar_arrive_expect_tx(bars + turn, cluster * warps * 8);
+            if ((lane & 15) < cluster && !lost) {
                 uint32_t to, bar;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                              : "=r"(to) : "r"(dev::smem_u32(slot)), "r"(lane & 15));
@@ -256,8 +277,8 @@ struct RowSums {
     __device__ __forceinline__ float2 get(bool& lost) {
         const int n = cluster * (blockDim.x >> 5), lane = threadIdx.x & 31;
         if (!lost)
-            lost = !(cluster == 1 ? dev::mbar_wait_bounded(bars + turn, parity)
-                                  : cluster_wait_bounded(bars + turn, parity));
+            lost = !(cluster == 1 ? wait_bounded<false>(bars + turn, parity, limit_ns)
+                                  : wait_bounded<true>(bars + turn, parity, limit_ns));
         const float* half = slots[turn][lane >= 16];
         parity ^= turn;
         turn ^= 1;
@@ -267,12 +288,6 @@ struct RowSums {
         return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
     }
 
-    // After a wait that gave up: what the peers may still be sending for the last
-    // get() has to land, or another limit run out, before the block ends.
-    __device__ __forceinline__ void drain() const {
-        const int last = turn ^ 1;
-        if (cluster > 1) cluster_wait_bounded(bars + last, parity ^ last);
-    }
     // Every block of the cluster has begun and set up its shared memory, or is
     // done with the others'.
     __device__ __forceinline__ void meet() const {
@@ -281,6 +296,20 @@ struct RowSums {
         else
             asm volatile("barrier.cluster.arrive.release;\n\t"
                          "barrier.cluster.wait.acquire;" ::: "memory");
+    }
+    // The block's last step.  Its shared memory stays until its peers have sent
+    // their last sums, and, where a wait gave up, until what had been sent has
+    // landed: nothing tells how many sends an unfinished turn got, so a lost
+    // thread stays for kLandNs, a thousand times what a send takes.  Every thread
+    // that gave up reports it, whichever it is.
+    static constexpr uint64_t kLandNs = 1000000;
+    __device__ __forceinline__ void end(bool lost, unsigned error) const {
+        if (cluster > 1) meet();
+        if (!lost) return;
+        atomicOr(&g_norm_error, error);
+        if (cluster > 1)
+            for (const uint64_t t0 = dev::globaltimer_ns(); dev::globaltimer_ns() - t0 < kLandNs;) {
+            }
     }
 };
 __device__ __forceinline__ float lanes_sum(uint64_t v) {
@@ -313,18 +342,19 @@ struct Ring {
             parity ^= 1;
         }
     }
-    // After a wait that gave up (thread 0): every stage's last copies have to
-    // land, or another limit run out, before the block ends.
+    // Where thread 0 gave up: every stage's last copies have to land, or another
+    // limit run out, before the block ends.  (A thread 0 that did not has waited
+    // for every row, and so for every copy.)
     __device__ __forceinline__ void drain() const {
         for (int f = max(0, fetched - stages); f < fetched; ++f)
-            dev::mbar_wait_bounded(full + f % stages, (f / stages) & 1);
+            if (!wait_bounded<false>(full + f % stages, (f / stages) & 1, dev::kWaitLimitNs)) return;
     }
     __device__ __forceinline__ void init() const {
         for (int i = 0; i < stages; ++i) dev::mbar_init(full + i, 1);
     }
     // `lost`: a wait gave up, here or earlier; then nothing is waited for.
     __device__ __forceinline__ void wait(bool& lost) const {
-        if (!lost) lost = !dev::mbar_wait_bounded(full + stage, parity);
+        if (!lost) lost = !wait_bounded<false>(full + stage, parity, dev::kWaitLimitNs);
     }
     __device__ __forceinline__ const uint8_t* at() const { return base + stage * stage_bytes; }
     static __device__ __forceinline__ uint32_t blocks_bytes(const void* src, uint32_t bytes) {
@@ -392,14 +422,16 @@ __device__ __forceinline__ void put_y(const NormArgs& a, int64_t at, const dev::
     store_fp8<G>(static_cast<uint8_t*>(a.y) + at, c, f, scale, a.fmt);
 }
 
-// The block's largest magnitude joins amax; the first block writes scale_inv.
-__device__ __forceinline__ void put_amax(const NormArgs& a, unsigned most, float scale, unsigned* block_max) {
+// The block's largest magnitude joins amax, unless a thread's wait gave up: the
+// history outlives the call.  The first block writes scale_inv.
+__device__ __forceinline__ void put_amax(const NormArgs& a, unsigned most, float scale, unsigned* block_max,
+                                         bool lost) {
     if (!a.scale) return;
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if ((threadIdx.x & 31) == 0) atomicMax(block_max, most);
-    __syncthreads();
+    const bool wrong = __syncthreads_or(lost);
     if (threadIdx.x == 0) {
-        if (*block_max) atomicMax(reinterpret_cast<unsigned*>(a.amax), *block_max);
+        if (*block_max && !wrong) atomicMax(reinterpret_cast<unsigned*>(a.amax), *block_max);
         if (blockIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, scale);
     }
 }
@@ -531,7 +563,7 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
     const float first_sum = sum_u(begin, u_now);
     int u_stage = 0;        // the leading stage that is done with next: this row's, KEEP: the next one's
     if (post) {
-        sums.send(first_sum, 0.0f);
+        sums.send(first_sum, 0.0f, lost);
         rstd_u = rsqrtf(sums.get(lost).x * per_column + a.eps);
         if (a.rstd_post && writes_rstd) a.rstd_post[begin] = rstd_u;
         if (KEEP) {
@@ -579,7 +611,7 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
             for (int j = 0; j < 4; ++j) part = fma2(v[p].p[j], v[p].p[j], part);
             sum_v += on(cols(p)) ? lanes_sum(part) : 0.0f;
         }
-        sums.send(next_u, sum_v);
+        sums.send(next_u, sum_v, lost);
         if constexpr (KEEP) u_now = u_next;
         if (row + 2 < end) next_u = sum_u(row + 2, u_next);
         const float2 sum = sums.get(lost);
@@ -608,17 +640,12 @@ __global__ void __launch_bounds__(kForwardThreads, 2) block_norm_kernel(const No
         }
     }
     dev::pdl_launch_dependents();
-    if (pre) put_amax(a, most, scale, &block_max);
-    if (lost) {
-        if (tid == 0) {
-            lead.drain();
-            trail.drain();
-            atomicOr(&g_norm_error, kErrWaitTimeout);
-        }
-        sums.drain();
+    if (pre) put_amax(a, most, scale, &block_max, lost);
+    if (lost && tid == 0) {
+        lead.drain();
+        trail.drain();
     }
-    // a block's shared memory stays until its peers have sent their last sums
-    if (s.cluster > 1) sums.meet();
+    sums.end(lost, kErrWaitTimeout);
 }
 
 // Forward, one row per cluster: for launches of no more rows than clusters fit.
@@ -677,7 +704,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) block_norm_row_kernel(cons
     if (a.u) {
         float rstd = 1.0f;
         if (a.post) {
-            sums.send(sum_squares(u), 0.0f);
+            sums.send(sum_squares(u), 0.0f, lost);
             rstd = rsqrtf(sums.get(lost).x * per_column + a.eps);
             if (a.rstd_post && rank == 0 && tid == 0) a.rstd_post[row] = rstd;
         }
@@ -691,7 +718,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) block_norm_row_kernel(cons
         }
     }
     if (a.pre) {
-        sums.send(0.0f, sum_squares(v));
+        sums.send(0.0f, sum_squares(v), lost);
         const float rstd = rsqrtf(sums.get(lost).y * per_column + a.eps);
         if (a.rstd_pre && rank == 0 && tid == 0) a.rstd_pre[row] = rstd;
         const uint64_t rstd2 = pair(rstd, rstd);
@@ -702,13 +729,9 @@ __global__ void __launch_bounds__(kForwardThreads, 1) block_norm_row_kernel(cons
             for (int j = 0; j < 4; ++j) v[p].p[j] = mul2(mul2(v[p].p[j], rstd2), w[p].p[j]);
             put_y<T>(a, at, cols(p), v[p], scale, most);
         }
-        put_amax(a, most, scale, &block_max);
+        put_amax(a, most, scale, &block_max, lost);
     }
-    if (lost) {
-        if (tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
-        sums.drain();
-    }
-    if (s.cluster > 1) sums.meet();
+    sums.end(lost, kErrWaitTimeout);
 }
 
 // What the workspace holds for the backward pass, [clusters][H] each: partial
@@ -864,7 +887,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     {
         const float sum = first_sum(begin, rstd_x);
         if (pre) {
-            sums.send(sum, 0.0f);
+            sums.send(sum, 0.0f, lost);
             mean_x = sums.get(lost).x * per_column;
         }
     }
@@ -924,7 +947,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
                 sum_p += on(cols(p)) ? lanes_sum(part) : 0.0f;
             }
         }
-        sums.send(sum_x, sum_p);
+        sums.send(sum_x, sum_p, lost);
         if (row + 2 < end) sum_x = first_sum(row + 2, far_x);
         const float2 sum = sums.get(lost);
         // everyone has read this row's stages
@@ -957,15 +980,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
 #pragma unroll
         for (int p = 0; p < kPer; ++p) store_v8<G>(part, cols(p), dw_pre[p]);
     }
-    if (lost) {
-        if (tid == 0) {
-            lead.drain();
-            trail.drain();
-            atomicOr(&g_norm_error, kErrWaitTimeout);
-        }
-        sums.drain();
+    if (lost && tid == 0) {
+        lead.drain();
+        trail.drain();
     }
-    if (s.cluster > 1) sums.meet();
+    sums.end(lost, kErrWaitTimeout);
 }
 
 // Backward, one row per cluster, likewise: its column sums are the row's terms
@@ -1028,7 +1047,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     }
     float mean = 0.0f;
     if (a.pre) {
-        sums.send(sum, 0.0f);
+        sums.send(sum, 0.0f, lost);
         mean = -sums.get(lost).x * per_column;
     }
     const uint64_t mean_x = pair(mean, mean), alpha = pair(a.branch_scale, a.branch_scale);
@@ -1068,7 +1087,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     if (a.u) {
         mean = 0.0f;
         if (a.post) {
-            sums.send(0.0f, sum);
+            sums.send(0.0f, sum, lost);
             mean = -sums.get(lost).y * per_column;
         }
         const uint64_t mean_p = pair(mean, mean);
@@ -1079,11 +1098,31 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             store_v8<G>(static_cast<T*>(a.du) + at, cols(p), d[p]);
         }
     }
-    if (lost) {
-        if (tid == 0) atomicOr(&g_norm_error, kErrWaitTimeout);
-        sums.drain();
+    sums.end(lost, kErrWaitTimeout);
+}
+
+// The give-up path by itself: a cluster exchanges sums three times, and after
+// the second time one thread of its first block goes on as if that wait had run
+// out.  Its warp's third sums are then missing where it would have sent them.
+constexpr int kSelftestThreads = 64;
+
+__global__ void __launch_bounds__(kSelftestThreads) norm_wait_selftest_kernel(int thread, uint64_t limit_ns) {
+    __shared__ float slots[2][2][kMaxCluster * kMaxWarps];
+    __shared__ __align__(8) uint64_t bars[2];
+    RowSums sums{slots, bars, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x), limit_ns};
+    bool lost = false;
+    if (threadIdx.x == 0) {
+        sums.init();
+        dev::fence_barrier_init();
     }
-    if (s.cluster > 1) sums.meet();
+    sums.meet();
+    dev::pdl_wait();      // so that what follows it in the stream follows what came before, too
+    for (int i = 0; i < 3; ++i) {
+        sums.send(1.0f, 2.0f, lost);
+        sums.get(lost);
+        if (i == 1 && blockIdx.x == 0 && threadIdx.x == thread) lost = true;
+    }
+    sums.end(lost, kErrSelftestTimeout);
 }
 
 // Joins the runs' column sums, in run order.  blockIdx.y 0, 1: dw_pre, dw_post;
@@ -1301,6 +1340,16 @@ cudaError_t read_norm_error(unsigned* value, bool clear) {
     if (e != cudaSuccess || !clear) return e;
     const unsigned zero = 0;
     return cudaMemcpyToSymbol(g_norm_error, &zero, sizeof(unsigned));
+}
+
+cudaError_t launch_norm_wait_selftest(int blocks, int thread, uint32_t limit_us, cudaStream_t stream) {
+    NormShape s = {};
+    s.cluster = blocks;
+    s.clusters = 1;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config_of(s, 0, stream, attr);
+    cfg.blockDim = dim3(kSelftestThreads);
+    return cudaLaunchKernelEx(&cfg, norm_wait_selftest_kernel, thread, uint64_t(limit_us) * 1000);
 }
 
 cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaStream_t stream) {

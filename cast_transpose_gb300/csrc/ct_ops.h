@@ -99,5 +99,8 @@ cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int
 
 // The block-norm kernels' own diagnostic word, as read_device_error.
 cudaError_t read_norm_error(unsigned* value, bool clear);
+// Their give-up path: `blocks` blocks of 64 threads, of which `thread` of the
+// first one gives up.
+cudaError_t launch_norm_wait_selftest(int blocks, int thread, uint32_t limit_us, cudaStream_t stream);
 
 }  // namespace ct

@@ -619,7 +619,9 @@ int block_norm_backward(const ct_block_norm_config* cfg, const void* dy, const v
  * instead of hanging, set a bit here and return early; in a correct run it
  * stays 0.  Reads (synchronously) and optionally clears the word.
  * Bits: 1 = a wait for a tile, or in block_norm for a row or its sums, timed
- * out; 2 = ct_selftest_bounded_wait ran (its wait always times out).
+ * out (of whichever thread; the call's outputs are then not to be used, and an
+ * FP8 amax has not been merged by the blocks concerned); 2 = a self-test ran
+ * (their waits always time out).
  */
 int ct_device_error(unsigned int* value_out, int clear);
 
@@ -631,6 +633,16 @@ int ct_device_error(unsigned int* value_out, int clear);
  * health checks.  Errors: CT_ERR_ARG, CT_ERR_CUDA.
  */
 int ct_selftest_bounded_wait(unsigned int limit_us, void* stream);
+
+/*
+ * ct_selftest_norm_wait -- the same for the exchange of sums in block_norm:
+ * `blocks` (1, 2, 4 or 8) blocks of 64 threads exchange sums, and thread
+ * `thread` of the first one goes on as if a wait of its had run out.  Threads
+ * that need what it no longer sends give up after `limit_us` microseconds (1 ..
+ * 1,000,000); then all report bit 2 and return.  Errors: CT_ERR_ARG,
+ * CT_ERR_CUDA.
+ */
+int ct_selftest_norm_wait(int blocks, int thread, unsigned int limit_us, void* stream);
 
 #ifdef __cplusplus
 }
