@@ -6,6 +6,7 @@
 #include "ct_types.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cooperative_groups.h>
 
 namespace ct {
@@ -523,12 +524,27 @@ cudaError_t by_type(int dtype, F&& f) {
 constexpr int64_t kSortOneBlock = 1024, kSortClusterMost = 24576;
 constexpr int64_t kSortBlockSlots = 1024, kSortMaxBlocks = 128;
 
-SortMode sort_mode(int64_t n) {
+static SortMode sort_mode(int64_t n) {
     return n <= kSortOneBlock ? kOne : n <= kSortClusterMost ? kCluster : kGrid;
 }
 
-int grid_blocks(int64_t n) {
+static int grid_blocks(int64_t n) {
     return static_cast<int>(std::min(kSortMaxBlocks, (n + kSortBlockSlots - 1) / kSortBlockSlots));
+}
+
+// The most a sort's kernel ever asks for is allowed once per kernel and device:
+// the limit belongs to the kernel, so one that followed each call's need could
+// be lowered by another host thread between a call's setting and its launch.
+static cudaError_t allow_sort_smem(const void* kernel, std::atomic<uint64_t>& allowed) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;   // beyond 64: every time
+    if (allowed.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    constexpr int most = sizeof(int) * sort_ints(kSortMaxThreads / 32, kMaxExperts);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 size_t sort_workspace(int64_t n, int experts) {
@@ -543,21 +559,20 @@ cudaError_t launch_moe_sort(const SortArgs& a, void* workspace, cudaStream_t str
                         : static_cast<int>(std::min<int64_t>(kSortMaxThreads, std::max<int64_t>(
                                                                  128, (most + 31) / 32 * 32)));
     const size_t smem = sizeof(int) * sort_ints(threads / 32, a.experts);
-    auto prepare = [&](const void* kernel) {
+    static std::atomic<uint64_t> allowed[4];   // by mode, and the counting kernel's
+    auto prepare = [&](auto* kernel, int which) {
         return smem <= 47 * 1024 ? cudaSuccess   // 48 KB with the static part
-                               
-                                 : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                        static_cast<int>(smem));
+                                 : allow_sort_smem(reinterpret_cast<const void*>(kernel), allowed[which]);
     };
     cudaError_t e;
     if (mode == kOne) {
-        e = prepare(reinterpret_cast<const void*>(moe_sort_kernel<kOne>));
+        e = prepare(moe_sort_kernel<kOne>, kOne);
         if (e != cudaSuccess) return e;
         return launch_pdl(moe_sort_kernel<kOne>, dim3(1), dim3(threads), smem, stream, a,
                           static_cast<const int*>(nullptr));
     }
     if (mode == kCluster) {
-        e = prepare(reinterpret_cast<const void*>(moe_sort_kernel<kCluster>));
+        e = prepare(moe_sort_kernel<kCluster>, kCluster);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kSortCluster);
@@ -575,8 +590,8 @@ cudaError_t launch_moe_sort(const SortArgs& a, void* workspace, cudaStream_t str
         return cudaLaunchKernelEx(&cfg, moe_sort_kernel<kCluster>, a,
                                   static_cast<const int*>(nullptr));
     }
-    e = prepare(reinterpret_cast<const void*>(moe_sort_kernel<kGrid>));
-    if (e == cudaSuccess) e = prepare(reinterpret_cast<const void*>(moe_count_kernel));
+    e = prepare(moe_sort_kernel<kGrid>, kGrid);
+    if (e == cudaSuccess) e = prepare(moe_count_kernel, 3);
     if (e != cudaSuccess) return e;
     const dim3 blocks(grid_blocks(a.n));
     int* block_counts = static_cast<int*>(workspace);

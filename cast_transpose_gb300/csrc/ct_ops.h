@@ -22,6 +22,8 @@ inline int sm_count() {
     return count;
 }
 
+constexpr int kMaxExperts = 1024;      // of moe_sort
+
 struct SortArgs {
     const void* idx;       // [n] int32, or int64 (index64)
     int64_t n, rows;

@@ -14,7 +14,8 @@ using ct::overlap;
 using ct::Range;
 using ct::range_of;
 
-constexpr int kMaxExperts = 1024, kMaxTopk = 64, kMaxAlign = 1024;
+using ct::kMaxExperts;
+constexpr int kMaxTopk = 64, kMaxAlign = 1024;
 constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxElements = int64_t(1) << 40;   // of a sorted matrix
 constexpr int64_t kMaxMoveHidden = int64_t(1) << 20, kMaxNormHidden = 32768;

@@ -1,0 +1,50 @@
+"""Expert movement as programs launch it: from several host threads, for many
+experts, right behind the library's own kernels, with a plan per layer."""
+import threading
+
+import pytest
+import torch
+
+import cast_transpose_gb300 as ct
+import ops_reference as ref
+from test_gpu_moe import check_plan, data, routing, sorted_plan
+
+pytestmark = pytest.mark.gpu
+
+
+# one block, a cluster, a grid, each with more than 48 KB of counts
+@pytest.mark.parametrize("tokens,topk", [(3, 4), (250, 4), (2000, 4), (6000, 4), (9000, 4)])
+@pytest.mark.parametrize("experts", [326, 512, 1024])
+def test_sort_into_many_experts(tokens, topk, experts):
+    idx = routing(tokens, topk, experts, tokens + experts)
+    check_plan(sorted_plan(idx, experts, 16), idx)
+
+
+def test_sorts_of_different_expert_counts_from_two_threads():
+    """What one call allows its kernel must not be taken back by another's."""
+    sizes, failed = {1024: 1000, 384: 1000}, []
+    start = threading.Barrier(len(sizes))
+    checks = []
+
+    def work(experts, tokens):
+        try:
+            idx = routing(tokens, 4, experts, experts)
+            plan = ct.MoePlan(tokens, 4, experts, align=16)
+            gpu, stream = idx.cuda(), torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            start.wait(60)
+            for _ in range(4000):
+                ct.moe_sort(gpu, plan, stream=stream)
+            stream.synchronize()
+            checks.append((plan, idx))
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            failed.append(f"{experts} experts: {e!r}")
+
+    threads = [threading.Thread(target=work, args=a) for a in sizes.items()]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for plan, idx in checks:
+        check_plan(plan, idx)
