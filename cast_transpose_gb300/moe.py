@@ -32,12 +32,25 @@ def moe_sorted_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int
     return int(lib().moe_sorted_rows(tokens, topk, experts, align))
 
 
+def _kept(name):
+    return property(lambda self: getattr(self, "_" + name))
+
+
 class MoePlan:
     """The buffers of one sorting: ``row_of`` int32 [T, K], ``src`` int32
     [rows], ``offsets`` int32 [E + 1], ``counts`` int32 [E].  Buffers given
     here are used, the others allocated.  ``rows`` defaults to what holds
     every slot (or to ``src``'s length); with fewer, the slots that come last
-    in expert order are dropped."""
+    in expert order are dropped.
+
+    Sizes and buffers were checked together and stay as they are: the
+    attributes cannot be assigned.  What a buffer holds can be changed, by
+    moe_sort or in place."""
+
+    tokens, topk, experts, align, rows, slots = map(
+        _kept, ("tokens", "topk", "experts", "align", "rows", "slots"))
+    row_of, src, offsets, counts, workspace = map(
+        _kept, ("row_of", "src", "offsets", "counts", "workspace"))
 
     def __init__(self, tokens, topk, experts, align=1, rows=None, device="cuda", row_of=None,
                  src=None, offsets=None, counts=None):
@@ -47,25 +60,25 @@ class MoePlan:
                              f"align {align} is outside the limits")
         if rows is None:
             rows = need if src is None else src.numel()
-        self.tokens, self.topk, self.experts, self.align, self.rows = (tokens, topk, experts,
-                                                                       align, rows)
+        self._tokens, self._topk, self._experts, self._align, self._rows = (tokens, topk, experts,
+                                                                            align, rows)
 
         def buffer(t, shape):
             return torch.empty(shape, dtype=_I32, device=device) if t is None else t
 
-        self.row_of = buffer(row_of, (tokens, topk))
-        self.src = buffer(src, (rows,))
-        self.offsets = buffer(offsets, (experts + 1,))
-        self.counts = buffer(counts, (experts,))
-        size = int(lib().moe_sort_workspace_size(tokens, topk, experts))
-        self.workspace = torch.empty(size, dtype=torch.uint8, device=self.row_of.device)
-        self.slots = (tokens, topk)
-        # these buffers stay the plan's: checked once, here
-        self._row_of = _ptr(self.row_of, "row_of", _I32, (tokens, topk))
-        self._src = _ptr(self.src, "src", _I32, (rows,))
-        self._offsets = _ptr(self.offsets, "offsets", _I32, (experts + 1,))
-        self._counts = _ptr(self.counts, "counts", _I32, (experts,))
-        self._workspace, self._workspace_size = self.workspace.data_ptr(), size
+        self._slots = (tokens, topk)
+        self._row_of = buffer(row_of, self._slots)
+        self._src = buffer(src, (rows,))
+        self._offsets = buffer(offsets, (experts + 1,))
+        self._counts = buffer(counts, (experts,))
+        self._workspace_size = int(lib().moe_sort_workspace_size(tokens, topk, experts))
+        self._workspace = torch.empty(self._workspace_size, dtype=torch.uint8,
+                                      device=self._row_of.device)
+        # checked once, here; their addresses are taken at each call
+        _ptr(self._row_of, "row_of", _I32, self._slots)
+        _ptr(self._src, "src", _I32, (rows,))
+        _ptr(self._offsets, "offsets", _I32, (experts + 1,))
+        _ptr(self._counts, "counts", _I32, (experts,))
 
 
 def _rows_of(t, name):
@@ -81,31 +94,33 @@ def _rows_of(t, name):
 def moe_sort(expert_idx, plan: MoePlan, noop_flag=None, stream=None) -> None:
     """Fill the plan from expert_idx [T, K] (int32 or int64).  The sort is
     stable; an index outside [0, E), -1 say, drops the slot."""
-    idx = _ptr(expert_idx, "expert_idx", _INDEX, plan.slots)
-    _check(lib().moe_sort(idx, 4 if expert_idx.dtype == _I32 else 8, plan.tokens, plan.topk,
-                          plan.experts, plan.align, plan.rows, plan._row_of, plan._src,
-                          plan._offsets, plan._counts, plan._workspace, plan._workspace_size,
+    idx = _ptr(expert_idx, "expert_idx", _INDEX, plan._slots)
+    size = plan._workspace_size
+    _check(lib().moe_sort(idx, 4 if expert_idx.dtype == _I32 else 8, plan._tokens, plan._topk,
+                          plan._experts, plan._align, plan._rows, plan._row_of.data_ptr(),
+                          plan._src.data_ptr(), plan._offsets.data_ptr(), plan._counts.data_ptr(),
+                          plan._workspace.data_ptr() if size else None, size,
                           _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
 def moe_dispatch(x, plan: MoePlan, out, noop_flag=None, stream=None) -> None:
     """x [T, hidden] -> out [rows, hidden] of the same type."""
     hidden, dtype = _rows_of(x, "x")
-    px = _ptr(x, "x", dtype, (plan.tokens, hidden))
-    po = _ptr(out, "out", dtype, (plan.rows, hidden))
-    _check(lib().moe_dispatch(px, plan.tokens, plan.topk, hidden, _DTYPES[dtype], plan._row_of,
-                              plan._src, plan.rows, po, _opt(noop_flag, "noop_flag"),
-                              _stream(stream)))
+    px = _ptr(x, "x", dtype, (plan._tokens, hidden))
+    po = _ptr(out, "out", dtype, (plan._rows, hidden))
+    _check(lib().moe_dispatch(px, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
+                              plan._row_of.data_ptr(), plan._src.data_ptr(), plan._rows, po,
+                              _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
 def moe_dispatch_backward(dout, plan: MoePlan, dx, noop_flag=None, stream=None) -> None:
     """dout [rows, hidden] -> dx [T, hidden] of the same type."""
     hidden, dtype = _rows_of(dout, "dout")
-    pd = _ptr(dout, "dout", dtype, (plan.rows, hidden))
-    px = _ptr(dx, "dx", dtype, (plan.tokens, hidden))
-    _check(lib().moe_dispatch_backward(pd, plan.tokens, plan.topk, hidden, _DTYPES[dtype],
-                                       plan._row_of, plan.rows, px, _opt(noop_flag, "noop_flag"),
-                                       _stream(stream)))
+    pd = _ptr(dout, "dout", dtype, (plan._rows, hidden))
+    px = _ptr(dx, "dx", dtype, (plan._tokens, hidden))
+    _check(lib().moe_dispatch_backward(pd, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
+                                       plan._row_of.data_ptr(), plan._rows, px,
+                                       _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
 def fp8_moe_dispatch(x, plan: MoePlan, scale, amax, scale_inv, out, out_t=None, fmt=E4M3,
@@ -114,12 +129,12 @@ def fp8_moe_dispatch(x, plan: MoePlan, scale, amax, scale_inv, out, out_t=None, 
     [hidden, rows].  weights: fp32 [T, K], multiplied in before the amax and
     the cast; with dy for x, FP8 gradients for the experts' outputs."""
     hidden, _ = _rows_of(x, "x")
-    px = _ptr(x, "x", torch.bfloat16, (plan.tokens, hidden))
-    po = _ptr(out, "out", _U8, (plan.rows, hidden))
-    pt = None if out_t is None else _ptr(out_t, "out_t", _U8, (hidden, plan.rows))
-    pw = None if weights is None else _ptr(weights, "weights", _F32, plan.slots)
-    _check(lib().fp8_moe_dispatch(px, plan.tokens, plan.topk, hidden, plan._src, plan.rows, pw,
-                                  _dev(scale, "scale", _F32, 1), _dev(amax, "amax", _F32, 1),
+    px = _ptr(x, "x", torch.bfloat16, (plan._tokens, hidden))
+    po = _ptr(out, "out", _U8, (plan._rows, hidden))
+    pt = None if out_t is None else _ptr(out_t, "out_t", _U8, (hidden, plan._rows))
+    pw = None if weights is None else _ptr(weights, "weights", _F32, plan._slots)
+    _check(lib().fp8_moe_dispatch(px, plan._tokens, plan._topk, hidden, plan._src.data_ptr(),
+                                  plan._rows, pw, _dev(scale, "scale", _F32, 1), _dev(amax, "amax", _F32, 1),
                                   _dev(scale_inv, "scale_inv", _F32, 1), po, pt, fmt,
                                   _opt(noop_flag, "noop_flag"), _stream(stream)))
 
@@ -127,11 +142,11 @@ def fp8_moe_dispatch(x, plan: MoePlan, scale, amax, scale_inv, out, out_t=None, 
 def moe_combine(ys, plan: MoePlan, weights, out, noop_flag=None, stream=None) -> None:
     """ys [rows, hidden], weights fp32 [T, K] -> out [T, hidden] of ys' type."""
     hidden, dtype = _rows_of(ys, "ys")
-    py = _ptr(ys, "ys", dtype, (plan.rows, hidden))
-    po = _ptr(out, "out", dtype, (plan.tokens, hidden))
-    _check(lib().moe_combine(py, plan.tokens, plan.topk, hidden, _DTYPES[dtype], plan._row_of,
-                             _ptr(weights, "weights", _F32, plan.slots), plan.rows, po,
-                             _opt(noop_flag, "noop_flag"), _stream(stream)))
+    py = _ptr(ys, "ys", dtype, (plan._rows, hidden))
+    po = _ptr(out, "out", dtype, (plan._tokens, hidden))
+    _check(lib().moe_combine(py, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
+                             plan._row_of.data_ptr(), _ptr(weights, "weights", _F32, plan._slots),
+                             plan._rows, po, _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
 def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=None,
@@ -139,11 +154,11 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
     """dout [T, hidden] -> dys [rows, hidden] and dweights fp32 [T, K]; either
     may be None (ys is read for dweights only)."""
     hidden, dtype = _rows_of(dout, "dout")
-    pd = _ptr(dout, "dout", dtype, (plan.tokens, hidden))
-    py = None if ys is None else _ptr(ys, "ys", dtype, (plan.rows, hidden))
-    ps = None if dys is None else _ptr(dys, "dys", dtype, (plan.rows, hidden))
-    pw = None if dweights is None else _ptr(dweights, "dweights", _F32, plan.slots)
-    _check(lib().moe_combine_backward(pd, py, plan.tokens, plan.topk, hidden, _DTYPES[dtype],
-                                      plan._row_of, plan._src,
-                                      _ptr(weights, "weights", _F32, plan.slots), plan.rows, ps, pw,
-                                      _opt(noop_flag, "noop_flag"), _stream(stream)))
+    pd = _ptr(dout, "dout", dtype, (plan._tokens, hidden))
+    py = None if ys is None else _ptr(ys, "ys", dtype, (plan._rows, hidden))
+    ps = None if dys is None else _ptr(dys, "dys", dtype, (plan._rows, hidden))
+    pw = None if dweights is None else _ptr(dweights, "dweights", _F32, plan._slots)
+    _check(lib().moe_combine_backward(pd, py, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
+                                      plan._row_of.data_ptr(), plan._src.data_ptr(),
+                                      _ptr(weights, "weights", _F32, plan._slots), plan._rows, ps,
+                                      pw, _opt(noop_flag, "noop_flag"), _stream(stream)))

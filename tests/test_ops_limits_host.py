@@ -1,6 +1,7 @@
 """Further host-side checks of the expert-movement and block-norm operators (no
 GPU needed): limits, refusals and their messages, the plan's attributes."""
 import pytest
+import torch
 
 import cast_transpose_gb300 as ct
 
@@ -17,3 +18,64 @@ def test_norm_wait_selftest_rejects(L):
     for blocks, thread, limit in ((0, 0, 10), (3, 0, 10), (16, 0, 10), (2, -1, 10), (2, 64, 10),
                                   (2, 0, 0), (2, 0, 1000001)):
         assert L.ct_selftest_norm_wait(blocks, thread, limit, None) == ARG
+
+
+class Recorder:
+    """In place of the library: sizes from it, other calls kept."""
+    def __init__(self, real):
+        self.real, self.calls = real, []
+
+    def __getattr__(self, name):
+        if name in ("moe_sorted_rows", "moe_sort_workspace_size"):
+            return getattr(self.real, name)
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def cpu_plan(monkeypatch, L):
+    """A plan with CPU buffers, whose calls go to a recorder."""
+    import cast_transpose_gb300.moe as moe
+    recorder = Recorder(L)
+    monkeypatch.setattr(moe, "lib", lambda: recorder)
+    monkeypatch.setattr(moe, "_ptr", lambda t, name, dtype, shape: t.data_ptr())
+    monkeypatch.setattr(moe, "_dev", lambda t, *rest: t.data_ptr())
+    monkeypatch.setattr(moe, "_stream", lambda stream: 0)
+    return ct.MoePlan(10000, 4, 8, align=16, device="cpu"), recorder
+
+
+ATTRIBUTES = ("row_of", "src", "offsets", "counts", "workspace", "tokens", "topk", "experts",
+              "align", "rows", "slots")
+
+
+@pytest.mark.parametrize("name", ATTRIBUTES)
+def test_a_plans_sizes_and_buffers_cannot_be_replaced(cpu_plan, name):
+    plan, _ = cpu_plan
+    before = getattr(plan, name)
+    with pytest.raises(AttributeError):
+        setattr(plan, name, before)
+    assert getattr(plan, name) is before
+
+
+def test_a_plans_addresses_are_those_of_its_buffers_now(cpu_plan):
+    """Also where a buffer's memory has been exchanged since."""
+    plan, recorder = cpu_plan
+    for t in (plan.row_of, plan.src, plan.offsets, plan.counts, plan.workspace):
+        t.set_(torch.zeros_like(t))
+    idx, x = torch.zeros(10000, 4, dtype=torch.int32), torch.zeros(10000, 8)
+    out, w = torch.zeros(plan.rows, 8), torch.zeros(10000, 4)
+    ct.moe_sort(idx, plan)
+    ct.moe_dispatch(x, plan, out)
+    ct.moe_dispatch_backward(out, plan, x)
+    ct.moe_combine(out, plan, w, x)
+    ct.moe_combine_backward(x, out, plan, w, out, w)
+    one, q = torch.zeros(1), torch.zeros(plan.rows, 8, dtype=torch.uint8)
+    ct.fp8_moe_dispatch(x, plan, one, one, one, q)
+    row_of, src, offsets, counts, ws = (t.data_ptr() for t in (
+        plan.row_of, plan.src, plan.offsets, plan.counts, plan.workspace))
+    args = dict(recorder.calls)
+    assert args["moe_sort"][7:12] == (row_of, src, offsets, counts, ws)
+    assert args["moe_dispatch"][5:7] == (row_of, src)
+    assert args["moe_dispatch_backward"][5] == row_of
+    assert args["moe_combine"][5] == row_of
+    assert args["moe_combine_backward"][6:8] == (row_of, src)
+    assert args["fp8_moe_dispatch"][4] == src
