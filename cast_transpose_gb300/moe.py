@@ -1,8 +1,12 @@
 """Tokens sorted by expert and back: argument checks and calls.
 
 T tokens choose K experts each, out of E.  ``MoePlan`` holds the buffers that
-``moe_sort`` fills from the router's choices and the other calls read; one plan
-serves every layer and step of a batch shape.
+``moe_sort`` fills from the router's choices and the other calls read, the
+backward calls too: until a layer's backward pass has run, its plan must not be
+sorted again.  In training every layer, and every microbatch in flight, has a
+plan of its own, reused from step to step; layers that only run forward can
+share one, each sorting before it moves.  A plan's buffers, its workspace among
+them, are used by one stream at a time.
 
   moe_sort               the plan: which sorted row every (token, k) slot gets
   moe_dispatch           out[row] = x[token], padding rows zero

@@ -486,7 +486,9 @@ int64_t moe_sorted_rows(int64_t tokens, int topk, int experts, int align);
 size_t moe_sort_workspace_size(int64_t tokens, int topk, int experts);
 
 /*
- * moe_sort -- the plan of the four calls below, from the router's choices.
+ * moe_sort -- the plan of the calls below, from the router's choices.  The
+ * backward calls read row_of and src as the forward pass had them: they must
+ * not be sorted over before.
  *
  *   expert_idx  [T, K], int32 (index_bytes = 4) or int64 (index_bytes = 8)
  *

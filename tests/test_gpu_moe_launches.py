@@ -48,3 +48,39 @@ def test_sorts_of_different_expert_counts_from_two_threads():
     assert not failed, failed
     for plan, idx in checks:
         check_plan(plan, idx)
+
+
+def test_layers_with_a_plan_each():
+    """Two layers forward, then both backward: each gets its own routing's
+    gradients, as from a plan that was sorted for it alone."""
+    tokens, topk, experts, hidden = 300, 2, 6, 64
+    layers = []
+    for seed in (1, 2):
+        idx = routing(tokens, topk, experts, seed).cuda()
+        layers.append((idx, ct.MoePlan(tokens, topk, experts, align=16)))
+    w = data((tokens, topk), torch.float32, 3).cuda()
+    x, dout = data((tokens, hidden), torch.float32, 4).cuda(), data((tokens, hidden), torch.float32, 5).cuda()
+
+    def forward(idx, plan):
+        ct.moe_sort(idx, plan)
+        ys = torch.empty(plan.rows, hidden, device="cuda")
+        ct.moe_dispatch(x, plan, ys)
+        return ys
+
+    def backward(plan, ys):
+        dys, dw, dx = torch.empty_like(ys), torch.empty_like(w), torch.empty_like(x)
+        ct.moe_combine_backward(dout, ys, plan, w, dys, dw)
+        ct.moe_dispatch_backward(dys, plan, dx)
+        return dys, dw, dx
+
+    kept = [forward(*layer) for layer in layers]
+    got = [backward(layer[1], ys) for layer, ys in zip(reversed(layers), reversed(kept))]
+    for (idx, _), ys, grads in zip(layers, kept, reversed(got)):
+        alone = ct.MoePlan(tokens, topk, experts, align=16)
+        assert torch.equal(forward(idx, alone), ys)
+        for a, b in zip(grads, backward(alone, ys)):
+            assert torch.equal(a, b)
+        rows = ref.sort(idx.cpu(), experts, 16, alone.rows)[0]
+        want, err, want_w, err_w = ref.combine_backward(dout.cpu(), ys.cpu(), rows, w.cpu(), alone.rows)
+        ref.close(grads[0], want, ref.rounded(want, err, torch.float32), "dys")
+        ref.close(grads[1], want_w, err_w + 1e-38, "dweights")
