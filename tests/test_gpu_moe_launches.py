@@ -84,3 +84,54 @@ def test_layers_with_a_plan_each():
         want, err, want_w, err_w = ref.combine_backward(dout.cpu(), ys.cpu(), rows, w.cpu(), alone.rows)
         ref.close(grads[0], want, ref.rounded(want, err, torch.float32), "dys")
         ref.close(grads[1], want_w, err_w + 1e-38, "dweights")
+
+
+# The writers let their successor start at their first instruction, so that its
+# prefetch of x runs while they write: moe_combine and moe_dispatch_backward for
+# tens of microseconds, the few-row norm for a few.
+def write_combine(state, i):
+    ct.moe_combine(state["ys"][i], state["plan"], state["w"], state["x"])
+
+
+def write_dispatch_backward(state, i):
+    ct.moe_dispatch_backward(state["ys"][i], state["plan"], state["x"])
+
+
+def write_norm(state, i):
+    u = state["ys"][i][:len(state["x"])]
+    ct.block_norm(u, state["res"], state["res_out"], state["x"])
+
+
+@pytest.mark.parametrize("sort_between", [False, True])
+@pytest.mark.parametrize("writer,tokens", [(write_combine, 4000), (write_dispatch_backward, 4000),
+                                           (write_norm, 60)])
+def test_dispatch_of_what_the_kernel_before_writes(writer, tokens, sort_between):
+    """x has new values each time, from a kernel of the library right before the
+    dispatch, or before its sort, without a pause in the stream."""
+    topk, experts, hidden, times = 4, 16, 4096, 5
+    idx = routing(tokens, topk, experts, 97).cuda()
+    plan, source = (ct.MoePlan(tokens, topk, experts, align=16) for _ in range(2))
+    ct.moe_sort(idx, plan)
+    ct.moe_sort(idx, source)
+    state = {"plan": source, "w": torch.rand(tokens, topk, device="cuda"),
+             "ys": [torch.randn(source.rows, hidden, device="cuda").to(torch.bfloat16)
+                    for _ in range(times)],
+             "res": torch.ones(tokens, hidden, device="cuda", dtype=torch.bfloat16),
+             "res_out": torch.empty(tokens, hidden, device="cuda", dtype=torch.bfloat16),
+             "x": torch.zeros(tokens, hidden, device="cuda", dtype=torch.bfloat16)}
+    outs = [torch.empty(plan.rows, hidden, device="cuda", dtype=torch.bfloat16) for _ in range(times)]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for i in range(times):
+            writer(state, i)
+            if sort_between:
+                ct.moe_sort(idx, plan)
+            ct.moe_dispatch(state["x"], plan, outs[i])
+        torch.cuda.synchronize()
+        slot = plan.src.clamp(min=0).long()
+        kept = (plan.src >= 0)[:, None]
+        for i in range(times):
+            writer(state, i)
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], torch.where(kept, state["x"][slot // topk], 0.0))
+            outs[i].fill_(float("nan"))
