@@ -98,9 +98,11 @@ def _rows_of(t, name):
 def moe_sort(expert_idx, plan: MoePlan, noop_flag=None, stream=None) -> None:
     """Fill the plan from expert_idx [T, K] (int32 or int64).  The sort is
     stable; an index outside [0, E), -1 say, drops the slot."""
-    idx = _ptr(expert_idx, "expert_idx", _INDEX, plan._slots)
+    dtype = getattr(expert_idx, "dtype", None)
+    # one dtype is the short way through _ptr
+    idx = _ptr(expert_idx, "expert_idx", dtype if dtype in _INDEX else _INDEX, plan._slots)
     size = plan._workspace_size
-    _check(lib().moe_sort(idx, 4 if expert_idx.dtype == _I32 else 8, plan._tokens, plan._topk,
+    _check(lib().moe_sort(idx, 4 if dtype is _I32 else 8, plan._tokens, plan._topk,
                           plan._experts, plan._align, plan._rows, plan._row_of.data_ptr(),
                           plan._src.data_ptr(), plan._offsets.data_ptr(), plan._counts.data_ptr(),
                           plan._workspace.data_ptr() if size else None, size,
