@@ -287,8 +287,9 @@ __device__ __forceinline__ void token_rows(const MoveArgs& a, int64_t t, int (&r
 }
 
 // A launch that writes sorted rows has blocks for the padding rows before
-// those of the tokens: each looks at 32 rows and clears the ones without a slot.
-constexpr int kPadRows = 32;
+// those of the tokens: each looks at kPadRows rows, a lane each, and clears the
+// ones without a slot.
+static_assert(kPadRows == 32, "a lane looks at a row");
 
 template <typename W>
 __device__ void clear_padding(const MoveArgs& a, int64_t words) {
@@ -500,9 +501,7 @@ bool vectors(const MoveArgs& a) { return a.hidden % 8 == 0 && allow(a, 16); }
 #define CT_BY_GROUP(kernel, T) \
     (vectors(a) ? kernel<T, 8> : allow(a, 2 * sizeof(T)) ? kernel<T, 2> : kernel<T, 1>)
 
-int pad_blocks(const MoveArgs& a) {
-    return static_cast<int>(a.sorted ? (a.rows + kPadRows - 1) / kPadRows : 0);
-}
+int pad_blocks(const MoveArgs& a) { return static_cast<int>(a.sorted ? ct::pad_blocks(a.rows) : 0); }
 
 // Threads of a block whose rows have `groups` words or groups of columns.
 dim3 move_threads(int64_t groups, int per_thread) {

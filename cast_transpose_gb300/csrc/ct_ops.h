@@ -52,6 +52,10 @@ struct MoveArgs {
     int64_t tokens, rows, hidden;
     int topk, elem_bytes;
 };
+// Launches that write sorted rows have a block per token, and before those one
+// per kPadRows rows.
+constexpr int kPadRows = 32;
+inline int64_t pad_blocks(int64_t rows) { return (rows + kPadRows - 1) / kPadRows; }
 cudaError_t launch_moe_dispatch(const MoveArgs& a, cudaStream_t stream);
 cudaError_t launch_moe_combine(const MoveArgs& a, int dtype, cudaStream_t stream);
 cudaError_t launch_moe_combine_backward(const MoveArgs& a, int dtype, cudaStream_t stream);

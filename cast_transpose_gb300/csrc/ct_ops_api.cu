@@ -57,6 +57,9 @@ int check_move(int64_t tokens, int topk, int64_t hidden, int64_t rows, int dtype
     return CT_OK;
 }
 
+// Blocks of a launch that writes sorted rows: as many as a grid can have.
+bool fits_grid(int64_t tokens, int64_t rows) { return tokens + ct::pad_blocks(rows) <= kMaxIndex; }
+
 }  // namespace
 
 extern "C" {
@@ -116,6 +119,7 @@ int moe_dispatch(const void* x, int64_t tokens, int topk, int64_t hidden, int dt
                  const float* noop_flag, void* stream) {
     int st = check_move(tokens, topk, hidden, rows, dtype);
     if (st != CT_OK) return st;
+    if (!fits_grid(tokens, rows)) return CT_ERR_SHAPE;
     if (hidden == 0 || rows == 0) return CT_OK;
     const int b = elem_bytes(dtype);
     st = check_buffers({{x, tokens * hidden * b, b, false},
@@ -184,6 +188,7 @@ int moe_combine_backward(const void* dout, const void* ys, int64_t tokens, int t
     int st = check_move(tokens, topk, hidden, rows, dtype);
     if (st != CT_OK) return st;
     if (!dys && !dweights) return CT_ERR_NULL;
+    if (dys && !fits_grid(tokens, rows)) return CT_ERR_SHAPE;
     const int b = elem_bytes(dtype);
     st = check_buffers({{dout, tokens * hidden * b, b, false},
                         {ys, rows * hidden * b, b, false, !dweights},

@@ -471,8 +471,11 @@ int ct_fp8_convert_f32(const float* in, int64_t n, int fmt, void* out, void* str
  * [0, rows) in row_of, or outside [0, T*K) in src, are treated as -1.
  * Arithmetic is fp32, rounded once to the output's type; sums run over k in
  * order and every result is the same from call to call.
- * Limits: 1 <= E <= 1024, 1 <= K <= 64, 1 <= align <= 1024, T*K and rows
- * below 2^31.  Buffers that a call writes must not overlap any other buffer.
+ * Limits: 1 <= E <= 1024, 1 <= K <= 64, 1 <= align <= 1024 (else CT_ERR_ARG);
+ * T*K and rows below 2^31, hidden <= 2^20, rows * hidden <= 2^40, and where
+ * sorted rows are written by moe_dispatch or moe_combine_backward T +
+ * ceil(rows / 32) below 2^31 (else CT_ERR_SHAPE).
+ * Buffers that a call writes must not overlap any other buffer.
  * Errors: CT_ERR_NULL, CT_ERR_SHAPE, CT_ERR_ALIGN, CT_ERR_FORMAT (data type,
  * fmt), CT_ERR_ARG (E, K, align), CT_ERR_ALIAS, CT_ERR_WORKSPACE, CT_ERR_CUDA.
  * ========================================================================== */

@@ -79,3 +79,34 @@ def test_a_plans_addresses_are_those_of_its_buffers_now(cpu_plan):
     assert args["moe_combine"][5] == row_of
     assert args["moe_combine_backward"][6:8] == (row_of, src)
     assert args["fp8_moe_dispatch"][4] == src
+
+
+MOST = 2 ** 31 - 1
+
+
+def test_blocks_beyond_a_launch(L):
+    """One block per token and one per 32 sorted rows have to fit a grid."""
+    def dispatch(tokens, rows):
+        return L.moe_dispatch(A, tokens, 1, 1, 0, B, C, rows, D, None, None)
+
+    def backward(tokens, rows, dys=F, dw=G):
+        return L.moe_combine_backward(A, B, tokens, 1, 1, 0, C, D, E, rows, dys, dw, None, None)
+    for call in (dispatch, backward):
+        assert call(MOST, 1) == SHAPE
+        assert call(MOST - 1, 33) == SHAPE
+        assert call(MOST // 33 * 32 + 33, MOST) == SHAPE
+    # nothing is sorted: a block per token alone (here no further than its buffers)
+    assert backward(MOST, MOST, dys=None, dw=G + 2) == ALIGN
+    assert L.moe_combine(A, MOST, 1, 1, 0, B, C, 1, D + 1, None, None) == ALIGN
+
+
+def test_limits_of_hidden_and_of_a_sorted_matrix(L):
+    def dispatch(hidden, rows):
+        return L.moe_dispatch(A, 10, 2, hidden, 0, B, C, rows, D + 1, None, None)
+
+    def cast(hidden, rows):
+        return L.fp8_moe_dispatch(A + 1, 10, 2, hidden, B, rows, None, C, D, E, F, None, 0, None, None)
+    for call in (dispatch, cast):
+        assert call(2 ** 20 + 1, 1) == SHAPE
+        assert call(2 ** 20, 2 ** 20 + 1) == SHAPE
+        assert call(2 ** 20, 2 ** 20) == ALIGN          # within them
