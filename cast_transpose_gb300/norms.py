@@ -35,9 +35,28 @@ def _given(t, name, dtype, shape):
     """_ptr of an optional tensor."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     return _ptr(t, name, dtype, shape)
+
+
+def _dtype_of(t, name):
+    try:
+        return t.dtype
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+
+
+def _matrix(t, name):
+    """The shape and type of a matrix that no call can do without."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D matrix")
+    return tuple(t.shape), t.dtype
 
 
 def _config(shape, res_dtype, dtype, w_post, w_pre, gate, rows_per_gate, eps, branch_scale,
@@ -45,7 +64,11 @@ def _config(shape, res_dtype, dtype, w_post, w_pre, gate, rows_per_gate, eps, br
     """The call's config, the type of its parameters and its gate's shape."""
     rows, hidden = shape
     first = w_post if w_post is not None else w_pre if w_pre is not None else gate
-    ptype = dtype if first is None else first.dtype
+    try:
+        ptype = dtype if first is None else first.dtype
+    except AttributeError:
+        name = "w_post" if first is w_post else "w_pre" if first is w_pre else "gate"
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if rows_per_gate is None:
         rows_per_gate = max(rows, 1)
     groups = (-(-rows // rows_per_gate) if rows_per_gate > 0 else 0, hidden)
@@ -71,14 +94,12 @@ def block_norm(u, res, res_out=None, y=None, w_post=None, w_pre=None, gate=None,
     i // rows_per_gate (default: one gate row for all).  rstd_post, rstd_pre
     fp32 [rows]: kept for the backward pass.  With scale, amax and scale_inv
     (fp32 scalars) y is FP8 of format fmt, cast as fp8_cast does."""
-    if res.dim() != 2:
-        raise ValueError("res must be a 2-D matrix")
-    shape, rtype = tuple(res.shape), res.dtype
+    shape, rtype = _matrix(res, "res")
     rows = shape[:1]
     if u is not None:
-        dtype = u.dtype
+        dtype = _dtype_of(u, "u")
     else:
-        dtype = y.dtype if y is not None and scale is None else rtype
+        dtype = _dtype_of(y, "y") if y is not None and scale is None else rtype
     cfg, _, _ = _config(shape, rtype, dtype, w_post, w_pre, gate, rows_per_gate, eps, branch_scale,
                         residual_scale, weight_offset, post_norm, pre_norm)
     _check(lib().block_norm(
@@ -100,15 +121,13 @@ def block_norm_backward(dy, dres_out, u, res_out, rstd_post, rstd_pre, du=None, 
                         residual_scale=1.0, weight_offset=0.0, post_norm=True, pre_norm=True,
                         noop_flag=None, stream=None) -> None:
     """From dy (of y) and dres_out (of res_out; None: zero), and the forward
-    pass's u, res_out (res where there was no u), rstd_post and rstd_pre: du,
-    dres, and those of dw_post, dw_pre, dgate that are given, in the
+    pass's u, res_out (res where there was no u), rstd_post and rstd_pre: du
+    (with u), dres (always), and those of dw_post, dw_pre, dgate that are given, in the
     parameters' type.  workspace: uint8, of at least
     block_norm_backward_workspace_size(rows, hidden) bytes."""
-    if dres.dim() != 2:
-        raise ValueError("dres must be a 2-D matrix")
-    shape, rtype = tuple(dres.shape), dres.dtype
+    shape, rtype = _matrix(dres, "dres")
     rows, columns = shape[:1], shape[1:]
-    dtype = u.dtype if u is not None else dy.dtype
+    dtype = _dtype_of(u, "u") if u is not None else _dtype_of(dy, "dy")
     cfg, ptype, groups = _config(shape, rtype, dtype, w_post, w_pre, gate, rows_per_gate, 0.0,
                                  branch_scale, residual_scale, weight_offset, post_norm, pre_norm)
     if w_post is None and w_pre is None and gate is None and not (

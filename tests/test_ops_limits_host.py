@@ -110,3 +110,34 @@ def test_limits_of_hidden_and_of_a_sorted_matrix(L):
         assert call(2 ** 20 + 1, 1) == SHAPE
         assert call(2 ** 20, 2 ** 20 + 1) == SHAPE
         assert call(2 ** 20, 2 ** 20) == ALIGN          # within them
+
+
+def test_norm_errors_name_the_argument():
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="dres"):            # the signature's default
+        ct.block_norm_backward(x, None, x, x, None, None, x)
+    with pytest.raises(TypeError, match="dy"):              # neither u nor dy: no type
+        ct.block_norm_backward(None, None, None, x, None, None, None, x)
+    with pytest.raises(TypeError, match="res"):
+        ct.block_norm(x, None, x, x)
+    with pytest.raises(TypeError, match="u must"):
+        ct.block_norm([1.0], x, x, x)
+    with pytest.raises(TypeError, match="w_pre"):
+        ct.block_norm(x, x, x, x, w_pre=1.0)
+    with pytest.raises(ValueError, match="res"):
+        ct.block_norm(x, x[0], x, x)
+    with pytest.raises(ValueError, match="dres"):
+        ct.block_norm_backward(x, None, x, x, None, None, x, x[0])
+
+
+class Gpu(torch.Tensor):
+    """A CPU tensor that says it is on a GPU: as far as the binding's checks go."""
+    is_cuda = True
+
+
+def test_norm_outputs_of_another_kind_are_named():
+    x = torch.zeros(4, 8, dtype=torch.bfloat16).as_subclass(Gpu)
+    with pytest.raises(TypeError, match="res_out must"):
+        ct.block_norm(x, x, 3.0, x)
+    with pytest.raises(TypeError, match="du must"):
+        ct.block_norm_backward(x, None, x, x, None, None, "du", x)
