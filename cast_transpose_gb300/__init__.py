@@ -171,10 +171,14 @@ _U8 = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 
 def _stream(stream) -> int:
     """The stream's handle; None: the current one's, without the Stream object
-    around it (0.2 us a call against 2.8)."""
-    if stream is None:
+    around it (0.2 us a call against 2.8) where torch has the private functions
+    for that."""
+    if stream is not None:
+        return stream.cuda_stream
+    try:
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t, name, dtype, shape) -> int:

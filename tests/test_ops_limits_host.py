@@ -141,3 +141,17 @@ def test_norm_outputs_of_another_kind_are_named():
         ct.block_norm(x, x, 3.0, x)
     with pytest.raises(TypeError, match="du must"):
         ct.block_norm_backward(x, None, x, x, None, None, "du", x)
+
+
+def test_current_stream_without_torchs_private_names(monkeypatch):
+    """The handle comes from two private functions of torch; where a version
+    has them no longer, from the public call."""
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    assert ct._stream(None) == 0x1234
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    assert ct._stream(None) == 0x1234
+    assert ct._stream(Stream) == 0x1234
