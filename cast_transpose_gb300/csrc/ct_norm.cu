@@ -35,7 +35,6 @@
 
 #include <algorithm>
 #include <mutex>
-#include <vector>
 
 namespace ct {
 namespace {
@@ -1293,18 +1292,24 @@ cudaError_t prepare(const void* kernel, NormShape& s, size_t smem) {
         size_t smem;
         int most;
     };
+    // the latest shapes; one that has been displaced is looked up again
+    constexpr int kKnown = 256;
     static std::mutex mutex;
-    static std::vector<Known> known;
+    static Known known[kKnown];
+    static unsigned remembered = 0;
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mutex);
-    for (const Known& k : known)
+    const int count = static_cast<int>(std::min(remembered, unsigned(kKnown)));
+    for (int i = 0; i < count; ++i) {
+        const Known& k = known[i];
         if (k.kernel == kernel && k.device == device && k.cluster == s.cluster &&
             k.threads == threads_of(s.width) && k.smem == smem) {
             if (s.lead) s.clusters = std::min(s.clusters, k.most);
             return cudaSuccess;
         }
+    }
     Known k = {kernel, device, s.cluster, threads_of(s.width), smem, s.clusters};
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - kSmemFixed);
     if (e == cudaSuccess)
@@ -1320,7 +1325,8 @@ cudaError_t prepare(const void* kernel, NormShape& s, size_t smem) {
         if (e != cudaSuccess) return e;
         k.most = std::max(most, 1);
     }
-    known.push_back(k);
+    known[remembered++ % kKnown] = k;
+    if (remembered == 2u * kKnown) remembered = kKnown;   // so that it never wraps
     if (s.lead) s.clusters = std::min(s.clusters, k.most);
     return cudaSuccess;
 }

@@ -1,5 +1,9 @@
 """Further host-side checks of the expert-movement and block-norm operators (no
 GPU needed): limits, refusals and their messages, the plan's attributes."""
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -155,3 +159,13 @@ def test_current_stream_without_torchs_private_names(monkeypatch):
     monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
     assert ct._stream(None) == 0x1234
     assert ct._stream(Stream) == 0x1234
+
+
+@pytest.mark.skipif(shutil.which("nm") is None, reason="needs nm")
+@pytest.mark.parametrize("unit", ["ct_moe", "ct_moe_cast", "ct_norm", "ct_ops_api"])
+def test_a_launch_needs_no_host_memory(unit):
+    """An allocation that failed would leave the C entry point as an exception:
+    the library's own objects ask for none."""
+    path = os.path.join(os.path.dirname(ct.__file__), "_build", unit + ".o")
+    wanted = subprocess.run(["nm", "-uC", path], capture_output=True, text=True, check=True).stdout
+    assert "operator new" not in wanted and "__throw_length_error" not in wanted
