@@ -21,6 +21,8 @@ synchronised, everything can be captured in a CUDA graph.
 """
 from __future__ import annotations
 
+from operator import attrgetter
+
 import torch
 
 from . import E4M3, _check, _dev, _opt, _ptr, _stream, _U8, lib
@@ -37,7 +39,7 @@ def moe_sorted_rows(tokens: int, topk: int, experts: int, align: int = 1) -> int
 
 
 def _kept(name):
-    return property(lambda self: getattr(self, "_" + name))
+    return property(attrgetter("_" + name))
 
 
 class MoePlan:
@@ -78,11 +80,14 @@ class MoePlan:
         self._workspace_size = int(lib().moe_sort_workspace_size(tokens, topk, experts))
         self._workspace = torch.empty(self._workspace_size, dtype=torch.uint8,
                                       device=self._row_of.device)
-        # checked once, here; their addresses are taken at each call
+        # checked once, here; each call asks for their addresses
         _ptr(self._row_of, "row_of", _I32, self._slots)
         _ptr(self._src, "src", _I32, (rows,))
         _ptr(self._offsets, "offsets", _I32, (experts + 1,))
         _ptr(self._counts, "counts", _I32, (experts,))
+        self._row_of_at, self._src_at = self._row_of.data_ptr, self._src.data_ptr
+        self._offsets_at, self._counts_at = self._offsets.data_ptr, self._counts.data_ptr
+        self._workspace_at = self._workspace.data_ptr
 
 
 def _rows_of(t, name):
@@ -103,9 +108,9 @@ def moe_sort(expert_idx, plan: MoePlan, noop_flag=None, stream=None) -> None:
     idx = _ptr(expert_idx, "expert_idx", dtype if dtype in _INDEX else _INDEX, plan._slots)
     size = plan._workspace_size
     _check(lib().moe_sort(idx, 4 if dtype is _I32 else 8, plan._tokens, plan._topk,
-                          plan._experts, plan._align, plan._rows, plan._row_of.data_ptr(),
-                          plan._src.data_ptr(), plan._offsets.data_ptr(), plan._counts.data_ptr(),
-                          plan._workspace.data_ptr() if size else None, size,
+                          plan._experts, plan._align, plan._rows, plan._row_of_at(),
+                          plan._src_at(), plan._offsets_at(), plan._counts_at(),
+                          plan._workspace_at() if size else None, size,
                           _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
@@ -115,7 +120,7 @@ def moe_dispatch(x, plan: MoePlan, out, noop_flag=None, stream=None) -> None:
     px = _ptr(x, "x", dtype, (plan._tokens, hidden))
     po = _ptr(out, "out", dtype, (plan._rows, hidden))
     _check(lib().moe_dispatch(px, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
-                              plan._row_of.data_ptr(), plan._src.data_ptr(), plan._rows, po,
+                              plan._row_of_at(), plan._src_at(), plan._rows, po,
                               _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
@@ -125,7 +130,7 @@ def moe_dispatch_backward(dout, plan: MoePlan, dx, noop_flag=None, stream=None) 
     pd = _ptr(dout, "dout", dtype, (plan._rows, hidden))
     px = _ptr(dx, "dx", dtype, (plan._tokens, hidden))
     _check(lib().moe_dispatch_backward(pd, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
-                                       plan._row_of.data_ptr(), plan._rows, px,
+                                       plan._row_of_at(), plan._rows, px,
                                        _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
@@ -139,7 +144,7 @@ def fp8_moe_dispatch(x, plan: MoePlan, scale, amax, scale_inv, out, out_t=None, 
     po = _ptr(out, "out", _U8, (plan._rows, hidden))
     pt = None if out_t is None else _ptr(out_t, "out_t", _U8, (hidden, plan._rows))
     pw = None if weights is None else _ptr(weights, "weights", _F32, plan._slots)
-    _check(lib().fp8_moe_dispatch(px, plan._tokens, plan._topk, hidden, plan._src.data_ptr(),
+    _check(lib().fp8_moe_dispatch(px, plan._tokens, plan._topk, hidden, plan._src_at(),
                                   plan._rows, pw, _dev(scale, "scale", _F32, 1), _dev(amax, "amax", _F32, 1),
                                   _dev(scale_inv, "scale_inv", _F32, 1), po, pt, fmt,
                                   _opt(noop_flag, "noop_flag"), _stream(stream)))
@@ -151,7 +156,7 @@ def moe_combine(ys, plan: MoePlan, weights, out, noop_flag=None, stream=None) ->
     py = _ptr(ys, "ys", dtype, (plan._rows, hidden))
     po = _ptr(out, "out", dtype, (plan._tokens, hidden))
     _check(lib().moe_combine(py, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
-                             plan._row_of.data_ptr(), _ptr(weights, "weights", _F32, plan._slots),
+                             plan._row_of_at(), _ptr(weights, "weights", _F32, plan._slots),
                              plan._rows, po, _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
@@ -165,6 +170,6 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
     ps = None if dys is None else _ptr(dys, "dys", dtype, (plan._rows, hidden))
     pw = None if dweights is None else _ptr(dweights, "dweights", _F32, plan._slots)
     _check(lib().moe_combine_backward(pd, py, plan._tokens, plan._topk, hidden, _DTYPES[dtype],
-                                      plan._row_of.data_ptr(), plan._src.data_ptr(),
+                                      plan._row_of_at(), plan._src_at(),
                                       _ptr(weights, "weights", _F32, plan._slots), plan._rows, ps,
                                       pw, _opt(noop_flag, "noop_flag"), _stream(stream)))
