@@ -238,7 +238,7 @@ const char* ct_status_string(int status) {
         case CT_ERR_NULL: return "CT_ERR_NULL: a required pointer is NULL";
         case CT_ERR_SHAPE: return "CT_ERR_SHAPE: invalid matrix shape";
         case CT_ERR_ALIGN: return "CT_ERR_ALIGN: misaligned buffer";
-        case CT_ERR_FORMAT: return "CT_ERR_FORMAT: unknown FP8 format";
+        case CT_ERR_FORMAT: return "CT_ERR_FORMAT: unknown FP8 format or data type";
         case CT_ERR_ARG: return "CT_ERR_ARG: invalid argument";
         case CT_ERR_ALIAS: return "CT_ERR_ALIAS: overlapping buffers";
         case CT_ERR_WORKSPACE: return "CT_ERR_WORKSPACE: workspace missing or too small";

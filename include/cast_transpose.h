@@ -97,7 +97,8 @@ typedef enum {
     CT_ERR_NULL = 1,        /* a required pointer is NULL                      */
     CT_ERR_SHAPE = 2,       /* negative size, or a size the kernels cannot index */
     CT_ERR_ALIGN = 3,       /* buffer misaligned for its element type          */
-    CT_ERR_FORMAT = 4,      /* fmt is not CT_E4M3 / CT_E5M2                    */
+    CT_ERR_FORMAT = 4,      /* fmt is not CT_E4M3 / CT_E5M2, or a ct_dtype is
+                               none or does not go with the others             */
     CT_ERR_ARG = 5,         /* other invalid scalar (history length, margin)   */
     CT_ERR_ALIAS = 6,       /* an output overlaps an input or another output   */
     CT_ERR_WORKSPACE = 7,   /* workspace missing or too small                  */

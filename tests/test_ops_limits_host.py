@@ -169,3 +169,8 @@ def test_a_launch_needs_no_host_memory(unit):
     path = os.path.join(os.path.dirname(ct.__file__), "_build", unit + ".o")
     wanted = subprocess.run(["nm", "-uC", path], capture_output=True, text=True, check=True).stdout
     assert "operator new" not in wanted and "__throw_length_error" not in wanted
+
+
+def test_a_refused_data_type_is_called_that(L):
+    assert L.moe_dispatch(A, 1, 1, 8, 3, B, C, 1, D, None, None) == FORMAT
+    assert "data type" in L.ct_status_string(FORMAT).decode()
