@@ -21,7 +21,7 @@ using dev::pdl_wait;
 // its expert's is (slots of earlier blocks) + (of earlier warps) + (earlier in
 // the warp's run): the first two are exclusive sums of counts, the third is
 // counted on the way, 32 slots at a time, from the lanes with the same expert.
-// Integers only, no atomics.  What it moves is small (12 bytes a slot); the
+// Integers only; no order depends on atomics.  What it moves is small (12 bytes a slot); the
 // time is latency, so blocks learn each other's counts in the cheapest way
 // their number allows:
 //   kOne      one block, up to kSortOneBlock slots

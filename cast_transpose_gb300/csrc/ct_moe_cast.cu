@@ -40,7 +40,10 @@ __device__ __forceinline__ unsigned max_bits(unsigned m, float v) {
 // the measured copy rate; the rest is issue (60% of the slots) and the last
 // wave of blocks.  With the sort before it: one tile a block 217 us, strips of
 // 2 / 4 / 8 196 / 190 / 208; whole tiles without checks, 180; one barrier a
-// tile, 175; single tiles in the last wave, 173.  Tiles stacked down the rows instead of side by side: 187.
+// tile, 175; single tiles in the last wave, 173.  Tiles stacked down the rows
+// instead of side by side: 187.  Four blocks per SM hold a thread to 64
+// registers: with the transpose it spills one word, with the weights six, but
+// three blocks with more registers take 204.
 template <int FMT, bool WEIGHTED, bool TRANSPOSE>
 __global__ void __launch_bounds__(kCastThreads, 4)
     sorted_cast_kernel(const SortedCastArgs a, int tile_rows, int tile_cols, int whole_strips) {

@@ -43,7 +43,8 @@ constexpr int kPer = 2;               // groups of eight columns per thread
 // Threads of a block: forward, two blocks with 80 registers a thread (512 with
 // 64 do not hold a row's u: 8191x6144 72.5 us, so: 68.8); backward, one with
 // 168, which its column sums and the compiler's room to interleave columns need
-// (8192x6144, 512 with 128: 109 us, so: 106; 12288x4096: 131, so: 119).
+// (8192x6144, 512 with 128: 109 us, so: 106; 12288x4096: 131, so: 119, where
+// blocks of 256 threads leave a third of the registers unused).
 constexpr int kForwardThreads = 384, kBackwardThreads = 384;
 constexpr int kMaxThreads = kForwardThreads;
 constexpr int kMaxCluster = 8;
@@ -1128,7 +1129,8 @@ __global__ void __launch_bounds__(kSelftestThreads) norm_wait_selftest_kernel(in
 // from 2 on the gate rows that more than one run has rows of, by gate row
 // (few of them, perhaps of many runs), else by the run they begin in.
 //
-// A block takes `cols` columns (32, or 8, one sector, of short rows) and gives each blockDim / cols threads, which add up every so many-th run.
+// A block takes `cols` columns (32, or 8, one sector, of short rows) and gives
+// each blockDim / cols threads, which add up every so many-th run.
 constexpr int kJoinThreads = 512;      // at most
 
 template <typename T>
@@ -1366,7 +1368,8 @@ cudaError_t launch_block_norm(const NormArgs& a, int dtype, int res_dtype, cudaS
         using R = decltype(r);
         size_t smem;
         const bool full = a.u && a.post && a.pre;
-        const int min_lead = full && vec && sizeof(T) == 2 ? 2 : 3;   // rows i+1, i+2, and i unless it is kept
+        // rows i+1, i+2, and i unless it is kept
+        const int min_lead = full && vec && sizeof(T) == 2 ? 2 : 3;
         NormShape s = shape_of(a.rows, a.hidden, sizeof(T), sizeof(R), 1, min_lead, vec, kForwardThreads,
                                2 * kForwardThreads, a.rows, &smem);
         auto* kernel = s.lead ? (vec ? (full ? block_norm_kernel<T, R, 8, true> : block_norm_kernel<T, R, 8, false>)
