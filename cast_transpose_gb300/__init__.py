@@ -17,6 +17,10 @@ Operations (TransformerEngine pages "[PyTorch] cuda graph support" and
   fp8_cast                  cast without transpose
   MoePlan, moe_*, fp8_moe_dispatch   tokens sorted by expert and back (moe.py)
   block_norm, block_norm_backward    norm, gate, residual sum, norm (norms.py)
+  layer_norm, layer_norm_backward    dropout, residual sum, layer norm (norms.py)
+  moe_router, moe_router_backward    experts, weights, counts, balance loss (moe.py)
+  embedding, embedding_backward      rows of a table by token id (embeddings.py)
+  dropout                            with nothing stored (dropouts.py)
 Every call accepts ``noop_flag``: a CUDA fp32 scalar tensor; when it holds a
 nonzero value at run time the kernels write nothing.
 """
@@ -121,7 +125,22 @@ def lib() -> ctypes.CDLL:
             L.block_norm_backward_workspace_size.restype = c.c_size_t
             L.block_norm_backward_workspace_size.argtypes = [i64, i64]
             L.block_norm_backward.argtypes = [vp] * 13 + [c.c_size_t, vp, vp]
-            for name in ("moe_sort", "moe_dispatch", "moe_dispatch_backward", "fp8_moe_dispatch",
+            L.dropout.argtypes = [vp, i64, i64, i32, c.c_float, vp, c.c_uint32, vp, vp, vp]
+            L.layer_norm.argtypes = [vp] * 10 + [i32, vp, vp]
+            L.layer_norm_backward_workspace_size.restype = c.c_size_t
+            L.layer_norm_backward_workspace_size.argtypes = [i64, i64]
+            L.layer_norm_backward.argtypes = [vp] * 11 + [c.c_size_t, vp, vp]
+            L.moe_router_workspace_size.restype = c.c_size_t
+            L.moe_router_workspace_size.argtypes = [i64, i32, i32]
+            L.moe_router.argtypes = [vp] * 8 + [c.c_size_t, vp, vp]
+            L.moe_router_backward.argtypes = [vp] * 10
+            L.embedding.argtypes = [vp, i32, i64, vp, i64, i64, i32, c.c_float, vp, vp, vp]
+            L.embedding_backward_workspace_size.restype = c.c_size_t
+            L.embedding_backward_workspace_size.argtypes = [i64, i64, i64]
+            L.embedding_backward.argtypes = [vp, i32, i64, vp, i64, i64, i32, c.c_float, vp, i32,
+                                             i32, vp, c.c_size_t, vp, vp]
+            for name in ("dropout", "layer_norm", "layer_norm_backward", "moe_router",
+                         "moe_router_backward", "embedding", "embedding_backward", "moe_sort", "moe_dispatch", "moe_dispatch_backward", "fp8_moe_dispatch",
                          "moe_combine", "moe_combine_backward", "block_norm",
                          "block_norm_backward",
                          "fp8_cast_transpose", "fp8_cast_transpose_ex", "fp8_cast",
@@ -192,6 +211,37 @@ def _ptr(t, name, dtype, shape) -> int:
     if isinstance(t, torch.Tensor) and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return _dev(t, name, dtype)
+
+
+def _given(t, name, dtype, shape):
+    """_ptr of an optional tensor."""
+    return None if t is None else _ptr(t, name, dtype, shape)
+
+
+def _here(stream, *tensors) -> int:
+    """The stream's handle, as _stream, for a call whose tensors (or None) and
+    stream have to be the current device's."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{device}")
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is "
+                         f"cuda:{device}")
+    return _stream(stream)
+
+
+_RNG = (2,)
+
+
+def _random(rng, p, site):
+    """The address of a generator's state (None: nothing is dropped)."""
+    if not 0 <= site < 1 << 32:
+        raise ValueError(f"site is {site}, expected 0 .. 2^32 - 1")
+    if rng is None and p * 65536 >= 0.5:
+        raise ValueError("a dropout needs rng: int64 [2], seed and step")
+    return _given(rng, "rng", torch.int64, _RNG)
 
 
 def _rc(x: torch.Tensor):
@@ -389,7 +439,12 @@ def empty_outputs(x: torch.Tensor):
             torch.empty(cols, rows, dtype=torch.uint8, device=x.device))
 
 
+from .dropouts import dropout  # noqa: E402
+from .embeddings import (embedding, embedding_backward,  # noqa: E402
+                         embedding_backward_workspace_size)
 from .moe import (MoePlan, fp8_moe_dispatch, moe_combine, moe_combine_backward,  # noqa: E402
-                  moe_dispatch, moe_dispatch_backward, moe_sort, moe_sorted_rows)
+                  moe_dispatch, moe_dispatch_backward, moe_router, moe_router_backward,
+                  moe_router_workspace_size, moe_sort, moe_sorted_rows)
 from .norms import (block_norm, block_norm_backward,  # noqa: E402
-                    block_norm_backward_workspace_size)
+                    block_norm_backward_workspace_size, layer_norm, layer_norm_backward,
+                    layer_norm_backward_workspace_size)

@@ -1,0 +1,95 @@
+// ct_dropout.cuh -- which elements a dropout keeps, from a counter-based
+// generator: nothing is stored, and whoever knows the seed, the step and the
+// place gets the same answer.
+//
+// The generator is Philox4x32 with ten rounds (Salmon, Moraes, Dror and Shaw,
+// "Parallel random numbers: as easy as 1, 2, 3", 2011).  One call gives eight
+// columns of a row 16 bits each: 32 bits each would double its cost, which is
+// what a dropout computes (some 60 operations a call), for chances finer than
+// 1/65536.
+//   counter  (column / 8, row, site, step mod 2^32)      key  the seed
+//   column j: half j % 2 (0: the lower) of word (j % 8) / 2
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ct_ops.h"
+
+namespace ct {
+namespace {
+
+__device__ __forceinline__ uint4 philox4x32(uint4 c, uint2 k) {
+#pragma unroll
+    for (int round = 0; round < 10; ++round) {
+        const uint64_t a = uint64_t(0xD2511F53u) * c.x, b = uint64_t(0xCD9E8D57u) * c.z;
+        c = make_uint4(uint32_t(b >> 32) ^ c.y ^ k.x, uint32_t(b), uint32_t(a >> 32) ^ c.w ^ k.y, uint32_t(a));
+        k.x += 0x9E3779B9u;
+        k.y += 0xBB67AE85u;
+    }
+    return c;
+}
+
+// The generator of one call, as its kernel uses it.
+struct Drops {
+    uint2 key;
+    uint32_t site, step;
+    uint32_t cut;           // dropped: 16 bits below this / 65536
+    float scale;            // of what is kept
+    bool some;              // anything to drop
+
+    __device__ __forceinline__ explicit Drops(const DropArgs& a) {
+        some = a.cut != 0;
+        cut = a.cut << 16;
+        scale = a.scale;
+        site = a.site;
+        if (!some) return;
+        const ulonglong2 s = make_ulonglong2(a.rng[0], a.rng[1]);
+        key = make_uint2(uint32_t(s.x), uint32_t(s.x >> 32));
+        step = uint32_t(s.y);
+    }
+    // Bit j: column 8 * group + j of the row is kept.
+    __device__ __forceinline__ uint32_t kept8(uint32_t row, uint32_t group) const {
+        const uint4 r = philox4x32(make_uint4(group, row, site, step), key);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bits |= ((w[i] << 16) >= cut ? 1u : 0u) << (2 * i);
+            bits |= (w[i] >= cut ? 1u : 0u) << (2 * i + 1);
+        }
+        return bits;
+    }
+    // Of a thread's columns Cols<G>(vi) of a row: its own group is group0 + vi,
+    // and where its columns are spread over the warp's 32 groups the lanes pass
+    // each other their bits.  The whole warp has to call it.
+    template <int G>
+    __device__ __forceinline__ uint32_t kept(uint32_t row, uint32_t group) const {
+        const uint32_t own = kept8(row, group);
+        if constexpr (G == 8) return own;
+        const int lane = threadIdx.x & 31;
+        uint32_t bits = 0;
+        if constexpr (G == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t m = __shfl_sync(0xFFFFFFFFu, own, 8 * i + (lane >> 2));
+                bits |= ((m >> ((2 * lane) & 7)) & 3u) << (2 * i);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t m = __shfl_sync(0xFFFFFFFFu, own, 4 * j + (lane >> 3));
+                bits |= ((m >> (lane & 7)) & 1u) << j;
+            }
+        }
+        return bits;
+    }
+    // v scaled where its bit is set, else 0, whatever v is.
+    __device__ __forceinline__ void apply(uint32_t bits, float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (bits >> j) & 1 ? v[j] * scale : 0.0f;
+    }
+};
+
+}  // namespace
+}  // namespace ct

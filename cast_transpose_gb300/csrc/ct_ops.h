@@ -1,5 +1,5 @@
-// ct_ops.h -- kernel arguments and launchers of the expert-movement and
-// block-norm operators.  Not installed.
+// ct_ops.h -- kernel arguments and launchers of the operators around the FP8
+// casts: expert movement, router, norms, dropout and embedding.  Not installed.
 #pragma once
 
 #include "ct_internal.h"
@@ -102,6 +102,86 @@ struct NormBackwardArgs {
 size_t norm_backward_workspace(int64_t rows, int64_t hidden);
 cudaError_t launch_block_norm_backward(const NormBackwardArgs& a, int dtype, int res_dtype,
                                        cudaStream_t stream);
+
+// A dropout: 16 random bits below `cut` drop an element, what stays is scaled.
+struct DropArgs {
+    const uint64_t* rng;   // seed and step; not read where cut is 0
+    uint32_t site, cut;
+    float scale;
+};
+
+struct DropoutArgs {
+    DropArgs drop;
+    const void* x;
+    void* out;
+    const float* noop;
+    int64_t rows, cols;
+};
+cudaError_t launch_dropout(const DropoutArgs& a, int dtype, cudaStream_t stream);
+
+struct LayerNormArgs {
+    DropArgs drop;
+    const void *u, *res, *weight, *bias;
+    void *res_out, *y;
+    float *mean, *rstd;
+    const float* scale;    // not null: y is FP8
+    float* amax;
+    float* scale_inv;
+    const float* noop;
+    int64_t rows;
+    float eps, weight_offset;
+    int hidden, param_f32, fmt;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int res_dtype, cudaStream_t stream);
+
+struct LayerNormBackwardArgs {
+    DropArgs drop;
+    const void *dy, *dres_out, *res_out, *weight;
+    const float *mean, *rstd;
+    void *dres, *du, *dweight, *dbias;
+    float* workspace;
+    const float* noop;
+    int64_t rows;
+    float weight_offset;
+    int hidden, param_f32;
+};
+size_t layer_norm_backward_workspace(int64_t rows, int64_t hidden);
+cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype, int res_dtype,
+                                       cudaStream_t stream);
+
+struct RouterArgs {
+    const void* logits;    // [tokens, experts]
+    const uint8_t* mask;   // [tokens], or null
+    int* idx;              // [tokens, topk]; read by the backward pass
+    float* weights;        // [tokens, topk]
+    int* counts;           // [experts + 1]; read by the backward pass
+    float* loss;           // or null
+    const float* dweights; // or null
+    const float* dloss;    // or null
+    void* dlogits;         // [tokens, experts]
+    void* workspace;
+    const float* noop;
+    int64_t tokens;
+    float balance, z;
+    int experts, topk, normalize;
+};
+size_t router_workspace(int64_t tokens, int topk, int experts);
+cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_router_backward(const RouterArgs& a, int dtype, cudaStream_t stream);
+
+struct EmbeddingArgs {
+    const void* idx;       // [tokens] int32, or int64 (index64)
+    const void* in;        // [vocab, hidden] the table, or [tokens, hidden] dout
+    void* out;             // [tokens, hidden], or [vocab, hidden] dtable
+    void* workspace;
+    const float* noop;
+    int64_t tokens, vocab, hidden;
+    float scale;
+    int index64, accumulate, grad_f32;
+};
+cudaError_t launch_embedding(const EmbeddingArgs& a, int dtype, cudaStream_t stream);
+size_t embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden);
+cudaError_t launch_embedding_backward(const EmbeddingArgs& a, int dtype, cudaStream_t stream);
 
 // The block-norm kernels' own diagnostic word, as read_device_error.
 cudaError_t read_norm_error(unsigned* value, bool clear);

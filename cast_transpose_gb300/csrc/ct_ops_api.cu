@@ -4,48 +4,19 @@
 #include "ct_checks.h"
 #include "ct_ops.h"
 
-#include <initializer_list>
-
 namespace {
 
-using ct::aligned;
 using ct::cuda_status;
-using ct::overlap;
-using ct::Range;
-using ct::range_of;
 
 using ct::kMaxExperts;
 constexpr int kMaxTopk = 64, kMaxAlign = 1024;
-constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxElements = int64_t(1) << 40;   // of a sorted matrix
-constexpr int64_t kMaxMoveHidden = int64_t(1) << 20, kMaxNormHidden = 32768;
-
-bool dtype_ok(int d) { return d == CT_BF16 || d == CT_FP16 || d == CT_FP32; }
-int elem_bytes(int d) { return d == CT_FP32 ? 4 : 2; }
-
-// A buffer of a call: null only where `optional`, aligned to `align`.
-struct Buffer {
-    const void* p;
-    int64_t bytes;
-    int align;
-    bool written;
-    bool optional = false;
-};
-
-// Buffers of no bytes are not checked (an empty matrix may have any pointer).
-int check_buffers(std::initializer_list<Buffer> buffers) {
-    for (const Buffer& b : buffers)
-        if (!b.p && !b.optional && b.bytes > 0) return CT_ERR_NULL;
-    for (const Buffer& b : buffers)
-        if (b.p && b.bytes > 0 && !aligned(b.p, b.align)) return CT_ERR_ALIGN;
-    for (const Buffer& w : buffers) {
-        if (!w.written || !w.p) continue;
-        for (const Buffer& o : buffers)
-            if (&o != &w && o.p && overlap(range_of(w.p, w.bytes), range_of(o.p, o.bytes)))
-                return CT_ERR_ALIAS;
-    }
-    return CT_OK;
-}
+using ct::dtype_ok;
+using ct::elem_bytes;
+using ct::check_buffers;
+using ct::kMaxElements;
+using ct::kMaxIndex;
+using ct::kMaxNormHidden;
+constexpr int64_t kMaxMoveHidden = int64_t(1) << 20;
 
 int check_move(int64_t tokens, int topk, int64_t hidden, int64_t rows, int dtype) {
     if (!dtype_ok(dtype)) return CT_ERR_FORMAT;

@@ -8,6 +8,8 @@ plan of its own, reused from step to step; layers that only run forward can
 share one, each sorting before it moves.  A plan's buffers, its workspace among
 them, are used by one stream at a time.
 
+  moe_router             the choices, their weights and counts, the balance loss
+  moe_router_backward    the gradient of the router's logits
   moe_sort               the plan: which sorted row every (token, k) slot gets
   moe_dispatch           out[row] = x[token], padding rows zero
   moe_dispatch_backward  dx[token] = sum over k of dout[row]
@@ -21,11 +23,12 @@ synchronised, everything can be captured in a CUDA graph.
 """
 from __future__ import annotations
 
+import ctypes
 from operator import attrgetter
 
 import torch
 
-from . import E4M3, _check, _dev, _opt, _ptr, _stream, _U8, lib
+from . import E4M3, _check, _dev, _given, _here, _opt, _ptr, _stream, _U8, lib
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _I32, _F32 = torch.int32, torch.float32
@@ -173,3 +176,62 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
                                       plan._row_of_at(), plan._src_at(),
                                       _ptr(weights, "weights", _F32, plan._slots), plan._rows, ps,
                                       pw, _opt(noop_flag, "noop_flag"), _stream(stream)))
+
+
+class _RouterConfig(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int), ("topk", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("flags", ctypes.c_int), ("balance", ctypes.c_float),
+                ("z", ctypes.c_float)]
+
+
+def moe_router_workspace_size(tokens: int, topk: int, experts: int) -> int:
+    return int(lib().moe_router_workspace_size(tokens, topk, experts))
+
+
+def _router(logits, expert_idx, normalize, balance, z):
+    """The call's config, and the shape of what is per slot."""
+    experts, dtype = _rows_of(logits, "logits")
+    if not isinstance(expert_idx, torch.Tensor) or expert_idx.dim() != 2:
+        raise ValueError("expert_idx must be a 2-D matrix")
+    tokens, slots = logits.shape[0], (logits.shape[0], expert_idx.shape[1])
+    return _RouterConfig(tokens, experts, slots[1], _DTYPES[dtype], 1 if normalize else 0, balance,
+                         z), slots
+
+
+_MASK = (torch.bool, torch.uint8)
+
+
+def moe_router(logits, expert_idx, weights, counts, loss=None, mask=None, normalize=True,
+               balance=0.0, z=0.0, workspace=None, noop_flag=None, stream=None) -> None:
+    """logits [T, E] -> expert_idx int32 [T, K], the experts with the largest
+    logits, best first (as moe_sort takes it), weights fp32 [T, K] (as
+    moe_combine takes them), counts int32 [E + 1] (slots per expert; last, the
+    tokens that are not padding) and loss fp32 [1]: balance times the balance
+    loss plus z times the mean squared logsumexp.  weights are probabilities,
+    with normalize divided by their sum.  mask bool or uint8 [T]: 0 for padding
+    tokens, which choose expert -1.  workspace: uint8, of at least
+    moe_router_workspace_size(T, K, E) bytes."""
+    cfg, slots = _router(logits, expert_idx, normalize, balance, z)
+    _check(lib().moe_router(
+        ctypes.byref(cfg), _ptr(logits, "logits", logits.dtype, logits.shape),
+        _given(mask, "mask", _MASK, slots[:1]), _ptr(expert_idx, "expert_idx", _I32, slots),
+        _ptr(weights, "weights", _F32, slots), _ptr(counts, "counts", _I32, (cfg.experts + 1,)),
+        _opt(loss, "loss"), None if workspace is None else _dev(workspace, "workspace", torch.uint8),
+        0 if workspace is None else workspace.numel(), _opt(noop_flag, "noop_flag"),
+        _here(stream, logits, mask, expert_idx, weights, counts, loss, workspace, noop_flag)))
+
+
+def moe_router_backward(dweights, dloss, logits, expert_idx, counts, dlogits, mask=None,
+                        normalize=True, balance=0.0, z=0.0, noop_flag=None, stream=None) -> None:
+    """From dweights fp32 [T, K] and dloss fp32 [1] (either may be None: zero)
+    and the forward pass's logits, mask, expert_idx and counts: dlogits [T, E]
+    of the logits' type."""
+    cfg, slots = _router(logits, expert_idx, normalize, balance, z)
+    dtype, shape = logits.dtype, logits.shape
+    _check(lib().moe_router_backward(
+        ctypes.byref(cfg), _ptr(logits, "logits", dtype, shape),
+        _given(mask, "mask", _MASK, slots[:1]), _ptr(expert_idx, "expert_idx", _I32, slots),
+        _ptr(counts, "counts", _I32, (cfg.experts + 1,)),
+        _given(dweights, "dweights", _F32, slots), _opt(dloss, "dloss"),
+        _ptr(dlogits, "dlogits", dtype, shape), _opt(noop_flag, "noop_flag"),
+        _here(stream, logits, mask, expert_idx, counts, dweights, dloss, dlogits, noop_flag)))

@@ -8,6 +8,14 @@ residual sum and the norm before the next block, forward and backward.
 with rstd = 1 / sqrt(mean(square) + eps) of u's and of res_out's rows.  Either
 norm can be left out (post_norm, pre_norm), and so can the weights (1) and the
 gate (1).  Without u (before the first block) only y is made, of res.
+
+layer_norm is the junction of blocks whose norm is a layer norm:
+
+    res_out = res + dropout(u)
+    y       = (res_out - mean) * rstd * (weight_offset + weight) + bias
+
+with mean and rstd = 1 / sqrt(variance + eps) of res_out's rows; dropout as in
+dropouts.py, its choices made again in the backward pass.
 """
 from __future__ import annotations
 
@@ -15,7 +23,7 @@ import ctypes
 
 import torch
 
-from . import E4M3, _check, _dev, _opt, _ptr, _stream, _U8, lib
+from . import E4M3, _check, _dev, _here, _opt, _ptr, _random, _stream, _U8, lib
 from .moe import _DTYPES
 
 _F32 = torch.float32
@@ -143,3 +151,81 @@ def block_norm_backward(dy, dres_out, u, res_out, rstd_post, rstd_pre, du=None, 
         None if workspace is None else _dev(workspace, "workspace", torch.uint8),
         0 if workspace is None else workspace.numel(), _opt(noop_flag, "noop_flag"),
         _stream(stream)))
+
+
+class _LayerConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("rng", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("p", ctypes.c_float),
+                ("site", ctypes.c_uint32), ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int),
+                ("param_dtype", ctypes.c_int)]
+
+
+def _layer_config(shape, res_dtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site):
+    columns = shape[1:]
+    try:
+        types = _DTYPES[dtype], _DTYPES[res_dtype], _DTYPES[ptype]
+    except KeyError as e:
+        raise TypeError(f"dtype {e} is not bfloat16, float16 or float32") from None
+    return _LayerConfig(*shape, _given(weight, "weight", ptype, columns),
+                        _given(bias, "bias", ptype, columns), _random(rng, p, site), eps,
+                        weight_offset, p, site, *types)
+
+
+def layer_norm(u, res, res_out=None, y=None, weight=None, bias=None, eps=1e-5, weight_offset=0.0,
+               p=0.0, rng=None, site=0, mean=None, rstd=None, scale=None, amax=None,
+               scale_inv=None, fmt=E4M3, noop_flag=None, stream=None) -> None:
+    """u [rows, hidden] (or None), res -> res_out = res + dropout(u) (res itself
+    for an update in place; None without u) and y, its layer norm.  res is of
+    u's type or fp32; weight and bias are both of u's type or both fp32.  p, rng
+    and site: the dropout of u.  mean, rstd fp32 [rows]: kept for the backward
+    pass.  With scale, amax and scale_inv (fp32 scalars) y is FP8 of format fmt,
+    cast as fp8_cast does."""
+    shape, rtype = _matrix(res, "res")
+    rows = shape[:1]
+    if u is not None:
+        dtype = _dtype_of(u, "u")
+    else:
+        dtype = _dtype_of(y, "y") if scale is None else rtype
+    first = weight if weight is not None else bias
+    ptype = dtype if first is None else _dtype_of(first, "weight" if first is weight else "bias")
+    cfg = _layer_config(shape, rtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site)
+    _check(lib().layer_norm(
+        ctypes.byref(cfg), _given(u, "u", dtype, shape), _ptr(res, "res", rtype, shape),
+        _given(res_out, "res_out", rtype, shape),
+        _given(y, "y", dtype if scale is None else _U8, shape), _given(mean, "mean", _F32, rows),
+        _given(rstd, "rstd", _F32, rows), _opt(scale, "scale"), _opt(amax, "amax"),
+        _opt(scale_inv, "scale_inv"), fmt, _opt(noop_flag, "noop_flag"),
+        _here(stream, u, res, res_out, y, weight, bias, rng, mean, rstd, scale, amax, scale_inv,
+              noop_flag)))
+
+
+def layer_norm_backward_workspace_size(rows: int, hidden: int) -> int:
+    return int(lib().layer_norm_backward_workspace_size(rows, hidden))
+
+
+def layer_norm_backward(dy, dres_out, res_out, mean, rstd, dres, du=None, dweight=None, dbias=None,
+                        workspace=None, weight=None, weight_offset=0.0, p=0.0, rng=None, site=0,
+                        noop_flag=None, stream=None) -> None:
+    """From dy (of y), dres_out (of res_out; None: zero) and the forward pass's
+    res_out (without u: res), mean and rstd: dres, and those of du (with the
+    forward pass's p, rng and site), dweight and dbias that are given, the last
+    two of weight's type.  workspace: uint8, of at least
+    layer_norm_backward_workspace_size(rows, hidden) bytes."""
+    shape, rtype = _matrix(dres, "dres")
+    rows, columns = shape[:1], shape[1:]
+    dtype = _dtype_of(dy, "dy")
+    first = weight if weight is not None else dweight if dweight is not None else dbias
+    ptype = dtype if first is None else _dtype_of(
+        first, "weight" if first is weight else "dweight" if first is dweight else "dbias")
+    cfg = _layer_config(shape, rtype, dtype, ptype, weight, None, rng, 0.0, weight_offset, p, site)
+    _check(lib().layer_norm_backward(
+        ctypes.byref(cfg), _ptr(dy, "dy", dtype, shape), _given(dres_out, "dres_out", rtype, shape),
+        _ptr(res_out, "res_out", rtype, shape), _ptr(mean, "mean", _F32, rows),
+        _ptr(rstd, "rstd", _F32, rows), _ptr(dres, "dres", rtype, shape),
+        _given(du, "du", dtype, shape), _given(dweight, "dweight", ptype, columns),
+        _given(dbias, "dbias", ptype, columns),
+        None if workspace is None else _dev(workspace, "workspace", torch.uint8),
+        0 if workspace is None else workspace.numel(), _opt(noop_flag, "noop_flag"),
+        _here(stream, dy, dres_out, res_out, mean, rstd, dres, du, dweight, dbias, workspace,
+              weight, rng, noop_flag)))

@@ -619,6 +619,172 @@ int block_norm_backward(const ct_block_norm_config* cfg, const void* dy, const v
                         void* dgate, void* workspace, size_t workspace_bytes,
                         const float* noop_flag, void* stream);
 
+/* ==========================================================================
+ * Between the token ids and the FP8 products: embedding, dropout, layer norm
+ * and the router.  The pages have no counterpart to these calls.
+ *
+ * Common to them: buffers belong to the current device, the stream's; rows are
+ * dense, with no alignment beyond their element's (rows of a multiple of 16
+ * bytes in 16-byte-aligned buffers are moved as 16-byte vectors).  Arithmetic
+ * is fp32, rounded once to each output's type.  Every result is the same from
+ * call to call.  Buffers that a call writes must not overlap any other buffer,
+ * unless it says so.  A workspace holds nothing between calls; calls that may
+ * run at the same time (two streams, two graphs) need one each.
+ *
+ * Random numbers.  `rng` is a device array of two int64: a seed and a step.
+ * The kernels read it when they run, so a captured graph drops other elements
+ * once the step has been changed in place.  `site` tells the dropouts of one
+ * step apart (one number per place in the model).  Element (i, j) of a matrix
+ * is kept if 16 bits, half j % 2 (0: the lower) of word (j % 8) / 2 of
+ * Philox4x32-10 with the counter (j / 8, i, site, step mod 2^32) and the seed
+ * as its key (low word first), are not below `cut` = p * 65536 rounded to the
+ * nearest integer; then it is multiplied by 65536 / (65536 - cut).  A dropped
+ * element is 0 whatever it was.  Nothing is stored: the backward pass is given
+ * the same rng, site and p.  0 <= p, cut <= 65535, else CT_ERR_ARG; with cut = 0
+ * rng is not read and may be NULL.
+ *
+ * Errors: CT_ERR_NULL, CT_ERR_SHAPE, CT_ERR_ALIGN, CT_ERR_FORMAT (types, index
+ * size, fmt), CT_ERR_ARG (the other scalars), CT_ERR_ALIAS, CT_ERR_WORKSPACE,
+ * CT_ERR_CUDA.
+ * ========================================================================== */
+
+/*
+ * dropout -- out = dropout(x) of a matrix [rows, cols] of a ct_dtype; out may be
+ * x itself.  The same call on the gradient of out gives that of x.
+ * Limits: rows < 2^31, cols <= 2^30, rows * cols <= 2^40.
+ */
+int dropout(const void* x, int64_t rows, int64_t cols, int dtype, float p, const int64_t* rng,
+            uint32_t site, void* out, const float* noop_flag, void* stream);
+
+/*
+ * The junction between two blocks whose norm is a layer norm.  For every row:
+ *     res_out = res + dropout(u)
+ *     mean, rstd of res_out:  rstd = 1/sqrt(mean((res_out - mean)^2) + eps)
+ *     y       = (res_out - mean) * rstd * (weight_offset + weight) + bias
+ * (no weight: factor 1, no bias: 0).  u NULL (before the first block, or a norm
+ * alone): y of res; res_out is then NULL too, and p is not used.  y and the
+ * statistics are computed from res_out before its rounding.
+ */
+typedef struct {              /* a host struct, read during the call */
+    int64_t rows, hidden;     /* rows < 2^31, hidden <= 32768 */
+    const void* weight;       /* [hidden] of param_dtype, nullable */
+    const void* bias;         /* [hidden] of param_dtype, nullable */
+    const int64_t* rng;       /* device int64 [2] */
+    float eps, weight_offset, p;
+    uint32_t site;
+    int dtype;                /* ct_dtype of u and y */
+    int res_dtype;            /* of res and res_out: dtype or CT_FP32 */
+    int param_dtype;          /* of weight and bias: dtype or CT_FP32 */
+} ct_layer_norm_config;
+
+/*
+ * layer_norm -- the forward pass.
+ *   u, res, res_out [rows, hidden]; res_out may be res itself
+ *   y [rows, hidden] of type dtype, or, where `scale` is not NULL, uint8: y =
+ *     fp8(y * scale), with amax (max-merged, of y before the scale) and
+ *     scale_inv as in fp8_cast_transpose
+ *   mean, rstd  fp32 [rows], nullable: kept for the backward pass
+ */
+int layer_norm(const ct_layer_norm_config* cfg, const void* u, const void* res, void* res_out,
+               void* y, float* mean, float* rstd, const float* scale, float* amax,
+               float* scale_inv, int fmt, const float* noop_flag, void* stream);
+
+/* Bytes of workspace layer_norm_backward needs for dweight and dbias (16-byte
+ * aligned; 0 for few rows). */
+size_t layer_norm_backward_workspace_size(int64_t rows, int64_t hidden);
+
+/*
+ * layer_norm_backward -- from dy (of y), dres_out (of res_out; NULL: zero), the
+ * forward pass's res_out (without u: res), mean and rstd; the config's eps and
+ * bias are not used.
+ *   dres [rows, hidden] of type res_dtype
+ *   du   [rows, hidden] of type dtype, nullable: dropout(dres), with the forward
+ *        pass's rng, site and p; without du they are not used
+ *   dweight, dbias [hidden] of param_dtype, each nullable: column sums, fp32 in
+ *        a fixed order.  With rows = 0 they are set to zero.
+ */
+int layer_norm_backward(const ct_layer_norm_config* cfg, const void* dy, const void* dres_out,
+                        const void* res_out, const float* mean, const float* rstd, void* dres,
+                        void* du, void* dweight, void* dbias, void* workspace,
+                        size_t workspace_bytes, const float* noop_flag, void* stream);
+
+/*
+ * The router of a mixture-of-experts block, in front of moe_sort.  Of T tokens'
+ * logits [T, E] it chooses the K largest each, by value, equal ones by the lower
+ * index.  A logit of -inf is never chosen: where fewer than K others are left the
+ * last slots get expert -1 and weight 0.  A token whose mask is 0, or whose
+ * logits are all -inf, is padding: all its slots get -1, and it takes no part in
+ * anything, whatever its logits.  With p = softmax(logits) and n tokens that are
+ * not padding:
+ *     weights_k = p of the chosen expert, with CT_ROUTER_NORMALIZE divided by the
+ *                 sum of the token's weights (a softmax over the chosen)
+ *     loss = balance * E * sum_e (counts_e / (n K)) * (sum_t p_te / n)
+ *          + z * sum_t logsumexp(logits_t)^2 / n                (0 with n = 0)
+ * A NaN is chosen first, and makes its token's weights and the loss NaN.
+ * Limits: 1 <= E <= 1024, 1 <= K <= min(E, 64) (else CT_ERR_ARG), T*K < 2^31.
+ */
+typedef enum { CT_ROUTER_NORMALIZE = 1 } ct_router_flags;
+
+typedef struct {              /* a host struct, read during the call */
+    int64_t tokens;
+    int experts, topk;
+    int dtype;                /* ct_dtype of the logits and their gradient */
+    int flags;                /* ct_router_flags */
+    float balance, z;
+} ct_router_config;
+
+/* Bytes of workspace moe_router needs (16-byte aligned; 0 for few tokens). */
+size_t moe_router_workspace_size(int64_t tokens, int topk, int experts);
+
+/*
+ * moe_router -- the forward pass.
+ *   mask       uint8 [T], nullable: 0 for padding tokens
+ *   expert_idx int32 [T, K], best first: as moe_sort takes it
+ *   weights    fp32 [T, K]: as moe_combine takes them
+ *   counts     int32 [E + 1]: slots that chose the expert; last, n
+ *   loss       fp32 [1], nullable
+ */
+int moe_router(const ct_router_config* cfg, const void* logits, const uint8_t* mask, int* expert_idx,
+               float* weights, int* counts, float* loss, void* workspace, size_t workspace_bytes,
+               const float* noop_flag, void* stream);
+
+/*
+ * moe_router_backward -- dlogits [T, E] from dweights (fp32 [T, K], of weights;
+ * NULL: zero; not read where expert_idx is outside [0, E)) and dloss (fp32 [1]
+ * on the device, of loss; NULL: zero), not both NULL, and the forward pass's
+ * logits, mask, expert_idx and counts.  The counts are constants to it.  Padding
+ * tokens and masked logits get 0.
+ */
+int moe_router_backward(const ct_router_config* cfg, const void* logits, const uint8_t* mask,
+                        const int* expert_idx, const int* counts, const float* dweights,
+                        const float* dloss, void* dlogits, const float* noop_flag, void* stream);
+
+/*
+ * embedding -- out[t] = scale * table[idx[t]]; 0 where idx is outside [0, V)
+ * (-1: a padding token).
+ *   idx [T], int32 (index_bytes = 4) or int64 (index_bytes = 8)
+ *   table [V, hidden], out [T, hidden], both of type `dtype`
+ * Limits: T, V < 2^31, hidden <= 2^20, T * hidden and V * hidden <= 2^40.
+ */
+int embedding(const void* idx, int index_bytes, int64_t tokens, const void* table, int64_t vocab,
+              int64_t hidden, int dtype, float scale, void* out, const float* noop_flag,
+              void* stream);
+
+/* Bytes of workspace embedding_backward needs (16-byte aligned). */
+size_t embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden);
+
+/*
+ * embedding_backward -- its gradient: dtable[v] = scale * sum of dout[t] over the
+ * t with idx[t] = v, in the order of t, rounded once; rows without a token are 0.
+ * With accumulate (0 or 1) dtable += that, and rows without a token are neither
+ * read nor written.
+ *   dout [T, hidden] of type `dtype`; dtable [V, hidden] of dtype or CT_FP32
+ */
+int embedding_backward(const void* idx, int index_bytes, int64_t tokens, const void* dout,
+                       int64_t vocab, int64_t hidden, int dtype, float scale, void* dtable,
+                       int grad_dtype, int accumulate, void* workspace, size_t workspace_bytes,
+                       const float* noop_flag, void* stream);
+
 /*
  * ct_device_error -- diagnostic word of the current device.  Kernels that
  * wait on an mbarrier give up after a bounded time (about two seconds)
