@@ -7,13 +7,16 @@
 #include "ct_vec.cuh"
 
 #include <algorithm>
+#include <cooperative_groups.h>
 
 namespace ct {
 namespace {
 
 // A warp takes a token; its lane l holds the logits of the experts l, l + 32, ...
-constexpr int kRouterWarps = 8;
-constexpr int kRouterMaxBlocks = 304;
+constexpr int kRouterWarps = 16;
+constexpr int kRouterCluster = 8;
+constexpr int kRouterMaxClusters = 32;
+constexpr int kRouterOneCluster = 4;    // tokens per warp up to which one cluster takes them all
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // Logits as numbers of the same order; equal values (0 and -0) get the same one.
@@ -52,14 +55,9 @@ __device__ __forceinline__ float exponentials(float (&x)[N], float top) {
     return dev::warp_sum(sum);
 }
 
-// Per block of a launch: sums of the probabilities [E], counts [E + 1] (last:
-// the tokens), the sum of squared logsumexps.
-__device__ __forceinline__ float* block_probs(const RouterArgs& a, int64_t b) {
-    return static_cast<float*>(a.workspace) + b * (2 * a.experts + 2);
-}
-__device__ __forceinline__ int* block_counts(const RouterArgs& a, int64_t b) {
-    return reinterpret_cast<int*>(block_probs(a, b) + a.experts);
-}
+// Sums over a part of the tokens: the probabilities [E], counts [E + 1] (last: the
+// tokens), the squared logsumexps.  In the workspace one for each cluster.
+__host__ __device__ constexpr int sum_words(int experts) { return 2 * experts + 2; }
 
 __device__ __forceinline__ void put_loss(const RouterArgs& a, float balance, float squares, int tokens) {
     if (!a.loss) return;
@@ -68,13 +66,20 @@ __device__ __forceinline__ void put_loss(const RouterArgs& a, float balance, flo
                           : a.balance * a.experts * (balance / (n * a.topk)) / n + a.z * (squares / n);
 }
 
+// A cluster's blocks add up their sums through each other's shared memory, each
+// some of the experts; a launch of one cluster goes on to the loss, else
+// router_join_kernel does.
 template <int N, typename T>
 __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterArgs a) {
     extern __shared__ float smem[];
-    float* probs = smem;                                                       // [warps][E]
-    int* counts = reinterpret_cast<int*>(smem + kRouterWarps * a.experts);     // [E + 1]
+    float* own = smem;                                                  // [sum_words]: of this block
+    int* counts = reinterpret_cast<int*>(own + a.experts);
+    float* probs = own + sum_words(a.experts);                          // [warps][E]
     __shared__ float warp_squares[kRouterWarps], warp_balance[kRouterWarps];
+    __shared__ float block_balance;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, K = a.topk;
+    const auto cluster = cooperative_groups::this_cluster();
+    const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
     dev::pdl_launch_dependents();
     for (int e = tid; e <= E; e += blockDim.x) counts[e] = 0;
     __syncthreads();
@@ -101,16 +106,14 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
         bool any = false;
         for (int k = 0; k < K; ++k) {
             unsigned best = key[0];
-            int at = 0;
 #pragma unroll
-            for (int i = 1; i < N; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i;
-                }
+            for (int i = 1; i < N; ++i) best = max(best, key[i]);
             const unsigned most = __reduce_max_sync(kAll, best);
             if (most <= kNever) break;
-            const int e = __reduce_min_sync(kAll, best == most ? unsigned(lane + 32 * at) : 0xFFFFu);
+            unsigned mine = 0xFFFFu;        // the lowest of the lane's experts with it
+#pragma unroll
+            for (int i = N - 1; i >= 0; --i) mine = key[i] == most ? lane + 32 * i : mine;
+            const int e = __reduce_min_sync(kAll, mine);
             if (k == 0) {
                 top = of_order(most);
                 any = true;
@@ -120,17 +123,16 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
                 logit[k >> 5] = of_order(most);
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (e == lane + 32 * i) key[i] = 0;
+            for (int i = 0; i < N; ++i) key[i] = e == lane + 32 * i ? 0 : key[i];
         }
         float sum = 1.0f;
         if (any) {
             sum = exponentials(x, top);
-            const float lse = top + logf(sum);
+            const float lse = top + logf(sum), one = 1.0f / sum;
             squares = fmaf(lse, lse, squares);
             ++tokens;
 #pragma unroll
-            for (int i = 0; i < N; ++i) sums[i] += x[i] / sum;
+            for (int i = 0; i < N; ++i) sums[i] = fmaf(x[i], one, sums[i]);
         }
         float part[2];
 #pragma unroll
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
             if (k >= K) continue;
             a.idx[t * K + k] = chosen[i];
             a.weights[t * K + k] = part[i] / sum;
-            if (chosen[i] >= 0) atomicAdd(counts + chosen[i], 1);
+            if (chosen[i] >= 0) atomicAdd(counts + chosen[i], 1);     // integers: any order gives the same
         }
     }
 #pragma unroll
@@ -153,43 +155,72 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
         atomicAdd(counts + E, tokens);
     }
     __syncthreads();
-    const bool last = gridDim.x == 1;
+    for (int e = tid; e < E; e += blockDim.x) {
+        float p = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kRouterWarps; ++w) p += probs[w * E + e];
+        own[e] = p;
+    }
+    if (tid == 0) {
+        float all = 0.0f;
+        for (int w = 0; w < kRouterWarps; ++w) all += warp_squares[w];
+        own[2 * E + 1] = all;
+    }
+    cluster.sync();
+    // the cluster's sums of the experts rank, rank + blocks, ...
+    const bool last = int(gridDim.x) == blocks;
+    float* out = static_cast<float*>(a.workspace) + int64_t(blockIdx.x / blocks) * sum_words(E);
     float balance = 0.0f;
-    for (int e = tid; e <= E; e += blockDim.x) {
-        const int count = counts[e];
-        if (e < E) {
-            float p = 0.0f;
-            for (int w = 0; w < kRouterWarps; ++w) p += probs[w * E + e];
-            balance = fmaf(static_cast<float>(count), p, balance);
-            if (!last) block_probs(a, blockIdx.x)[e] = p;
+    for (int e = rank + blocks * tid; e <= E; e += blocks * blockDim.x) {
+        float p = 0.0f, q = 0.0f;
+        int count = 0;
+        for (int b = 0; b < blocks; ++b) {
+            const float* other = cluster.map_shared_rank(own, b);
+            count += reinterpret_cast<const int*>(other)[E + e];
+            if (e < E) p += other[e];
+            else q += other[2 * E + 1];
         }
-        if (last)
+        if (e < E) balance = fmaf(static_cast<float>(count), p, balance);
+        if (last) {
             a.counts[e] = count;
-        else
-            block_counts(a, blockIdx.x)[e] = count;
+            if (e == E) {                   // the last one keeps them for the loss
+                tokens = count;
+                squares = q;
+            }
+        } else {
+            if (e < E) out[e] = p;
+            else out[2 * E + 1] = q;
+            reinterpret_cast<int*>(out)[E + e] = count;
+        }
     }
-    balance = dev::warp_sum(balance);
-    if (lane == 0) warp_balance[warp] = balance;
-    __syncthreads();
-    if (tid != 0) return;
-    float all = 0.0f, loss = 0.0f;
-    for (int w = 0; w < kRouterWarps; ++w) {
-        all += warp_squares[w];
-        loss += warp_balance[w];
+    if (last) {
+        balance = dev::warp_sum(balance);
+        if (lane == 0) warp_balance[warp] = balance;
+        __syncthreads();
+        if (tid == 0) {
+            float all = 0.0f;
+            for (int w = 0; w < kRouterWarps; ++w) all += warp_balance[w];
+            block_balance = all;
+        }
+        cluster.sync();
+        if (rank == E % blocks && tid == E / blocks % blockDim.x) {
+            float all = 0.0f;
+            for (int b = 0; b < blocks; ++b) all += *cluster.map_shared_rank(&block_balance, b);
+            put_loss(a, all, squares, tokens);
+        }
     }
-    if (last)
-        put_loss(a, loss, all, counts[E]);
-    else
-        reinterpret_cast<float*>(block_counts(a, blockIdx.x))[E + 1] = all;
+    cluster.sync();      // before a block leaves that others read from
 }
 
-// Joins the blocks' sums, in their order.
+// Joins the clusters' sums, in their order.
 constexpr int kRouterJoinThreads = 1024;
 
-__global__ void __launch_bounds__(kRouterJoinThreads) router_join_kernel(const RouterArgs a, int blocks) {
+__global__ void __launch_bounds__(kRouterJoinThreads) router_join_kernel(const RouterArgs a, int parts) {
     __shared__ float warp_sums[2][32];
     __shared__ int all_tokens;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, words = sum_words(E);
+    const float* sums = static_cast<const float*>(a.workspace);
+    const int* counts = reinterpret_cast<const int*>(sums) + E;
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
@@ -197,16 +228,19 @@ __global__ void __launch_bounds__(kRouterJoinThreads) router_join_kernel(const R
     for (int e = tid; e <= E; e += blockDim.x) {
         float p = 0.0f;
         int count = 0;
-        for (int b = 0; b < blocks; ++b) {
-            count += block_counts(a, b)[e];
-            if (e < E) p += block_probs(a, b)[e];
+#pragma unroll 16
+        for (int b = 0; b < parts; ++b) {
+            count += counts[b * words + e];
+            p += sums[b * words + (e < E ? e : 2 * E + 1)];
         }
         a.counts[e] = count;
-        if (e < E) balance = fmaf(static_cast<float>(count), p, balance);
-        else all_tokens = count;
+        if (e < E) {
+            balance = fmaf(static_cast<float>(count), p, balance);
+        } else {
+            all_tokens = count;
+            squares = p;
+        }
     }
-    for (int b = tid; b < blocks; b += blockDim.x)
-        squares += reinterpret_cast<const float*>(block_counts(a, b))[E + 1];
     balance = dev::warp_sum(balance);
     squares = dev::warp_sum(squares);
     if (lane == 0) {
@@ -286,14 +320,17 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
                 const float d = __shfl_sync(kAll, k < 32 ? dw[0] : dw[1], k & 31);
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    if (e == lane + 32 * i) (a.normalize ? g : each)[i] += d;
+                    if (e == lane + 32 * i) {
+                        if (a.normalize) g[i] += d;
+                        else each[i] += d;
+                    }
             }
         const float sum = exponentials(x, top);
-        const float lse = top + logf(sum);
+        const float lse = top + logf(sum), one = 1.0f / sum;
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x[i] /= sum;
+            x[i] *= one;
             dot = fmaf(x[i], each[i], dot);
         }
         dot = dev::warp_sum(dot);
@@ -304,8 +341,13 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
     }
 }
 
+// Blocks of a launch; up to kRouterCluster of them are one cluster.
 int router_blocks(int64_t tokens) {
-    return static_cast<int>(std::min<int64_t>(kRouterMaxBlocks, (tokens + kRouterWarps - 1) / kRouterWarps));
+    const int64_t blocks = std::max<int64_t>(1, (tokens + kRouterWarps - 1) / kRouterWarps);
+    if (blocks <= kRouterCluster) return static_cast<int>(blocks);
+    if (blocks <= kRouterCluster * kRouterOneCluster) return kRouterCluster;
+    return static_cast<int>(std::min<int64_t>(kRouterMaxClusters, (blocks + kRouterCluster - 1) / kRouterCluster)) *
+           kRouterCluster;
 }
 
 // The kernel for this many experts, K<N, T>::get(), N of them per lane.
@@ -331,17 +373,33 @@ struct Backward {
 
 size_t router_workspace(int64_t tokens, int topk, int experts) {
     const int blocks = router_blocks(tokens);
-    return blocks > 1 ? size_t(blocks) * (2 * experts + 2) * 4 : 0;
+    return blocks > kRouterCluster ? size_t(blocks / kRouterCluster) * sum_words(experts) * 4 : 0;
 }
 
 cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream) {
-    const int blocks = std::max(1, router_blocks(a.tokens));
-    const size_t smem = (size_t(kRouterWarps) * a.experts + a.experts + 1) * 4;   // 36 KB at most
+    const int blocks = router_blocks(a.tokens), parts = blocks / kRouterCluster;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(32 * kRouterWarps);
+    cfg.dynamicSmemBytes = (size_t(kRouterWarps) * a.experts + sum_words(a.experts)) * 4;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = std::min(blocks, kRouterCluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     const cudaError_t e = by_experts<Forward>(a.experts, dtype, [&](auto kernel) {
-        return launch_pdl(kernel, dim3(blocks), dim3(32 * kRouterWarps), smem, stream, a);
+        cudaError_t e = cudaSuccess;
+        if (cfg.dynamicSmemBytes > 48 * 1024)      // of more than 512 experts
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (kRouterWarps * kMaxExperts + sum_words(kMaxExperts)) * 4);
+        return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a);
     });
-    if (e != cudaSuccess || blocks == 1) return e;
-    return launch_pdl(router_join_kernel, dim3(1), dim3(kRouterJoinThreads), 0, stream, a, blocks);
+    if (e != cudaSuccess || parts <= 1) return e;
+    return launch_pdl(router_join_kernel, dim3(1), dim3(kRouterJoinThreads), 0, stream, a, parts);
 }
 
 cudaError_t launch_router_backward(const RouterArgs& a, int dtype, cudaStream_t stream) {
