@@ -6,6 +6,8 @@
 #include "ct_vec.cuh"
 
 #include <algorithm>
+#include <atomic>
+#include <cooperative_groups.h>
 
 namespace ct {
 namespace {
@@ -39,10 +41,12 @@ __global__ void __launch_bounds__(kEmbedThreads) embedding_kernel(const Embeddin
 }
 
 // ---- sort --------------------------------------------------------------------
-// A stable radix sort of the ids, the position of each along: passes of eight
-// bits from the lowest, each of a count per block and digit, the sums of the
-// counts, and the movement.  Ids outside the table get the number `vocab`, and
-// so come last.
+// A stable radix sort of the ids, the position of each along, from the lowest
+// digit.  Ids outside the table get the number `vocab`, and so come last.  Up to
+// kClusterKeys of them are sorted by one cluster in its shared memory; the fill
+// of the table, which needs nothing but the ids, runs beside it.  More go through
+// global memory: per digit a count per block, the sums of the counts, and the
+// movement.
 constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
 constexpr int kSortWarps = 8, kSortThreads = 32 * kSortWarps;
 constexpr int kWarpKeys = 256, kBlockKeys = kWarpKeys * kSortWarps;
@@ -51,7 +55,10 @@ struct Sort {
     unsigned* key[2];     // [tokens], a pass reads one and writes the other
     int* pos[2];
     int* counts;          // [digits][blocks]
+    float* parts;         // [chunks][2][stride], see embedding_sum_kernel
+    int64_t stride;
     int blocks;
+    int chunk, chunks;    // tokens in sorted order, by the chunk
 };
 int sort_blocks(int64_t tokens) { return static_cast<int>((tokens + kBlockKeys - 1) / kBlockKeys); }
 int id_bits(int64_t vocab) {
@@ -59,19 +66,6 @@ int id_bits(int64_t vocab) {
     while (bits < 31 && (int64_t(1) << bits) <= vocab) ++bits;
     return bits;
 }
-Sort sort_of(const EmbeddingArgs& a) {
-    Sort s;
-    const int64_t n = (a.tokens + 3) / 4 * 4;
-    unsigned* w = static_cast<unsigned*>(a.workspace);
-    for (int i = 0; i < 2; ++i) {
-        s.key[i] = w + i * n;
-        s.pos[i] = reinterpret_cast<int*>(w + (2 + i) * n);
-    }
-    s.counts = reinterpret_cast<int*>(w + 4 * n);
-    s.blocks = sort_blocks(a.tokens);
-    return s;
-}
-
 // Key i of pass `pass`, and its position.
 __device__ __forceinline__ unsigned key_at(const EmbeddingArgs& a, const Sort& s, int pass, int64_t i) {
     if (pass > 0) return s.key[(pass - 1) & 1][i];
@@ -174,6 +168,182 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const Embedding
     }
 }
 
+// ---- sort in one cluster ------------------------------------------------------
+// Every block holds `share` consecutive positions, every thread KEYS of them in
+// registers.  A pass: the rank of a key among its warp's with the same digit from
+// a count per digit and warp, the sums of those over the warps, then over the
+// blocks (read from their shared memory), and the key goes to its place in some
+// block's shared memory, in the last pass to global memory.
+constexpr int kClusterBlocks = 8, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterMaxPerThread = 16;
+constexpr int64_t kClusterKeys = int64_t(kClusterBlocks) * kClusterThreads * kClusterMaxPerThread;
+constexpr int kClusterMaxBits = 9;                  // of a digit
+constexpr int kHistRow = kClusterWarps + 1;         // so that neither a row's nor a column's entries share a bank
+
+struct ClusterSort {
+    unsigned* keys;       // [tokens] sorted
+    int* pos;
+    int blocks;           // of the cluster
+    int share;            // positions per block
+    int bits, passes;     // of a digit; digits
+    int fill_blocks;      // blocks after the cluster's, which clear the table
+};
+size_t cluster_smem(const ClusterSort& s) {
+    return size_t(s.share) * 8 + (size_t(1) << s.bits) * (kHistRow + 2) * 4;
+}
+
+// Clears the rows of the table that no token has, some of them per block: a bit
+// for each row of the range that an id falls into.
+constexpr int kFillRows = 32768;
+
+template <typename D>
+__device__ void clear_rows(const EmbeddingArgs& a, unsigned* used, int block, int blocks) {
+    const int64_t begin = a.vocab * block / blocks, end = a.vocab * (block + 1) / blocks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t H = a.hidden;
+    const bool vec = H * sizeof(D) % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+    for (int64_t q = begin; q < end; q += kFillRows) {
+        const int rows = static_cast<int>(min(end - q, int64_t(kFillRows)));
+        for (int i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) used[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int64_t t = threadIdx.x; t < a.tokens; t += blockDim.x) {
+            const int64_t r = id_of(a, t) - q;
+            if (r >= 0 && r < rows) atomicOr(used + (r >> 5), 1u << (r & 31));
+        }
+        __syncthreads();
+        for (int r = warp; r < rows; r += warps) {
+            if ((used[r >> 5] >> (r & 31)) & 1) continue;
+            D* row = static_cast<D*>(a.out) + (q + r) * H;
+            if (vec) {
+                uint4* w = reinterpret_cast<uint4*>(row);
+                for (int64_t i = lane; i < H * int(sizeof(D)) / 16; i += 32) w[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int64_t i = lane; i < H; i += 32) row[i] = D{};
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int KEYS, typename D>
+__global__ void __launch_bounds__(kClusterThreads, 1)
+    embedding_sort_kernel(const EmbeddingArgs a, const ClusterSort s) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int warp_sums[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    dev::pdl_launch_dependents();
+    dev::pdl_wait();
+    if (a.noop && *a.noop != 0.0f) return;
+    if (int(blockIdx.x) >= s.blocks) {
+        clear_rows<D>(a, reinterpret_cast<unsigned*>(smem), blockIdx.x - s.blocks, s.fill_blocks);
+        return;
+    }
+    const auto cluster = cooperative_groups::this_cluster();
+    const int rank = blockIdx.x, digits = 1 << s.bits;
+    uint2* kv = reinterpret_cast<uint2*>(smem);                     // [share]
+    int* hist = reinterpret_cast<int*>(kv + s.share);               // [digits][kHistRow]
+    int* own = hist + digits * kHistRow;                            // [digits]: keys of this block
+    int* base = own + digits;                                       // [digits]: where they go
+    const int64_t first = int64_t(rank) * s.share;
+    const int count = static_cast<int>(max(int64_t(0), min(int64_t(s.share), a.tokens - first)));
+    unsigned key[KEYS];
+    int pos[KEYS], at[KEYS];
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+        const int p = (warp * KEYS + i) * 32 + lane;
+        int64_t id = a.vocab;
+        if (p < count) id = id_of(a, first + p);
+        key[i] = static_cast<unsigned>(id >= 0 && id < a.vocab ? id : a.vocab);
+        pos[i] = static_cast<int>(first) + p;
+    }
+    for (int pass = 0; pass < s.passes; ++pass) {
+        const int shift = pass * s.bits;
+        for (int i = tid; i < digits * kHistRow; i += kClusterThreads) hist[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) {
+            const bool here = (warp * KEYS + i) * 32 + lane < count;
+            const int digit = (key[i] >> shift) & (digits - 1);
+            unsigned same = __ballot_sync(0xFFFFFFFFu, here);
+            same = here ? same : 0;
+            for (int b = 0; b < s.bits; ++b) {
+                const bool bit = (digit >> b) & 1;
+                const unsigned set = __ballot_sync(0xFFFFFFFFu, bit);
+                same &= bit ? set : ~set;
+            }
+            int* entry = hist + digit * kHistRow + warp;
+            const int before = __popc(same & ((1u << lane) - 1));
+            at[i] = here ? *entry + before : 0;
+            __syncwarp();
+            if (here && before == 0) *entry += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int d = tid; d < digits; d += kClusterThreads) {
+            int* row = hist + d * kHistRow;
+            int sum = 0;
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const int c = row[w];
+                row[w] = sum;
+                sum += c;
+            }
+            own[d] = sum;
+        }
+        cluster.sync();                     // and everyone has its keys in registers
+        int before = 0, total = 0;          // digits <= threads: a thread per digit
+        if (tid < digits)
+            for (int o = 0; o < s.blocks; ++o) {
+                const int c = cluster.map_shared_rank(own, o)[tid];
+                before += o < rank ? c : 0;
+                total += c;
+            }
+        int sum = total;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (lane == 31) warp_sums[warp] = sum;
+        __syncthreads();
+        int sums = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, sums, o);
+            if (lane >= o) sums += up;
+        }
+        const int earlier = __shfl_sync(0xFFFFFFFFu, sums, warp > 0 ? warp - 1 : 0);
+        if (tid < digits) base[tid] = (warp > 0 ? earlier : 0) + sum - total + before;
+        __syncthreads();
+        const bool last = pass + 1 == s.passes;
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) {
+            if ((warp * KEYS + i) * 32 + lane >= count) continue;
+            const int digit = (key[i] >> shift) & (digits - 1);
+            const unsigned to = base[digit] + hist[digit * kHistRow + warp] + at[i];
+            if (last) {
+                s.keys[to] = key[i];
+                s.pos[to] = pos[i];
+            } else {
+                const unsigned block = to / s.share;
+                cluster.map_shared_rank(kv, block)[to - block * s.share] = make_uint2(key[i], pos[i]);
+            }
+        }
+        cluster.sync();                     // the last time: before a block leaves that others read from
+        if (last) break;
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) {
+            const int p = (warp * KEYS + i) * 32 + lane;
+            if (p < count) {
+                const uint2 v = kv[p];
+                key[i] = v.x;
+                pos[i] = static_cast<int>(v.y);
+            }
+        }
+    }
+}
+
 // ---- gradient -----------------------------------------------------------------
 // Zeros for the whole table.
 __global__ void __launch_bounds__(kEmbedThreads) embedding_clear_kernel(const EmbeddingArgs a, int bytes) {
@@ -187,32 +357,232 @@ __global__ void __launch_bounds__(kEmbedThreads) embedding_clear_kernel(const Em
     }
 }
 
-// A block per sorted position: the first of an id sums all of it.
+// Sums of the rows of each id, in sorted order.  A block takes a chunk of the
+// sorted tokens and some columns; kRows rows are loaded at a time, whichever ids
+// they have.  An id whose tokens all lie in the chunk is written; of one that
+// goes on in the chunk before or after, the chunk's sum goes to the workspace:
+// place 0 where the id began before, else place 1.
+constexpr int kMaxChunk = 1024;
+
+template <typename T, typename D>
+__device__ __forceinline__ constexpr int rows_at_a_time() { return sizeof(T) == 4 ? 4 : 8; }
+
+template <typename D, int G>
+__device__ __forceinline__ void put_row(const EmbeddingArgs& a, unsigned id, const dev::Cols<G>& c, float (&sum)[8]) {
+    D* out = static_cast<D*>(a.out) + int64_t(id) * a.hidden;
+    float old[8] = {};
+    if (a.accumulate) dev::load_cols<G>(out, c, old);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) old[j] = fmaf(sum[j], a.scale, old[j]);
+    dev::store_cols<G>(out, c, old);
+}
+
 template <typename T, typename D, int G>
 __global__ void __launch_bounds__(kEmbedThreads)
-    embedding_sum_kernel(const EmbeddingArgs a, const unsigned* keys, const int* pos) {
+    embedding_sum_kernel(const EmbeddingArgs a, const Sort s, const unsigned* keys, const int* pos) {
+    __shared__ unsigned key[kMaxChunk + 2];      // the chunk's, with the one before and the one after
+    __shared__ int row[kMaxChunk];
+    constexpr int kRows = rows_at_a_time<T, D>();
+    constexpr unsigned kNone = 0xFFFFFFFFu;
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    const int H = static_cast<int>(a.hidden);
-    const int64_t first = blockIdx.x;
-    const unsigned id = keys[first];
-    if (id >= a.vocab || (first > 0 && keys[first - 1] == id)) return;
-    D* out = static_cast<D*>(a.out) + int64_t(id) * H;
-    for (int vi = threadIdx.x; vi < (H + 255) / 256 * 32; vi += blockDim.x) {
-        const dev::Cols<G> c(vi, H);
-        float sum[8] = {}, f[8];
-        for (int64_t i = first; i < a.tokens && keys[i] == id; ++i) {
-            dev::load_cols<G>(static_cast<const T*>(a.in) + int64_t(pos[i]) * H, c, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += f[j];
-        }
-        float old[8] = {};
-        if (a.accumulate) dev::load_cols<G>(out, c, old);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = fmaf(sum[j], a.scale, old[j]);
-        dev::store_cols<G>(out, c, sum);
+    const int H = static_cast<int>(a.hidden), chunk = blockIdx.x;
+    const int64_t lo = int64_t(chunk) * s.chunk;
+    const int n = static_cast<int>(min(int64_t(s.chunk), a.tokens - lo));
+    for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
+        const int64_t p = lo + i - 1;
+        key[i] = p >= 0 && p < a.tokens ? keys[p] : kNone;
+        if (i < n) row[i] = pos[lo + i];
     }
+    __syncthreads();
+    for (int vi = blockIdx.y * blockDim.x + threadIdx.x; vi < (H + 255) / 256 * 32; vi += gridDim.y * blockDim.x) {
+        const dev::Cols<G> c(vi, H);
+        float sum[8] = {};
+        bool began = key[0] == key[1];           // the id began in the chunk before
+        for (int i0 = 0; i0 < n; i0 += kRows) {
+            if (key[i0 + 1] >= a.vocab) break;
+            float f[kRows][8];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (i0 + r < n) dev::load_cols<G>(static_cast<const T*>(a.in) + int64_t(row[i0 + r]) * H, c, f[r]);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const int i = i0 + r;
+                if (i >= n || key[i + 1] >= a.vocab) break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += f[r][j];
+                const bool goes_on = key[i + 2] == key[i + 1];
+                if (goes_on && i + 1 < n) continue;
+                if (!began && !goes_on)
+                    put_row<D>(a, key[i + 1], c, sum);
+                else
+                    dev::store_cols<G>(s.parts + (2 * int64_t(chunk) + (began ? 0 : 1)) * s.stride, c, sum);
+                began = false;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+            }
+        }
+    }
+}
+
+// The ids that lie in more than one chunk, each by the block of the chunk that it
+// begins in: the sums of the chunks, every kJoinWays-th by a row of threads.
+constexpr int kJoinWays = 8, kJoinColumns = 32;
+
+template <typename D>
+__global__ void __launch_bounds__(kJoinWays * kJoinColumns)
+    embedding_join_kernel(const EmbeddingArgs a, const Sort s, const unsigned* keys) {
+    __shared__ float sums[kJoinWays][kJoinColumns];
+    dev::pdl_launch_dependents();
+    dev::pdl_wait();
+    if (a.noop && *a.noop != 0.0f) return;
+    const int64_t chunk = blockIdx.x, lo = chunk * s.chunk, next = lo + s.chunk;
+    const unsigned id = keys[next - 1];          // there is a chunk after this one
+    if (id >= a.vocab || keys[next] != id || (lo > 0 && keys[lo - 1] == id)) return;
+    // the chunks after this one that begin with the id
+    const int lane = threadIdx.x & 31;
+    int64_t more = 0;
+    for (;; more += 32) {
+        const int64_t p = next + (more + lane) * s.chunk;
+        const unsigned other = __ballot_sync(0xFFFFFFFFu, p >= a.tokens || keys[p] != id);
+        if (other) {
+            more += __ffs(other) - 1;
+            break;
+        }
+    }
+    const int x = threadIdx.x % kJoinColumns, y = threadIdx.x / kJoinColumns;
+    for (int64_t c0 = int64_t(blockIdx.y) * kJoinColumns; c0 < a.hidden; c0 += int64_t(gridDim.y) * kJoinColumns) {
+        const int64_t col = c0 + x;
+        float sum = 0.0f;
+        if (col < a.hidden) {
+            const float* part = s.parts + 2 * chunk * s.stride + col;
+            if (y == 0) sum = part[s.stride];
+#pragma unroll 8
+            for (int64_t i = 1 + y; i <= more; i += kJoinWays) sum += part[2 * i * s.stride];
+        }
+        __syncthreads();
+        sums[y][x] = sum;
+        __syncthreads();
+        if (y != 0 || col >= a.hidden) continue;
+        for (int w = 1; w < kJoinWays; ++w) sum += sums[w][x];
+        D* out = static_cast<D*>(a.out) + int64_t(id) * a.hidden + col;
+        dev::from_f32(*out, fmaf(sum, a.scale, a.accumulate ? dev::to_f32(*out) : 0.0f));
+    }
+}
+
+// The tokens by chunks: 16 each, more where those would be more than 2048.
+void set_chunks(Sort& s, int64_t tokens, int64_t hidden) {
+    s.chunk = static_cast<int>(std::min<int64_t>(kMaxChunk, std::max<int64_t>(16, (tokens + 2047) / 2048)));
+    s.chunks = static_cast<int>((tokens + s.chunk - 1) / s.chunk);
+    s.stride = (hidden + 3) / 4 * 4;
+}
+Sort sort_of(const EmbeddingArgs& a) {
+    Sort s = {};
+    const int64_t n = (a.tokens + 3) / 4 * 4;
+    const int copies = a.tokens > kClusterKeys ? 2 : 1;
+    unsigned* w = static_cast<unsigned*>(a.workspace);
+    for (int i = 0; i < copies; ++i, w += 2 * n) {
+        s.key[i] = w;
+        s.pos[i] = reinterpret_cast<int*>(w + n);
+    }
+    set_chunks(s, a.tokens, a.hidden);
+    s.parts = reinterpret_cast<float*>(w);
+    s.blocks = sort_blocks(a.tokens);
+    s.counts = reinterpret_cast<int*>(s.parts + 2 * s.chunks * s.stride);
+    return s;
+}
+
+// Before the first launch on a device: allows the kernels the shared memory that
+// they may ask for.  Gives the clusters of kClusterBlocks that are resident at a
+// time.
+template <typename D>
+cudaError_t prepare_sort(int* clusters) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];     // 0: not yet
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const bool keep = device >= 0 && device < kDevices;
+    if (keep && (*clusters = known[device].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+    ClusterSort most = {};
+    most.share = kClusterThreads * kClusterMaxPerThread;
+    most.bits = kClusterMaxBits;
+    const size_t smem = cluster_smem(most);
+    for (auto* kernel : {embedding_sort_kernel<1, D>, embedding_sort_kernel<2, D>, embedding_sort_kernel<4, D>,
+                         embedding_sort_kernel<8, D>, embedding_sort_kernel<16, D>}) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kClusterBlocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(kClusterBlocks);
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(clusters, embedding_sort_kernel<16, D>, &cfg);
+    if (e != cudaSuccess) return e;
+    *clusters = std::max(1, *clusters);
+    if (keep) known[device].store(*clusters, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <typename D>
+cudaError_t launch_cluster_sort(const EmbeddingArgs& a, const Sort& to, cudaStream_t stream) {
+    ClusterSort s = {};
+    s.keys = to.key[0];
+    s.pos = to.pos[0];
+    s.blocks = a.tokens <= kClusterThreads ? 1 : kClusterBlocks;
+    s.share = static_cast<int>((a.tokens + s.blocks - 1) / s.blocks);
+    const int all = id_bits(a.vocab);
+    s.passes = (all + kClusterMaxBits - 1) / kClusterMaxBits;
+    s.bits = (all + s.passes - 1) / s.passes;
+    const int keys = (s.share + kClusterThreads - 1) / kClusterThreads;
+    auto* kernel = keys <= 1 ? embedding_sort_kernel<1, D> : keys <= 2 ? embedding_sort_kernel<2, D>
+                 : keys <= 4 ? embedding_sort_kernel<4, D> : keys <= 8 ? embedding_sort_kernel<8, D>
+                             : embedding_sort_kernel<16, D>;
+    int clusters = 0;
+    cudaError_t e = prepare_sort<D>(&clusters);
+    if (e != cudaSuccess) return e;
+    if (!a.accumulate) {
+        // as many as are resident beside the sort's, each with 64 KB at least
+        const int64_t bytes = a.vocab * a.hidden * int64_t(sizeof(D));
+        const int64_t room = s.blocks == 1 ? sm_count() - 1 : (clusters - 1) * kClusterBlocks;
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(room, (bytes + 65535) / 65536));
+        s.fill_blocks = static_cast<int>((want + s.blocks - 1) / s.blocks * s.blocks);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(s.blocks + s.fill_blocks);
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = std::max<size_t>(cluster_smem(s), kFillRows / 8);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = s.blocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, s);
+}
+
+cudaError_t launch_grid_sort(const EmbeddingArgs& a, const Sort& s, int grad_bytes, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    if (!a.accumulate)
+        e = launch_pdl(embedding_clear_kernel, dim3(sm_count() * 8), dim3(kEmbedThreads), 0, stream, a, grad_bytes);
+    const int passes = (id_bits(a.vocab) + kDigitBits - 1) / kDigitBits;
+    for (int pass = 0; pass < passes && e == cudaSuccess; ++pass) {
+        e = launch_pdl(sort_count_kernel, dim3(s.blocks), dim3(kSortThreads), 0, stream, a, s, pass);
+        if (e == cudaSuccess) e = launch_pdl(sort_scan_kernel, dim3(1), dim3(1024), 0, stream, a, s);
+        if (e == cudaSuccess)
+            e = launch_pdl(sort_move_kernel, dim3(s.blocks), dim3(kSortThreads), 0, stream, a, s, pass);
+    }
+    return e;
 }
 
 }  // namespace
@@ -227,34 +597,31 @@ cudaError_t launch_embedding(const EmbeddingArgs& a, int dtype, cudaStream_t str
 }
 
 size_t embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden) {
-    return size_t((tokens + 3) / 4 * 4) * 16 + size_t(kDigits) * sort_blocks(tokens) * 4;
+    Sort s = {};
+    set_chunks(s, tokens, hidden);
+    const size_t lists = size_t((tokens + 3) / 4 * 4) * 8, parts = size_t(s.chunks) * 2 * s.stride * 4;
+    return tokens > kClusterKeys ? 2 * lists + parts + size_t(kDigits) * sort_blocks(tokens) * 4 : lists + parts;
 }
 
 cudaError_t launch_embedding_backward(const EmbeddingArgs& a, int dtype, cudaStream_t stream) {
-    cudaError_t e = cudaSuccess;
-    if (!a.accumulate) {
-        e = launch_pdl(embedding_clear_kernel, dim3(sm_count() * 8), dim3(kEmbedThreads), 0, stream, a,
-                       a.grad_f32 || dtype == 2 ? 4 : 2);
-        if (e != cudaSuccess) return e;
-    }
-    if (a.tokens == 0) return e;
     const Sort s = sort_of(a);
-    const int passes = (id_bits(a.vocab) + kDigitBits - 1) / kDigitBits;
-    for (int pass = 0; pass < passes; ++pass) {
-        e = launch_pdl(sort_count_kernel, dim3(s.blocks), dim3(kSortThreads), 0, stream, a, s, pass);
-        if (e == cudaSuccess) e = launch_pdl(sort_scan_kernel, dim3(1), dim3(1024), 0, stream, a, s);
-        if (e == cudaSuccess)
-            e = launch_pdl(sort_move_kernel, dim3(s.blocks), dim3(kSortThreads), 0, stream, a, s, pass);
-        if (e != cudaSuccess) return e;
-    }
-    const unsigned* keys = s.key[(passes - 1) & 1];
-    const int* pos = s.pos[(passes - 1) & 1];
     const bool vec = a.hidden % 8 == 0 && all_aligned(a.in, a.out);
     return by_types(dtype, a.grad_f32 ? 2 : dtype, [&](auto t, auto d) {
         using T = decltype(t);
         using D = decltype(d);
-        return launch_pdl(vec ? embedding_sum_kernel<T, D, 8> : embedding_sum_kernel<T, D, 1>,
-                          dim3(static_cast<unsigned>(a.tokens)), dim3(kEmbedThreads), 0, stream, a, keys, pos);
+        const bool grid = a.tokens > kClusterKeys;
+        cudaError_t e = grid ? launch_grid_sort(a, s, sizeof(D), stream) : launch_cluster_sort<D>(a, s, stream);
+        if (e != cudaSuccess || a.tokens == 0) return e;
+        const int last = grid ? ((id_bits(a.vocab) + kDigitBits - 1) / kDigitBits - 1) & 1 : 0;
+        const int items = static_cast<int>((a.hidden + 255) / 256 * 32);
+        const int threads = std::min(items, kEmbedThreads);
+        e = launch_pdl(vec ? embedding_sum_kernel<T, D, 8> : embedding_sum_kernel<T, D, 1>,
+                       dim3(s.chunks, std::min((items + threads - 1) / threads, 64)), dim3(threads), 0, stream, a, s,
+                       s.key[last], s.pos[last]);
+        if (e != cudaSuccess || s.chunks == 1) return e;
+        const int columns = static_cast<int>(std::min<int64_t>((a.hidden + kJoinColumns - 1) / kJoinColumns, 8));
+        return launch_pdl(embedding_join_kernel<D>, dim3(s.chunks - 1, columns), dim3(kJoinWays * kJoinColumns), 0,
+                          stream, a, s, s.key[last]);
     });
 }
 
