@@ -18,7 +18,9 @@ __device__ __forceinline__ int64_t id_of(const EmbeddingArgs& a, int64_t t) {
 
 constexpr int kEmbedThreads = 256;
 
-// A block per token.
+// A block per token; a thread's kEmbedItems loads are in flight together.
+constexpr int kEmbedItems = 4;
+
 template <typename T, int G>
 __global__ void __launch_bounds__(kEmbedThreads) embedding_kernel(const EmbeddingArgs a) {
     dev::pdl_launch_dependents();
@@ -28,15 +30,22 @@ __global__ void __launch_bounds__(kEmbedThreads) embedding_kernel(const Embeddin
     const int64_t t = blockIdx.x, id = id_of(a, t);
     const bool inside = id >= 0 && id < a.vocab;
     const T* row = static_cast<const T*>(a.in) + (inside ? id : 0) * H;
-    for (int vi = threadIdx.x; vi < (H + 255) / 256 * 32; vi += blockDim.x) {
-        const dev::Cols<G> c(vi, H);
-        float f[8] = {};
-        if (inside) {
-            dev::load_cols<G>(row, c, f);
+    T* out = static_cast<T*>(a.out) + t * H;
+    for (int v0 = threadIdx.x; v0 < (H + 255) / 256 * 32; v0 += kEmbedItems * blockDim.x) {
+        dev::RawCols<G, T> raw[kEmbedItems];
+        if (inside)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] *= a.scale;
+            for (int i = 0; i < kEmbedItems; ++i) raw[i].load(row, dev::Cols<G>(v0 + i * blockDim.x, H));
+#pragma unroll
+        for (int i = 0; i < kEmbedItems; ++i) {
+            float f[8] = {};
+            if (inside) {
+                raw[i].get(f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] *= a.scale;
+            }
+            dev::store_cols<G>(out, dev::Cols<G>(v0 + i * blockDim.x, H), f);
         }
-        dev::store_cols<G>(static_cast<T*>(a.out) + t * H, c, f);
     }
 }
 
@@ -56,6 +65,7 @@ struct Sort {
     int* pos[2];
     int* counts;          // [digits][blocks]
     float* parts;         // [chunks][2][stride], see embedding_sum_kernel
+    int* leaves;          // [chunks]: an id of more than kShort tokens begins in the chunk and goes on
     int64_t stride;
     int blocks;
     int chunk, chunks;    // tokens in sorted order, by the chunk
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const Embedding
 // a count per digit and warp, the sums of those over the warps, then over the
 // blocks (read from their shared memory), and the key goes to its place in some
 // block's shared memory, in the last pass to global memory.
-constexpr int kClusterBlocks = 8, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterBlocks = 8, kSmallCluster = 4, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterMaxPerThread = 16;
 constexpr int64_t kClusterKeys = int64_t(kClusterBlocks) * kClusterThreads * kClusterMaxPerThread;
 constexpr int kClusterMaxBits = 9;                  // of a digit
@@ -359,13 +369,13 @@ __global__ void __launch_bounds__(kEmbedThreads) embedding_clear_kernel(const Em
 
 // Sums of the rows of each id, in sorted order.  A block takes a chunk of the
 // sorted tokens and some columns; kRows rows are loaded at a time, whichever ids
-// they have.  An id whose tokens all lie in the chunk is written; of one that
-// goes on in the chunk before or after, the chunk's sum goes to the workspace:
-// place 0 where the id began before, else place 1.
+// they have.  An id of at most kShort tokens is summed and written by the block of
+// the chunk that it begins in, which goes on past its chunk for that; of one with
+// more every chunk's sum goes to the workspace: place 0 where the id began in an
+// earlier chunk, else place 1.  (Unless such a one begins and ends in one chunk.)
 constexpr int kMaxChunk = 1024;
-
-template <typename T, typename D>
-__device__ __forceinline__ constexpr int rows_at_a_time() { return sizeof(T) == 4 ? 4 : 8; }
+constexpr int kShort = 32;                       // a warp's lanes look at as many keys
+constexpr unsigned kNone = 0xFFFFFFFFu;
 
 template <typename D, int G>
 __device__ __forceinline__ void put_row(const EmbeddingArgs& a, unsigned id, const dev::Cols<G>& c, float (&sum)[8]) {
@@ -377,48 +387,71 @@ __device__ __forceinline__ void put_row(const EmbeddingArgs& a, unsigned id, con
     dev::store_cols<G>(out, c, old);
 }
 
+// Of at most kShort: how many keys before (step -1) or from (step 1) p on are id.
+__device__ __forceinline__ int same_keys(const unsigned* p, int step, unsigned id) {
+    const unsigned other = __ballot_sync(0xFFFFFFFFu, p[step * int(threadIdx.x & 31)] != id);
+    return other ? __ffs(other) - 1 : kShort;
+}
+
 template <typename T, typename D, int G>
 __global__ void __launch_bounds__(kEmbedThreads)
     embedding_sum_kernel(const EmbeddingArgs a, const Sort s, const unsigned* keys, const int* pos) {
-    __shared__ unsigned key[kMaxChunk + 2];      // the chunk's, with the one before and the one after
-    __shared__ int row[kMaxChunk];
-    constexpr int kRows = rows_at_a_time<T, D>();
-    constexpr unsigned kNone = 0xFFFFFFFFu;
+    __shared__ unsigned window[kMaxChunk + 2 * kShort + 1];      // the chunk's keys and those around it
+    __shared__ int row[kMaxChunk + kShort];
+    constexpr int kRows = sizeof(T) == 4 ? 4 : 8;
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     const int H = static_cast<int>(a.hidden), chunk = blockIdx.x;
     const int64_t lo = int64_t(chunk) * s.chunk;
     const int n = static_cast<int>(min(int64_t(s.chunk), a.tokens - lo));
-    for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
-        const int64_t p = lo + i - 1;
-        key[i] = p >= 0 && p < a.tokens ? keys[p] : kNone;
-        if (i < n) row[i] = pos[lo + i];
+    const unsigned* key = window + kShort;
+    for (int i = threadIdx.x; i < n + 2 * kShort + 1; i += blockDim.x) {
+        const int64_t p = lo + i - kShort;
+        window[i] = p >= 0 && p < a.tokens ? keys[p] : kNone;
+        if (i < n + kShort && lo + i < a.tokens) row[i] = pos[lo + i];
     }
     __syncthreads();
+    // [begin, end): what this block sums.  Its first id may have begun before, its
+    // last one may go on.
+    int begin = 0, end = n;
+    const int earlier = same_keys(key - 1, -1, key[0]);
+    const bool began = earlier == kShort || (earlier > 0 && key[kShort - earlier] == key[0]);
+    if (earlier > 0 && !began)
+        for (begin = 1; begin < n && key[begin] == key[0];) ++begin;
+    if (begin < n && key[n] == key[n - 1]) {
+        const int inside = same_keys(key + n - 1, -1, key[n - 1]);     // these may lie before the chunk, too
+        if (inside < kShort && key[n - inside + kShort] != key[n - 1]) end = n + same_keys(key + n, 1, key[n - 1]);
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        const bool whole = began && key[0] == key[n - 1];
+        s.leaves[chunk] = end == n && key[n] == key[n - 1] && key[n] < a.vocab && begin < n && !whole;
+    }
     for (int vi = blockIdx.y * blockDim.x + threadIdx.x; vi < (H + 255) / 256 * 32; vi += gridDim.y * blockDim.x) {
         const dev::Cols<G> c(vi, H);
         float sum[8] = {};
-        bool began = key[0] == key[1];           // the id began in the chunk before
-        for (int i0 = 0; i0 < n; i0 += kRows) {
-            if (key[i0 + 1] >= a.vocab) break;
-            float f[kRows][8];
+        bool part = began;                       // of an id that began in an earlier chunk
+        for (int i0 = begin; i0 < end; i0 += kRows) {
+            if (key[i0] >= a.vocab) break;
+            dev::RawCols<G, T> raw[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r)
-                if (i0 + r < n) dev::load_cols<G>(static_cast<const T*>(a.in) + int64_t(row[i0 + r]) * H, c, f[r]);
+                raw[r].load(static_cast<const T*>(a.in) + int64_t(row[min(i0 + r, end - 1)]) * H, c);
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 const int i = i0 + r;
-                if (i >= n || key[i + 1] >= a.vocab) break;
+                if (i >= end || key[i] >= a.vocab) break;
+                float f[8];
+                raw[r].get(f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] += f[r][j];
-                const bool goes_on = key[i + 2] == key[i + 1];
-                if (goes_on && i + 1 < n) continue;
-                if (!began && !goes_on)
-                    put_row<D>(a, key[i + 1], c, sum);
+                for (int j = 0; j < 8; ++j) sum[j] += f[j];
+                const bool goes_on = key[i + 1] == key[i];
+                if (goes_on && i + 1 < end) continue;
+                if (part || goes_on)
+                    dev::store_cols<G>(s.parts + (2 * int64_t(chunk) + (part ? 0 : 1)) * s.stride, c, sum);
                 else
-                    dev::store_cols<G>(s.parts + (2 * int64_t(chunk) + (began ? 0 : 1)) * s.stride, c, sum);
-                began = false;
+                    put_row<D>(a, key[i], c, sum);
+                part = false;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
             }
@@ -426,48 +459,78 @@ __global__ void __launch_bounds__(kEmbedThreads)
     }
 }
 
-// The ids that lie in more than one chunk, each by the block of the chunk that it
-// begins in: the sums of the chunks, every kJoinWays-th by a row of threads.
-constexpr int kJoinWays = 8, kJoinColumns = 32;
+// The ids of more than kShort tokens that lie in more than one chunk: the sums of
+// the chunks, every kJoinWays-th by a warp.  A block looks at some chunks for those
+// that such an id begins in.
+constexpr int kJoinWays = 8, kJoinThreads = 32 * kJoinWays;
+constexpr int kJoinColumns = 128;                // of a step: four for every lane
+constexpr int kJoinBatch = 8;
+constexpr int kJoinBlocks = 64;
 
 template <typename D>
-__global__ void __launch_bounds__(kJoinWays * kJoinColumns)
+__global__ void __launch_bounds__(kJoinThreads)
     embedding_join_kernel(const EmbeddingArgs a, const Sort s, const unsigned* keys) {
-    __shared__ float sums[kJoinWays][kJoinColumns];
+    __shared__ float4 sums[kJoinWays][32];
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    const int64_t chunk = blockIdx.x, lo = chunk * s.chunk, next = lo + s.chunk;
-    const unsigned id = keys[next - 1];          // there is a chunk after this one
-    if (id >= a.vocab || keys[next] != id || (lo > 0 && keys[lo - 1] == id)) return;
-    // the chunks after this one that begin with the id
-    const int lane = threadIdx.x & 31;
-    int64_t more = 0;
-    for (;; more += 32) {
-        const int64_t p = next + (more + lane) * s.chunk;
-        const unsigned other = __ballot_sync(0xFFFFFFFFu, p >= a.tokens || keys[p] != id);
-        if (other) {
-            more += __ffs(other) - 1;
-            break;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // frequent ids lie side by side: every gridDim.x-th chunk
+    for (int64_t group = blockIdx.x; group < s.chunks; group += 32 * int64_t(gridDim.x)) {
+        const int64_t mine = group + lane * int64_t(gridDim.x);
+        unsigned left = __ballot_sync(0xFFFFFFFFu, mine < s.chunks && s.leaves[min(mine, int64_t(s.chunks) - 1)]);
+        for (; left; left &= left - 1) {
+            const int64_t chunk = group + (__ffs(left) - 1) * int64_t(gridDim.x), next = (chunk + 1) * s.chunk;
+            const unsigned id = keys[next];
+            int64_t more = 0;                    // the chunks after this one that begin with the id
+            for (;; more += 32) {
+                const int64_t p = next + (more + lane) * s.chunk;
+                const unsigned end = __ballot_sync(0xFFFFFFFFu, p >= a.tokens || keys[min(p, a.tokens - 1)] != id);
+                if (end) {
+                    more += __ffs(end) - 1;
+                    break;
+                }
+            }
+            for (int64_t c0 = int64_t(blockIdx.y) * kJoinColumns; c0 < a.hidden;
+                 c0 += int64_t(gridDim.y) * kJoinColumns) {
+                const int64_t col = c0 + 4 * lane;   // the workspace's rows are whole multiples of four
+                const bool here = col < a.hidden;
+                const float* part = s.parts + 2 * chunk * s.stride + (here ? col : 0);
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (warp == 0) sum = *reinterpret_cast<const float4*>(part + s.stride);
+                for (int64_t i0 = 1 + warp; i0 <= more; i0 += kJoinWays * kJoinBatch) {
+                    float4 v[kJoinBatch];
+#pragma unroll
+                    for (int i = 0; i < kJoinBatch; ++i)
+                        v[i] = *reinterpret_cast<const float4*>(part + 2 * min(i0 + i * kJoinWays, more) * s.stride);
+#pragma unroll
+                    for (int i = 0; i < kJoinBatch; ++i) {     // a condition around the sums would draw the loads in
+                        const bool use = i0 + i * kJoinWays <= more;
+                        sum.x += use ? v[i].x : 0.0f;
+                        sum.y += use ? v[i].y : 0.0f;
+                        sum.z += use ? v[i].z : 0.0f;
+                        sum.w += use ? v[i].w : 0.0f;
+                    }
+                }
+                __syncthreads();
+                sums[warp][lane] = sum;
+                __syncthreads();
+                if (warp != 0) continue;
+                for (int w = 1; w < kJoinWays; ++w) {
+                    const float4 v = sums[w][lane];
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                }
+                const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+                D* out = static_cast<D*>(a.out) + int64_t(id) * a.hidden + col;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (col + j < a.hidden)
+                        dev::from_f32(out[j], fmaf(f[j], a.scale, a.accumulate ? dev::to_f32(out[j]) : 0.0f));
+            }
         }
-    }
-    const int x = threadIdx.x % kJoinColumns, y = threadIdx.x / kJoinColumns;
-    for (int64_t c0 = int64_t(blockIdx.y) * kJoinColumns; c0 < a.hidden; c0 += int64_t(gridDim.y) * kJoinColumns) {
-        const int64_t col = c0 + x;
-        float sum = 0.0f;
-        if (col < a.hidden) {
-            const float* part = s.parts + 2 * chunk * s.stride + col;
-            if (y == 0) sum = part[s.stride];
-#pragma unroll 8
-            for (int64_t i = 1 + y; i <= more; i += kJoinWays) sum += part[2 * i * s.stride];
-        }
-        __syncthreads();
-        sums[y][x] = sum;
-        __syncthreads();
-        if (y != 0 || col >= a.hidden) continue;
-        for (int w = 1; w < kJoinWays; ++w) sum += sums[w][x];
-        D* out = static_cast<D*>(a.out) + int64_t(id) * a.hidden + col;
-        dev::from_f32(*out, fmaf(sum, a.scale, a.accumulate ? dev::to_f32(*out) : 0.0f));
     }
 }
 
@@ -488,23 +551,25 @@ Sort sort_of(const EmbeddingArgs& a) {
     }
     set_chunks(s, a.tokens, a.hidden);
     s.parts = reinterpret_cast<float*>(w);
+    s.leaves = reinterpret_cast<int*>(s.parts + 2 * s.chunks * s.stride);
     s.blocks = sort_blocks(a.tokens);
-    s.counts = reinterpret_cast<int*>(s.parts + 2 * s.chunks * s.stride);
+    s.counts = s.leaves + s.chunks;
     return s;
 }
 
 // Before the first launch on a device: allows the kernels the shared memory that
-// they may ask for.  Gives the clusters of kClusterBlocks that are resident at a
-// time.
+// they may ask for.  Gives the clusters of `blocks` blocks (kClusterBlocks or
+// kSmallCluster) that are resident at a time.
 template <typename D>
-cudaError_t prepare_sort(int* clusters) {
+cudaError_t prepare_sort(int blocks, int* clusters) {
     constexpr int kDevices = 64;
-    static std::atomic<int> known[kDevices];     // 0: not yet
+    static std::atomic<int> known[2][kDevices];  // 0: not yet
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     const bool keep = device >= 0 && device < kDevices;
-    if (keep && (*clusters = known[device].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+    std::atomic<int>* place = known[blocks == kClusterBlocks] + (keep ? device : 0);
+    if (keep && (*clusters = place->load(std::memory_order_acquire)) > 0) return cudaSuccess;
     ClusterSort most = {};
     most.share = kClusterThreads * kClusterMaxPerThread;
     most.bits = kClusterMaxBits;
@@ -517,9 +582,9 @@ cudaError_t prepare_sort(int* clusters) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = kClusterBlocks;
+    attr.val.clusterDim.x = blocks;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(kClusterBlocks);
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kClusterThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = &attr;
@@ -527,7 +592,7 @@ cudaError_t prepare_sort(int* clusters) {
     e = cudaOccupancyMaxActiveClusters(clusters, embedding_sort_kernel<16, D>, &cfg);
     if (e != cudaSuccess) return e;
     *clusters = std::max(1, *clusters);
-    if (keep) known[device].store(*clusters, std::memory_order_release);
+    if (keep) place->store(*clusters, std::memory_order_release);
     return cudaSuccess;
 }
 
@@ -536,7 +601,8 @@ cudaError_t launch_cluster_sort(const EmbeddingArgs& a, const Sort& to, cudaStre
     ClusterSort s = {};
     s.keys = to.key[0];
     s.pos = to.pos[0];
-    s.blocks = a.tokens <= kClusterThreads ? 1 : kClusterBlocks;
+    s.blocks = a.tokens <= kClusterThreads ? 1
+             : !a.accumulate && a.tokens <= kSmallCluster * kClusterThreads * 8 ? kSmallCluster : kClusterBlocks;
     s.share = static_cast<int>((a.tokens + s.blocks - 1) / s.blocks);
     const int all = id_bits(a.vocab);
     s.passes = (all + kClusterMaxBits - 1) / kClusterMaxBits;
@@ -546,12 +612,12 @@ cudaError_t launch_cluster_sort(const EmbeddingArgs& a, const Sort& to, cudaStre
                  : keys <= 4 ? embedding_sort_kernel<4, D> : keys <= 8 ? embedding_sort_kernel<8, D>
                              : embedding_sort_kernel<16, D>;
     int clusters = 0;
-    cudaError_t e = prepare_sort<D>(&clusters);
+    cudaError_t e = prepare_sort<D>(s.blocks == kClusterBlocks ? kClusterBlocks : kSmallCluster, &clusters);
     if (e != cudaSuccess) return e;
     if (!a.accumulate) {
         // as many as are resident beside the sort's, each with 64 KB at least
         const int64_t bytes = a.vocab * a.hidden * int64_t(sizeof(D));
-        const int64_t room = s.blocks == 1 ? sm_count() - 1 : (clusters - 1) * kClusterBlocks;
+        const int64_t room = s.blocks == 1 ? sm_count() - 1 : (clusters - 1) * s.blocks;
         const int64_t want = std::max<int64_t>(1, std::min<int64_t>(room, (bytes + 65535) / 65536));
         s.fill_blocks = static_cast<int>((want + s.blocks - 1) / s.blocks * s.blocks);
     }
@@ -591,15 +657,17 @@ cudaError_t launch_embedding(const EmbeddingArgs& a, int dtype, cudaStream_t str
     const bool vec = a.hidden % 8 == 0 && all_aligned(a.in, a.out);
     return by_types(dtype, dtype, [&](auto t, auto) {
         using T = decltype(t);
+        const int items = static_cast<int>((a.hidden + 255) / 256 * 32);
+        const int threads = std::min(kEmbedThreads, (items / 32 + kEmbedItems - 1) / kEmbedItems * 32);
         return launch_pdl(vec ? embedding_kernel<T, 8> : embedding_kernel<T, 1>,
-                          dim3(static_cast<unsigned>(a.tokens)), dim3(kEmbedThreads), 0, stream, a);
+                          dim3(static_cast<unsigned>(a.tokens)), dim3(threads), 0, stream, a);
     });
 }
 
 size_t embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden) {
     Sort s = {};
     set_chunks(s, tokens, hidden);
-    const size_t lists = size_t((tokens + 3) / 4 * 4) * 8, parts = size_t(s.chunks) * 2 * s.stride * 4;
+    const size_t lists = size_t((tokens + 3) / 4 * 4) * 8, parts = size_t(s.chunks) * (2 * s.stride + 1) * 4;
     return tokens > kClusterKeys ? 2 * lists + parts + size_t(kDigits) * sort_blocks(tokens) * 4 : lists + parts;
 }
 
@@ -618,10 +686,11 @@ cudaError_t launch_embedding_backward(const EmbeddingArgs& a, int dtype, cudaStr
         e = launch_pdl(vec ? embedding_sum_kernel<T, D, 8> : embedding_sum_kernel<T, D, 1>,
                        dim3(s.chunks, std::min((items + threads - 1) / threads, 64)), dim3(threads), 0, stream, a, s,
                        s.key[last], s.pos[last]);
-        if (e != cudaSuccess || s.chunks == 1) return e;
-        const int columns = static_cast<int>(std::min<int64_t>((a.hidden + kJoinColumns - 1) / kJoinColumns, 8));
-        return launch_pdl(embedding_join_kernel<D>, dim3(s.chunks - 1, columns), dim3(kJoinWays * kJoinColumns), 0,
-                          stream, a, s, s.key[last]);
+        // no id has more tokens than there are
+        if (e != cudaSuccess || s.chunks == 1 || a.tokens <= kShort) return e;
+        const int columns = static_cast<int>(std::min<int64_t>((a.hidden + kJoinColumns - 1) / kJoinColumns, 32));
+        return launch_pdl(embedding_join_kernel<D>, dim3(std::min(s.chunks, kJoinBlocks), columns),
+                          dim3(kJoinThreads), 0, stream, a, s, s.key[last]);
     });
 }
 

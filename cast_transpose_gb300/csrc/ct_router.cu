@@ -13,10 +13,10 @@ namespace ct {
 namespace {
 
 // A warp takes a token; its lane l holds the logits of the experts l, l + 32, ...
-constexpr int kRouterWarps = 16;
+constexpr int kRouterWarps = 8;
 constexpr int kRouterCluster = 8;
-constexpr int kRouterMaxClusters = 32;
-constexpr int kRouterOneCluster = 4;    // tokens per warp up to which one cluster takes them all
+constexpr int kRouterMaxClusters = 48;
+constexpr int kRouterOneCluster = 8;    // tokens per warp up to which one cluster takes them all
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // Logits as numbers of the same order; equal values (0 and -0) get the same one.
@@ -32,16 +32,26 @@ __device__ __forceinline__ float of_order(unsigned o) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// What a warp reads of a token, without waiting for any of it: its logits and
+// whether it counts.
 template <int N, typename T>
-__device__ __forceinline__ void load_logits(const RouterArgs& a, int64_t t, float (&x)[N]) {
-    const T* row = static_cast<const T*>(a.logits) + t * a.experts;
-    const int lane = threadIdx.x & 31;
+struct Token {
+    T v[N];
+    uint8_t counted;
+
+    __device__ __forceinline__ void load(const RouterArgs& a, int64_t t) {
+        const T* row = static_cast<const T*>(a.logits) + t * a.experts;
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int e = lane + 32 * i;
-        x[i] = e < a.experts ? dev::to_f32(row[e]) : -INFINITY;
+        for (int i = 0; i < N; ++i) v[i] = row[min(lane + 32 * i, a.experts - 1)];
+        counted = a.mask ? a.mask[t] : 1;
     }
-}
+    __device__ __forceinline__ void get(const RouterArgs& a, float (&x)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = (threadIdx.x & 31) + 32 * i < a.experts ? dev::to_f32(v[i]) : -INFINITY;
+    }
+};
 
 // exp(x - top) in place of x; the sum of all.
 template <int N>
@@ -88,20 +98,22 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
     float sums[N] = {};
     float squares = 0.0f;
     int tokens = 0;
-    for (int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp; t < a.tokens; t += int64_t(gridDim.x) * kRouterWarps) {
+    const int64_t step = int64_t(gridDim.x) * kRouterWarps;
+    constexpr bool kAhead = N <= 8;         // the next token's loads before this one's work: while registers last
+    Token<N, T> next;
+    int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp;
+    if (kAhead && t < a.tokens) next.load(a, t);
+    for (; t < a.tokens; t += step) {
         float x[N];
         unsigned key[N];
-        const bool counted = !a.mask || a.mask[t];
         int chosen[2] = {-1, -1};           // lane k: of slots k and k + 32
         float logit[2] = {};
-        if (counted) {
-            load_logits<N, T>(a, t, x);
+        if (!kAhead) next.load(a, t);
+        next.get(a, x);
+        const bool counted = next.counted;
+        if (kAhead && t + step < a.tokens) next.load(a, t + step);
 #pragma unroll
-            for (int i = 0; i < N; ++i) key[i] = lane + 32 * i < E ? order_of(x[i]) : 0;
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) key[i] = 0;
-        }
+        for (int i = 0; i < N; ++i) key[i] = counted && lane + 32 * i < E ? order_of(x[i]) : 0;
         float top = 0.0f;
         bool any = false;
         for (int k = 0; k < K; ++k) {
@@ -172,24 +184,24 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
     float* out = static_cast<float*>(a.workspace) + int64_t(blockIdx.x / blocks) * sum_words(E);
     float balance = 0.0f;
     for (int e = rank + blocks * tid; e <= E; e += blocks * blockDim.x) {
-        float p = 0.0f, q = 0.0f;
+        float p = 0.0f;
         int count = 0;
-        for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+        for (int b = 0; b < kRouterCluster; ++b) {
+            if (b >= blocks) break;
             const float* other = cluster.map_shared_rank(own, b);
             count += reinterpret_cast<const int*>(other)[E + e];
-            if (e < E) p += other[e];
-            else q += other[2 * E + 1];
+            p += other[e < E ? e : 2 * E + 1];
         }
         if (e < E) balance = fmaf(static_cast<float>(count), p, balance);
         if (last) {
             a.counts[e] = count;
             if (e == E) {                   // the last one keeps them for the loss
                 tokens = count;
-                squares = q;
+                squares = p;
             }
         } else {
-            if (e < E) out[e] = p;
-            else out[2 * E + 1] = q;
+            out[e < E ? e : 2 * E + 1] = p;
             reinterpret_cast<int*>(out)[E + e] = count;
         }
     }
@@ -212,46 +224,69 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
     cluster.sync();      // before a block leaves that others read from
 }
 
-// Joins the clusters' sums, in their order.
-constexpr int kRouterJoinThreads = 1024;
+// Joins the clusters' sums in a fixed order: a thread takes every `ways`-th of them
+// for one expert, eight loads at a time.
+constexpr int kRouterJoinThreads = 1024, kJoinBatch = 8;
 
 __global__ void __launch_bounds__(kRouterJoinThreads) router_join_kernel(const RouterArgs a, int parts) {
-    __shared__ float warp_sums[2][32];
-    __shared__ int all_tokens;
+    __shared__ float probs[kRouterJoinThreads];
+    __shared__ int counts[kRouterJoinThreads];
+    __shared__ float warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, words = sum_words(E);
+    const int columns = min((E + 32) / 32 * 32, kRouterJoinThreads), ways = kRouterJoinThreads / columns;
+    const int x = tid % columns, y = tid / columns;
     const float* sums = static_cast<const float*>(a.workspace);
-    const int* counts = reinterpret_cast<const int*>(sums) + E;
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     float balance = 0.0f, squares = 0.0f;
-    for (int e = tid; e <= E; e += blockDim.x) {
+    int tokens = 0;
+    for (int e0 = 0; e0 <= E; e0 += columns) {
+        const int e = e0 + x;
         float p = 0.0f;
         int count = 0;
-#pragma unroll 16
-        for (int b = 0; b < parts; ++b) {
-            count += counts[b * words + e];
-            p += sums[b * words + (e < E ? e : 2 * E + 1)];
+        if (e <= E && y < ways)
+            for (int b0 = y; b0 < parts; b0 += ways * kJoinBatch) {
+                float q[kJoinBatch];
+                int c[kJoinBatch];
+#pragma unroll
+                for (int i = 0; i < kJoinBatch; ++i) {
+                    const float* part = sums + min(b0 + i * ways, parts - 1) * words;
+                    q[i] = part[e < E ? e : 2 * E + 1];
+                    c[i] = reinterpret_cast<const int*>(part)[E + e];
+                }
+#pragma unroll
+                for (int i = 0; i < kJoinBatch; ++i) {
+                    const bool use = b0 + i * ways < parts;
+                    p += use ? q[i] : 0.0f;
+                    count += use ? c[i] : 0;
+                }
+            }
+        probs[tid] = p;
+        counts[tid] = count;
+        __syncthreads();
+        if (y == 0 && e <= E) {
+            for (int w = 1; w < ways; ++w) {
+                p += probs[w * columns + x];
+                count += counts[w * columns + x];
+            }
+            a.counts[e] = count;
+            if (e < E) {
+                balance = fmaf(static_cast<float>(count), p, balance);
+            } else {                        // this thread keeps them for the loss
+                tokens = count;
+                squares = p;
+            }
         }
-        a.counts[e] = count;
-        if (e < E) {
-            balance = fmaf(static_cast<float>(count), p, balance);
-        } else {
-            all_tokens = count;
-            squares = p;
-        }
+        __syncthreads();
     }
     balance = dev::warp_sum(balance);
-    squares = dev::warp_sum(squares);
-    if (lane == 0) {
-        warp_sums[0][warp] = balance;
-        warp_sums[1][warp] = squares;
-    }
+    if (lane == 0) warp_sums[warp] = balance;
     __syncthreads();
-    if (tid >= 32) return;
-    balance = dev::warp_sum(warp_sums[0][lane]);
-    squares = dev::warp_sum(warp_sums[1][lane]);
-    if (tid == 0) put_loss(a, balance, squares, all_tokens);
+    if (tid != E % columns) return;
+    balance = 0.0f;
+    for (int w = 0; w < 32; ++w) balance += warp_sums[w];
+    put_loss(a, balance, squares, tokens);
 }
 
 // With p = softmax(logits), A_e = c f_e + (its weight's gradient, where weights are
@@ -275,33 +310,40 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
     }
     for (int64_t t = int64_t(blockIdx.x) * kRouterWarps + warp; t < a.tokens; t += int64_t(gridDim.x) * kRouterWarps) {
         T* out = static_cast<T*>(a.dlogits) + t * E;
-        float x[N], g[N] = {}, each[N];
-        float top = -INFINITY;
-        bool nan = false;
-        if (!a.mask || a.mask[t]) {
-            load_logits<N, T>(a, t, x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                top = fmaxf(top, x[i]);
-                nan |= x[i] != x[i];
-            }
-        }
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-        if (!__any_sync(kAll, top > -INFINITY || nan)) {      // not a token
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (lane + 32 * i < E) dev::from_f32(out[lane + 32 * i], 0.0f);
-            continue;
-        }
+        Token<N, T> token;
+        token.load(a, t);
         int chosen[2];
         float dw[2], w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int k = lane + 32 * i;
-            chosen[i] = k < K ? a.idx[t * K + k] : -1;
-            if (chosen[i] >= E || !a.dweights) chosen[i] = -1;
-            dw[i] = chosen[i] >= 0 ? a.dweights[t * K + k] : 0.0f;
+            const bool here = a.dweights && k < K;
+            chosen[i] = here ? a.idx[t * K + k] : -1;
+            dw[i] = here ? a.dweights[t * K + k] : 0.0f;
         }
+        float x[N], g[N] = {}, each[N];
+        float top = -INFINITY;
+        bool some = false;                       // a logit that is not -inf
+        token.get(a, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            top = fmaxf(top, x[i]);
+            some |= !(x[i] == -INFINITY);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        if (!__any_sync(kAll, some && token.counted)) {       // padding
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (lane + 32 * i < E) dev::from_f32(out[lane + 32 * i], 0.0f);
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (chosen[i] < 0 || chosen[i] >= E) {
+                chosen[i] = -1;
+                dw[i] = 0.0f;
+            }
 #pragma unroll
         for (int i = 0; i < N; ++i) each[i] = load[i];
         if (a.normalize) {

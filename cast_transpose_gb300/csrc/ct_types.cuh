@@ -155,6 +155,31 @@ __device__ __forceinline__ void load_cols(const T* row, const Cols<G>& c, float 
     }
 }
 
+// The same in two steps: the loads of several rows can be in flight before the
+// first is used.  No load is conditional: columns past the row's end are read from
+// its beginning.  (load_cols ends a condition with a value in hand, so that one of
+// its loads waits for the one before.)
+template <int G, typename T>
+struct RawCols;
+template <typename T>
+struct RawCols<8, T> {
+    Raw8<T> v;
+    __device__ __forceinline__ void load(const T* row, const Cols<8>& c) { v = load8(row + (c.any() ? c.first : 0)); }
+    __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(v, f); }
+};
+template <typename T>
+struct RawCols<1, T> {
+    T v[8];
+    __device__ __forceinline__ void load(const T* row, const Cols<1>& c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = row[c.has(j) ? c.at(j) : 0];
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = to_f32(v[j]);
+    }
+};
+
 template <int G, typename T>
 __device__ __forceinline__ void store_cols(T* row, const Cols<G>& c, const float (&f)[8]) {
     if constexpr (G == 8) {
