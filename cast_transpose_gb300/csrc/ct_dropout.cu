@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutArgs
         T* out = static_cast<T*>(a.out) + row * a.cols;
         float f[8];
         dev::load_cols<G>(x, c, f);
-        if (drops.some) drops.apply(drops.kept<G>(static_cast<uint32_t>(row), vi), f);
+        if (drops.some) drops.apply<G>(static_cast<uint32_t>(row), vi, f);
         dev::store_cols<G>(out, c, f);
     }
 }

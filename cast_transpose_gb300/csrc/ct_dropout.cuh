@@ -48,46 +48,38 @@ struct Drops {
         key = make_uint2(uint32_t(s.x), uint32_t(s.x >> 32));
         step = uint32_t(s.y);
     }
-    // Bit j: column 8 * group + j of the row is kept.
-    __device__ __forceinline__ uint32_t kept8(uint32_t row, uint32_t group) const {
-        const uint4 r = philox4x32(make_uint4(group, row, site, step), key);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bits |= ((w[i] << 16) >= cut ? 1u : 0u) << (2 * i);
-            bits |= (w[i] >= cut ? 1u : 0u) << (2 * i + 1);
-        }
-        return bits;
+    __device__ __forceinline__ uint4 words(uint32_t row, uint32_t group) const {
+        return philox4x32(make_uint4(group, row, site, step), key);
     }
-    // Of a thread's columns Cols<G>(vi) of a row: its own group is group0 + vi,
-    // and where its columns are spread over the warp's 32 groups the lanes pass
-    // each other their bits.  The whole warp has to call it.
+    // v of the thread's columns Cols<G>(vi), dropped or scaled.  With G = 8 they are
+    // the group's own; where they are spread over the warp's 32 groups, of which
+    // the lane's has the number `group`, the lanes pass each other a bit for each
+    // column.  The whole warp has to call it.
     template <int G>
-    __device__ __forceinline__ uint32_t kept(uint32_t row, uint32_t group) const {
-        const uint32_t own = kept8(row, group);
-        if constexpr (G == 8) return own;
-        const int lane = threadIdx.x & 31;
-        uint32_t bits = 0;
-        if constexpr (G == 2) {
+    __device__ __forceinline__ void apply(uint32_t row, uint32_t group, float (&v)[8]) const {
+        const uint4 r = words(row, group);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        if constexpr (G == 8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t m = __shfl_sync(0xFFFFFFFFu, own, 8 * i + (lane >> 2));
-                bits |= ((m >> ((2 * lane) & 7)) & 3u) << (2 * i);
+                v[2 * i] = (w[i] << 16) >= cut ? v[2 * i] * scale : 0.0f;
+                v[2 * i + 1] = w[i] >= cut ? v[2 * i + 1] * scale : 0.0f;
             }
         } else {
+            static_assert(G == 1, "pairs are not used");
+            uint32_t own = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                own |= ((w[i] << 16) >= cut ? 1u : 0u) << (2 * i);
+                own |= (w[i] >= cut ? 1u : 0u) << (2 * i + 1);
+            }
+            const int lane = threadIdx.x & 31;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t m = __shfl_sync(0xFFFFFFFFu, own, 4 * j + (lane >> 3));
-                bits |= ((m >> (lane & 7)) & 1u) << j;
+                const uint32_t bits = __shfl_sync(0xFFFFFFFFu, own, 4 * j + (lane >> 3));
+                v[j] = (bits >> (lane & 7)) & 1 ? v[j] * scale : 0.0f;
             }
         }
-        return bits;
-    }
-    // v scaled where its bit is set, else 0, whatever v is.
-    __device__ __forceinline__ void apply(uint32_t bits, float (&v)[8]) const {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (bits >> j) & 1 ? v[j] * scale : 0.0f;
     }
 };
 

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_row_kernel(const La
             float u[8];
             dev::load_cols<G>(static_cast<const T*>(a.u) + at, cols(p), u);
             const Drops drops(a.drop);
-            if (drops.some) drops.apply(drops.kept<G>(static_cast<uint32_t>(row), p * blockDim.x + tid), u);
+            if (drops.some) drops.apply<G>(static_cast<uint32_t>(row), p * blockDim.x + tid, u);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[p][j] += u[j];
             dev::store_cols<G>(static_cast<R*>(a.res_out) + at, cols(p), v[p]);
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
         for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, g[p][j] - level - x[p][j] * along, d[j]);
         dev::store_cols<G>(static_cast<R*>(a.dres) + at, cols(p), d);
         if (!a.du) continue;
-        if (drops.some) drops.apply(drops.kept<G>(static_cast<uint32_t>(row), p * blockDim.x + tid), d);
+        if (drops.some) drops.apply<G>(static_cast<uint32_t>(row), p * blockDim.x + tid, d);
         dev::store_cols<G>(static_cast<T*>(a.du) + at, cols(p), d);
     }
 }
@@ -213,26 +213,30 @@ struct Staged {
     }
 };
 
-// Columns of the thread's group that lie past the row's end are 0 from here on.
+// Columns of the thread's group that lie past the row's end are 0 from here on,
+// where there may be some beside others; a group that is past it as a whole adds
+// nothing by on().
 template <int G>
 __device__ __forceinline__ void cut(const dev::Cols<G>& c, V8& v) {
-    if constexpr (G == 8) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v.p[j] = c.any() ? v.p[j] : 0;
-    } else {
-        float f[8];
-        floats(v, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = c.has(j) ? f[j] : 0.0f;
-        v = pairs(f);
-    }
-}
-
-__device__ __forceinline__ V8 dropped(const Drops& drops, uint32_t bits, const V8& v) {
+    if constexpr (G == 8) return;
     float f[8];
     floats(v, f);
-    drops.apply(bits, f);
-    return pairs(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = c.has(j) ? f[j] : 0.0f;
+    v = pairs(f);
+}
+
+template <int G>
+__device__ __forceinline__ void drop(const Drops& drops, int64_t row, int item, V8& v) {
+    float f[8];
+    floats(v, f);
+    drops.apply<G>(static_cast<uint32_t>(row), item, f);
+    v = pairs(f);
+}
+// s / n, rounded to nearest but for rare last bits, given r = 1 / n.
+__device__ __forceinline__ float divided(float s, float n, float r) {
+    const float q = s * r;
+    return fmaf(fmaf(-q, n, s), r, q);
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
@@ -293,6 +297,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const Layer
         return static_cast<float>(n);
     };
     const float own_columns = columns_of(warp), lane_columns = lane < warps ? columns_of(lane) : 1.0f;
+    const float per_own = 1.0f / own_columns, per_lane = 1.0f / lane_columns, per_column = 1.0f / H;
     unsigned most = 0;
     int stage = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -301,45 +306,58 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const Layer
         if (G != 8) __syncthreads();
         const uint8_t* here = smem + stage * stage_bytes;
         V8 v[kRingPer];
-        uint64_t part = 0;
+        float sum_w = 0.0f, squares_w = 0.0f;
+        if (a.u) {
+            V8 x[kRingPer];
 #pragma unroll
-        for (int p = 0; p < kRingPer; ++p) {
-            v[p] = res.get(here, row, p);
-            if (a.u) {
-                V8 x = u.get(here + second, row, p);
-                if (drops.some) x = dropped(drops, drops.kept<G>(static_cast<uint32_t>(row), p * blockDim.x + tid), x);
+            for (int p = 0; p < kRingPer; ++p) x[p] = u.get(here + second, row, p);
+            if (drops.some) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[p].p[j] = add2(v[p].p[j], x.p[j]);
+                for (int p = 0; p < kRingPer; ++p) drop<G>(drops, row, p * blockDim.x + tid, x[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < kRingPer; ++p) {
+                v[p] = res.get(here, row, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[p].p[j] = add2(v[p].p[j], x[p].p[j]);
                 store_v8<G>(static_cast<R*>(a.res_out) + at, cols(p), v[p]);
             }
-            cut<G>(cols(p), v[p]);
+        } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part = add2(part, v[p].p[j]);
+            for (int p = 0; p < kRingPer; ++p) v[p] = res.get(here, row, p);
+        }
+#pragma unroll
+        for (int p = 0; p < kRingPer; ++p) {
+            cut<G>(cols(p), v[p]);
+            const float part = lanes_sum(add2(add2(v[p].p[0], v[p].p[1]), add2(v[p].p[2], v[p].p[3])));
+            sum_w += on(cols(p)) ? part : 0.0f;
         }
         // the stage before this one is free
         fetch(row + int64_t(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
         if (++stage == stages) stage = 0;
-        const float sum_w = dev::warp_sum(lanes_sum(part)), mean_w = sum_w / own_columns;
+        sum_w = dev::warp_sum(sum_w);
+        const float mean_w = divided(sum_w, own_columns, per_own);
         const uint64_t away = pair(-mean_w, -mean_w);
-        part = 0;
 #pragma unroll
         for (int p = 0; p < kRingPer; ++p) {
             V8 d;
+            uint64_t part = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) d.p[j] = add2(v[p].p[j], away);
             cut<G>(cols(p), d);
 #pragma unroll
             for (int j = 0; j < 4; ++j) part = fma2(d.p[j], d.p[j], part);
+            squares_w += on(cols(p)) ? lanes_sum(part) : 0.0f;
         }
-        const float squares_w = dev::warp_sum(lanes_sum(part));
+        squares_w = dev::warp_sum(squares_w);
         if (lane == 0) slots[turn][warp] = make_float2(sum_w, squares_w);
         __syncthreads();
         const float2 other = lane < warps ? slots[turn][lane] : make_float2(0.0f, 0.0f);
         turn ^= 1;
         const float mean = dev::warp_sum(other.x) / H;
-        const float apart = lane < warps ? other.x / lane_columns - mean : 0.0f;
+        const float apart = lane < warps ? divided(other.x, lane_columns, per_lane) - mean : 0.0f;
         const float squares = dev::warp_sum(fmaf(lane_columns * apart, apart, other.y));
-        const float rstd = rsqrtf(squares / H + a.eps);
+        const float rstd = rsqrtf(fmaf(squares, per_column, a.eps));
         if (tid == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
@@ -408,6 +426,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(p), f);
         w[p] = pairs(f);
     }
+    const float per_column = 1.0f / H;
     float mean = 0.0f, rstd = 0.0f;
     if (blockIdx.x < a.rows) {
         mean = a.mean[blockIdx.x];
@@ -424,11 +443,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         fetch(row + int64_t(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
         if (++stage == stages) stage = 0;
         const uint64_t mean2 = pair(-mean, -mean), rstd2 = pair(rstd, rstd);
-        uint64_t sum_g = 0, sum_gx = 0;
+        float one = 0.0f, two = 0.0f;
 #pragma unroll
         for (int p = 0; p < kRingPer; ++p) {
             const V8 x = res.get(here, row, p);
             V8 g = dy.get(here + second, row, p);
+            uint64_t sum_g = 0, sum_gx = 0;
             cut<G>(cols(p), g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -438,13 +458,16 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 sum_g = add2(sum_g, gw);
                 sum_gx = fma2(gw, hat, sum_gx);
             }
+            one += on(cols(p)) ? lanes_sum(sum_g) : 0.0f;
+            two += on(cols(p)) ? lanes_sum(sum_gx) : 0.0f;
         }
-        const float one = dev::warp_sum(lanes_sum(sum_g)), two = dev::warp_sum(lanes_sum(sum_gx));
+        one = dev::warp_sum(one);
+        two = dev::warp_sum(two);
         if (lane == 0) slots[turn][warp] = make_float2(one, two);
         __syncthreads();
         const float2 other = lane < warps ? slots[turn][lane] : make_float2(0.0f, 0.0f);
         turn ^= 1;
-        const float level = -dev::warp_sum(other.x) / H, along = -dev::warp_sum(other.y) / H;
+        const float level = -dev::warp_sum(other.x) * per_column, along = -dev::warp_sum(other.y) * per_column;
         const uint64_t level2 = pair(level, level), along2 = pair(along, along);
 #pragma unroll
         for (int p = 0; p < kRingPer; ++p) {
@@ -458,7 +481,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
             store_v8<G>(static_cast<R*>(a.dres) + at, cols(p), d);
             if (!a.du) continue;
-            if (drops.some) d = dropped(drops, drops.kept<G>(static_cast<uint32_t>(row), p * blockDim.x + tid), d);
+            if (drops.some) drop<G>(drops, row, p * blockDim.x + tid, d);
             store_v8<G>(static_cast<T*>(a.du) + at, cols(p), d);
         }
         mean = next_mean;
