@@ -213,35 +213,83 @@ def _ptr(t, name, dtype, shape) -> int:
     return _dev(t, name, dtype)
 
 
-def _given(t, name, dtype, shape):
-    """_ptr of an optional tensor."""
-    return None if t is None else _ptr(t, name, dtype, shape)
-
-
-def _here(stream, *tensors) -> int:
-    """The stream's handle, as _stream, for a call whose tensors (or None) and
-    stream have to be the current device's."""
-    device = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is "
-                             f"cuda:{device}")
+def _here(stream):
+    """The current device, which all tensors of a call have to be on (-2: there is
+    none), and the handle of the stream, which has to be its, too."""
+    try:
+        device = torch._C._cuda_getDevice()
+    except AttributeError:
+        device = torch.cuda.current_device()
+    except RuntimeError:
+        return -2, 0
     if stream is not None and stream.device_index != device:
         raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is "
                          f"cuda:{device}")
-    return _stream(stream)
+    return device, _stream(stream)
+
+
+def _at(t, name, dtype, shape, device):
+    """As _ptr, for a tensor (None: left out) that has to be on this device."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _ptr(t, name, dtype, shape)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                         f"cuda:{device}")
+    return p
+
+
+def _need(t, name, dtype, shape, device):
+    """As _at, where the tensor cannot be left out."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return _at(t, name, dtype, shape, device)
+
+
+def _scalar(t, name, device):
+    """As _opt, for a tensor that has to be on this device."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is torch.float32 and t.numel() == 1 and t.get_device() == device:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _opt(t, name)
+    return _at(t, name, torch.float32, t.shape, device)
+
+
+def _space(t, device):
+    """The address and the bytes of a workspace."""
+    if t is None:
+        return None, 0
+    try:
+        if t.dtype is torch.uint8 and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
+    _dev(t, "workspace", torch.uint8)
+    return _at(t, "workspace", torch.uint8, t.shape, device), t.numel()
 
 
 _RNG = (2,)
 
 
-def _random(rng, p, site):
+def _random(rng, p, site, device):
     """The address of a generator's state (None: nothing is dropped)."""
     if not 0 <= site < 1 << 32:
         raise ValueError(f"site is {site}, expected 0 .. 2^32 - 1")
-    if rng is None and p * 65536 >= 0.5:
-        raise ValueError("a dropout needs rng: int64 [2], seed and step")
-    return _given(rng, "rng", torch.int64, _RNG)
+    if rng is None:
+        if p * 65536 >= 0.5:
+            raise ValueError("a dropout needs rng: int64 [2], seed and step")
+        return None
+    return _at(rng, "rng", torch.int64, _RNG, device)
 
 
 def _rc(x: torch.Tensor):

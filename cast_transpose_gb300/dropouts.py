@@ -9,15 +9,17 @@ to the nearest 1/65536.
 """
 from __future__ import annotations
 
-from . import _check, _here, _ptr, _opt, _random, lib
+from . import _check, _here, _need, _random, _scalar, lib
 from .moe import _DTYPES, _rows_of
 
 
 def dropout(x, out, p, rng, site=0, noop_flag=None, stream=None) -> None:
     """x [rows, cols] -> out of the same type, or x itself: 0 with probability
     p, else x / (1 - p).  With the gradient of out for x, its gradient."""
+    device, handle = _here(stream)
     cols, dtype = _rows_of(x, "x")
     shape = x.shape
-    _check(lib().dropout(_ptr(x, "x", dtype, shape), shape[0], cols, _DTYPES[dtype], p,
-                         _random(rng, p, site), site, _ptr(out, "out", dtype, shape),
-                         _opt(noop_flag, "noop_flag"), _here(stream, x, out, rng, noop_flag)))
+    _check(lib().dropout(_need(x, "x", dtype, shape, device), shape[0], cols, _DTYPES[dtype], p,
+                         _random(rng, p, site, device), site,
+                         _need(out, "out", dtype, shape, device),
+                         _scalar(noop_flag, "noop_flag", device), handle))

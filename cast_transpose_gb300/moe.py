@@ -23,12 +23,13 @@ synchronised, everything can be captured in a CUDA graph.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from operator import attrgetter
 
 import torch
 
-from . import E4M3, _check, _dev, _given, _here, _opt, _ptr, _stream, _U8, lib
+from . import (E4M3, _at, _check, _dev, _here, _need, _opt, _ptr, _scalar, _space, _stream, _U8,
+               lib)
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _I32, _F32 = torch.int32, torch.float32
@@ -178,10 +179,8 @@ def moe_combine_backward(dout, ys, plan: MoePlan, weights, dys=None, dweights=No
                                       pw, _opt(noop_flag, "noop_flag"), _stream(stream)))
 
 
-class _RouterConfig(ctypes.Structure):
-    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int), ("topk", ctypes.c_int),
-                ("dtype", ctypes.c_int), ("flags", ctypes.c_int), ("balance", ctypes.c_float),
-                ("z", ctypes.c_float)]
+# ct_router_config: tokens, experts, topk, dtype, flags, balance, z
+_router_config = struct.Struct("@q4i2f").pack
 
 
 def moe_router_workspace_size(tokens: int, topk: int, experts: int) -> int:
@@ -189,16 +188,23 @@ def moe_router_workspace_size(tokens: int, topk: int, experts: int) -> int:
 
 
 def _router(logits, expert_idx, normalize, balance, z):
-    """The call's config, and the shape of what is per slot."""
+    """The call's config, the number of experts and the shape of what is per slot."""
     experts, dtype = _rows_of(logits, "logits")
     if not isinstance(expert_idx, torch.Tensor) or expert_idx.dim() != 2:
         raise ValueError("expert_idx must be a 2-D matrix")
-    tokens, slots = logits.shape[0], (logits.shape[0], expert_idx.shape[1])
-    return _RouterConfig(tokens, experts, slots[1], _DTYPES[dtype], 1 if normalize else 0, balance,
-                         z), slots
+    slots = logits.shape[0], expert_idx.shape[1]
+    return _router_config(slots[0], experts, slots[1], _DTYPES[dtype], 1 if normalize else 0,
+                          balance, z), experts, slots
 
 
 _MASK = (torch.bool, torch.uint8)
+
+
+def _mask(mask, shape, device):
+    if mask is None:
+        return None
+    dtype = getattr(mask, "dtype", None)
+    return _at(mask, "mask", dtype if dtype in _MASK else _MASK, shape, device)
 
 
 def moe_router(logits, expert_idx, weights, counts, loss=None, mask=None, normalize=True,
@@ -211,14 +217,14 @@ def moe_router(logits, expert_idx, weights, counts, loss=None, mask=None, normal
     with normalize divided by their sum.  mask bool or uint8 [T]: 0 for padding
     tokens, which choose expert -1.  workspace: uint8, of at least
     moe_router_workspace_size(T, K, E) bytes."""
-    cfg, slots = _router(logits, expert_idx, normalize, balance, z)
+    device, handle = _here(stream)
+    cfg, experts, slots = _router(logits, expert_idx, normalize, balance, z)
     _check(lib().moe_router(
-        ctypes.byref(cfg), _ptr(logits, "logits", logits.dtype, logits.shape),
-        _given(mask, "mask", _MASK, slots[:1]), _ptr(expert_idx, "expert_idx", _I32, slots),
-        _ptr(weights, "weights", _F32, slots), _ptr(counts, "counts", _I32, (cfg.experts + 1,)),
-        _opt(loss, "loss"), None if workspace is None else _dev(workspace, "workspace", torch.uint8),
-        0 if workspace is None else workspace.numel(), _opt(noop_flag, "noop_flag"),
-        _here(stream, logits, mask, expert_idx, weights, counts, loss, workspace, noop_flag)))
+        cfg, _need(logits, "logits", logits.dtype, logits.shape, device),
+        _mask(mask, slots[:1], device), _need(expert_idx, "expert_idx", _I32, slots, device),
+        _need(weights, "weights", _F32, slots, device),
+        _need(counts, "counts", _I32, (experts + 1,), device), _scalar(loss, "loss", device),
+        *_space(workspace, device), _scalar(noop_flag, "noop_flag", device), handle))
 
 
 def moe_router_backward(dweights, dloss, logits, expert_idx, counts, dlogits, mask=None,
@@ -226,12 +232,13 @@ def moe_router_backward(dweights, dloss, logits, expert_idx, counts, dlogits, ma
     """From dweights fp32 [T, K] and dloss fp32 [1] (either may be None: zero)
     and the forward pass's logits, mask, expert_idx and counts: dlogits [T, E]
     of the logits' type."""
-    cfg, slots = _router(logits, expert_idx, normalize, balance, z)
+    device, handle = _here(stream)
+    cfg, experts, slots = _router(logits, expert_idx, normalize, balance, z)
     dtype, shape = logits.dtype, logits.shape
     _check(lib().moe_router_backward(
-        ctypes.byref(cfg), _ptr(logits, "logits", dtype, shape),
-        _given(mask, "mask", _MASK, slots[:1]), _ptr(expert_idx, "expert_idx", _I32, slots),
-        _ptr(counts, "counts", _I32, (cfg.experts + 1,)),
-        _given(dweights, "dweights", _F32, slots), _opt(dloss, "dloss"),
-        _ptr(dlogits, "dlogits", dtype, shape), _opt(noop_flag, "noop_flag"),
-        _here(stream, logits, mask, expert_idx, counts, dweights, dloss, dlogits, noop_flag)))
+        cfg, _need(logits, "logits", dtype, shape, device), _mask(mask, slots[:1], device),
+        _need(expert_idx, "expert_idx", _I32, slots, device),
+        _need(counts, "counts", _I32, (experts + 1,), device),
+        _at(dweights, "dweights", _F32, slots, device), _scalar(dloss, "dloss", device),
+        _need(dlogits, "dlogits", dtype, shape, device),
+        _scalar(noop_flag, "noop_flag", device), handle))

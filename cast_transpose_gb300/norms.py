@@ -20,10 +20,12 @@ dropouts.py, its choices made again in the backward pass.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from . import E4M3, _check, _dev, _here, _opt, _ptr, _random, _stream, _U8, lib
+from . import (E4M3, _at, _check, _dev, _here, _need, _opt, _ptr, _random, _scalar, _space,
+               _stream, _U8, lib)
 from .moe import _DTYPES
 
 _F32 = torch.float32
@@ -153,23 +155,22 @@ def block_norm_backward(dy, dres_out, u, res_out, rstd_post, rstd_pre, du=None, 
         _stream(stream)))
 
 
-class _LayerConfig(ctypes.Structure):
-    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("weight", ctypes.c_void_p),
-                ("bias", ctypes.c_void_p), ("rng", ctypes.c_void_p), ("eps", ctypes.c_float),
-                ("weight_offset", ctypes.c_float), ("p", ctypes.c_float),
-                ("site", ctypes.c_uint32), ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int),
-                ("param_dtype", ctypes.c_int)]
+# ct_layer_norm_config: rows, hidden, weight, bias, rng, eps, weight_offset, p,
+# site, dtype, res_dtype, param_dtype
+_pack_layer_config = struct.Struct("@2q3P3fI3i4x").pack
 
 
-def _layer_config(shape, res_dtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site):
+def _layer_config(shape, res_dtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site,
+                  device):
     columns = shape[1:]
     try:
         types = _DTYPES[dtype], _DTYPES[res_dtype], _DTYPES[ptype]
     except KeyError as e:
         raise TypeError(f"dtype {e} is not bfloat16, float16 or float32") from None
-    return _LayerConfig(*shape, _given(weight, "weight", ptype, columns),
-                        _given(bias, "bias", ptype, columns), _random(rng, p, site), eps,
-                        weight_offset, p, site, *types)
+    return _pack_layer_config(*shape, _at(weight, "weight", ptype, columns, device) or 0,
+                              _at(bias, "bias", ptype, columns, device) or 0,
+                              _random(rng, p, site, device) or 0, eps, weight_offset, p, site,
+                              *types)
 
 
 def layer_norm(u, res, res_out=None, y=None, weight=None, bias=None, eps=1e-5, weight_offset=0.0,
@@ -181,6 +182,7 @@ def layer_norm(u, res, res_out=None, y=None, weight=None, bias=None, eps=1e-5, w
     and site: the dropout of u.  mean, rstd fp32 [rows]: kept for the backward
     pass.  With scale, amax and scale_inv (fp32 scalars) y is FP8 of format fmt,
     cast as fp8_cast does."""
+    device, handle = _here(stream)
     shape, rtype = _matrix(res, "res")
     rows = shape[:1]
     if u is not None:
@@ -189,15 +191,20 @@ def layer_norm(u, res, res_out=None, y=None, weight=None, bias=None, eps=1e-5, w
         dtype = _dtype_of(y, "y") if scale is None else rtype
     first = weight if weight is not None else bias
     ptype = dtype if first is None else _dtype_of(first, "weight" if first is weight else "bias")
-    cfg = _layer_config(shape, rtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site)
+    cfg = _layer_config(shape, rtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site,
+                        device)
+    if scale is None:
+        ytype = dtype
+    else:
+        ytype = getattr(y, "dtype", None)
+        ytype = ytype if ytype in _U8 else _U8
     _check(lib().layer_norm(
-        ctypes.byref(cfg), _given(u, "u", dtype, shape), _ptr(res, "res", rtype, shape),
-        _given(res_out, "res_out", rtype, shape),
-        _given(y, "y", dtype if scale is None else _U8, shape), _given(mean, "mean", _F32, rows),
-        _given(rstd, "rstd", _F32, rows), _opt(scale, "scale"), _opt(amax, "amax"),
-        _opt(scale_inv, "scale_inv"), fmt, _opt(noop_flag, "noop_flag"),
-        _here(stream, u, res, res_out, y, weight, bias, rng, mean, rstd, scale, amax, scale_inv,
-              noop_flag)))
+        cfg, _at(u, "u", dtype, shape, device), _need(res, "res", rtype, shape, device),
+        _at(res_out, "res_out", rtype, shape, device), _need(y, "y", ytype, shape, device),
+        _at(mean, "mean", _F32, rows, device), _at(rstd, "rstd", _F32, rows, device),
+        _scalar(scale, "scale", device), _scalar(amax, "amax", device),
+        _scalar(scale_inv, "scale_inv", device), fmt, _scalar(noop_flag, "noop_flag", device),
+        handle))
 
 
 def layer_norm_backward_workspace_size(rows: int, hidden: int) -> int:
@@ -212,20 +219,19 @@ def layer_norm_backward(dy, dres_out, res_out, mean, rstd, dres, du=None, dweigh
     forward pass's p, rng and site), dweight and dbias that are given, the last
     two of weight's type.  workspace: uint8, of at least
     layer_norm_backward_workspace_size(rows, hidden) bytes."""
+    device, handle = _here(stream)
     shape, rtype = _matrix(dres, "dres")
     rows, columns = shape[:1], shape[1:]
     dtype = _dtype_of(dy, "dy")
     first = weight if weight is not None else dweight if dweight is not None else dbias
     ptype = dtype if first is None else _dtype_of(
         first, "weight" if first is weight else "dweight" if first is dweight else "dbias")
-    cfg = _layer_config(shape, rtype, dtype, ptype, weight, None, rng, 0.0, weight_offset, p, site)
+    cfg = _layer_config(shape, rtype, dtype, ptype, weight, None, rng, 0.0, weight_offset, p, site,
+                        device)
     _check(lib().layer_norm_backward(
-        ctypes.byref(cfg), _ptr(dy, "dy", dtype, shape), _given(dres_out, "dres_out", rtype, shape),
-        _ptr(res_out, "res_out", rtype, shape), _ptr(mean, "mean", _F32, rows),
-        _ptr(rstd, "rstd", _F32, rows), _ptr(dres, "dres", rtype, shape),
-        _given(du, "du", dtype, shape), _given(dweight, "dweight", ptype, columns),
-        _given(dbias, "dbias", ptype, columns),
-        None if workspace is None else _dev(workspace, "workspace", torch.uint8),
-        0 if workspace is None else workspace.numel(), _opt(noop_flag, "noop_flag"),
-        _here(stream, dy, dres_out, res_out, mean, rstd, dres, du, dweight, dbias, workspace,
-              weight, rng, noop_flag)))
+        cfg, _need(dy, "dy", dtype, shape, device), _at(dres_out, "dres_out", rtype, shape, device),
+        _need(res_out, "res_out", rtype, shape, device), _need(mean, "mean", _F32, rows, device),
+        _need(rstd, "rstd", _F32, rows, device), _need(dres, "dres", rtype, shape, device),
+        _at(du, "du", dtype, shape, device), _at(dweight, "dweight", ptype, columns, device),
+        _at(dbias, "dbias", ptype, columns, device), *_space(workspace, device),
+        _scalar(noop_flag, "noop_flag", device), handle))

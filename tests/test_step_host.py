@@ -1,14 +1,12 @@
 """Host-side refusals of dropout, layer norm, router and embedding (no GPU
 needed): status codes of the C ABI and errors of the binding.  The pointers
 passed are never dereferenced."""
-import ctypes
-
 import pytest
 import torch
 
 import cast_transpose_gb300 as ct
-from cast_transpose_gb300.moe import _RouterConfig
-from cast_transpose_gb300.norms import _LayerConfig
+from cast_transpose_gb300.moe import _router_config
+from cast_transpose_gb300.norms import _pack_layer_config
 
 OK, NULL, SHAPE, ALIGN, FORMAT, ARG, ALIAS, WORKSPACE = range(8)
 A, B, C, D, E, F, G, H, I, J, K, M = (0x100000000 * (i + 1) for i in range(12))
@@ -42,7 +40,7 @@ def config(**kw):
     c = dict(rows=10, hidden=64, weight=K, bias=M, rng=J, eps=1e-5, weight_offset=0.0, p=0.1, site=0, dtype=0,
              res_dtype=0, param_dtype=0)
     c.update({k: v for k, v in kw.items() if k in c})
-    return ctypes.byref(_LayerConfig(*c.values())), {k: v for k, v in kw.items() if k not in c}
+    return _pack_layer_config(*(0 if v is None else v for v in c.values())), {k: v for k, v in kw.items() if k not in c}
 
 
 def test_layer_norm_rejects(L):
@@ -105,7 +103,7 @@ def test_layer_norm_backward_rejects(L):
 def router(**kw):
     c = dict(tokens=10, experts=8, topk=2, dtype=2, flags=1, balance=0.1, z=0.1)
     c.update({k: v for k, v in kw.items() if k in c})
-    return ctypes.byref(_RouterConfig(*c.values())), {k: v for k, v in kw.items() if k not in c}
+    return _router_config(*c.values()), {k: v for k, v in kw.items() if k not in c}
 
 
 BAD_ROUTERS = [(dict(dtype=3), FORMAT), (dict(experts=0), ARG), (dict(experts=1025), ARG), (dict(topk=0), ARG),
@@ -210,7 +208,7 @@ def fake(monkeypatch, L):
     f = Fake(L)
     monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(ct, "_stream", lambda stream: 0)
     for m in MODULES:
         monkeypatch.setattr(importlib.import_module("cast_transpose_gb300." + m), "lib", lambda: f)
@@ -334,8 +332,16 @@ def test_another_device_is_refused(fake, monkeypatch):
     x, rng = torch.zeros(4, 8, dtype=BF), torch.zeros(2, dtype=torch.int64)
     out = torch.zeros(4, 8, dtype=BF)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is rng else 0)
-    with pytest.raises(ValueError, match="cuda:1"):
+    with pytest.raises(ValueError, match="rng is on cuda:1"):
         ct.dropout(x, out, 0.1, rng)
+    flag = torch.zeros(1)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is flag else 0)
+    with pytest.raises(ValueError, match="noop_flag is on cuda:1"):
+        ct.dropout(x, out, 0.1, rng, noop_flag=flag)
+    space = torch.zeros(1 << 16, dtype=torch.uint8)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is space else 0)
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        ct.embedding_backward(torch.zeros(4, dtype=torch.int64), x, out, space)
 
     class Stream:
         device_index, cuda_stream = 1, 0
