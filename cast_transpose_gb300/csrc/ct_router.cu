@@ -53,6 +53,65 @@ struct Token {
     }
 };
 
+// The largest of the lanes' values, a NaN if there is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lanes_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// A lane's choice: slot i of the token gets the expert (-1: none) with this logit.
+struct Choice {
+    int slot, expert;
+    float logit;
+};
+
+// The K <= 32 largest logits x of a token, whose largest, `top`, is a number.  The
+// K-th largest of the lanes' own largest is a bound that K logits reach at least,
+// and few more do (with 8 of 256 some 10): those go to a lane each and are ranked by
+// comparing all with all.  False where more than 32 reach it: many equal ones.
+template <int N>
+__device__ __forceinline__ bool choose_few(const float (&x)[N], float best, float top, int K, float2* among,
+                                           Choice& mine) {
+    const int lane = threadIdx.x & 31;
+    float bound = top;
+    for (int k = 1; k < K; ++k) {
+        const unsigned with = __ballot_sync(kAll, best == bound);
+        if (lane == __ffs(with) - 1) best = -INFINITY;
+        bound = lanes_max(best);
+    }
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool reaches = x[i] >= bound && x[i] > -INFINITY;
+        const unsigned with = __ballot_sync(kAll, reaches);
+        const int at = total + __popc(with & ((1u << lane) - 1));
+        if (reaches && at < 32) among[at] = make_float2(x[i], __int_as_float(lane + 32 * i));
+        total += __popc(with);
+    }
+    if (total > 32) return false;
+    __syncwarp();
+    const bool here = lane < total;
+    const float2 own = among[here ? lane : 0];
+    mine.logit = own.x;
+    mine.expert = __float_as_int(own.y);
+    int before = 0;
+    for (int j = 0; j < total; ++j) {
+        const float2 other = among[j];
+        before += other.x > mine.logit || (other.x == mine.logit && __float_as_int(other.y) < mine.expert);
+    }
+    __syncwarp();
+    // slots past the number of those that can be chosen get none
+    mine.slot = here ? before : lane;
+    if (!here) mine.expert = -1;
+    return true;
+}
+
 // exp(x - top) in place of x; the sum of all.
 template <int N>
 __device__ __forceinline__ float exponentials(float (&x)[N], float top) {
@@ -87,6 +146,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
     float* probs = own + sum_words(a.experts);                          // [warps][E]
     __shared__ float warp_squares[kRouterWarps], warp_balance[kRouterWarps];
     __shared__ float block_balance;
+    __shared__ float2 among[kRouterWarps][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, K = a.topk;
     const auto cluster = cooperative_groups::this_cluster();
     const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -105,37 +165,42 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
     if (kAhead && t < a.tokens) next.load(a, t);
     for (; t < a.tokens; t += step) {
         float x[N];
-        unsigned key[N];
-        int chosen[2] = {-1, -1};           // lane k: of slots k and k + 32
-        float logit[2] = {};
         if (!kAhead) next.load(a, t);
         next.get(a, x);
         const bool counted = next.counted;
         if (kAhead && t + step < a.tokens) next.load(a, t + step);
+        float best = x[0];
 #pragma unroll
-        for (int i = 0; i < N; ++i) key[i] = counted && lane + 32 * i < E ? order_of(x[i]) : 0;
-        float top = 0.0f;
-        bool any = false;
-        for (int k = 0; k < K; ++k) {
-            unsigned best = key[0];
+        for (int i = 1; i < N; ++i) best = max_nan(best, x[i]);
+        float top = lanes_max(best);
+        const bool any = counted && !(top == -INFINITY);
+        Choice mine[2] = {{lane, -1, 0.0f}, {lane + 32, -1, 0.0f}};
+        // (with a lane's one or two logits there is nothing to leave out first)
+        const bool few = N >= 4 && K <= 32 && top == top;
+        if (any && !(few && choose_few<N>(x, best, top, K, among[warp], mine[0]))) {
+            // one after the other
+            unsigned key[N];
 #pragma unroll
-            for (int i = 1; i < N; ++i) best = max(best, key[i]);
-            const unsigned most = __reduce_max_sync(kAll, best);
-            if (most <= kNever) break;
-            unsigned mine = 0xFFFFu;        // the lowest of the lane's experts with it
+            for (int i = 0; i < N; ++i) key[i] = lane + 32 * i < E ? order_of(x[i]) : 0;
+            for (int k = 0; k < K; ++k) {
+                unsigned high = key[0];
 #pragma unroll
-            for (int i = N - 1; i >= 0; --i) mine = key[i] == most ? lane + 32 * i : mine;
-            const int e = __reduce_min_sync(kAll, mine);
-            if (k == 0) {
-                top = of_order(most);
-                any = true;
+                for (int i = 1; i < N; ++i) high = max(high, key[i]);
+                const unsigned most = __reduce_max_sync(kAll, high);
+                if (most <= kNever) break;
+                unsigned low = 0xFFFFu;     // the lowest of the lane's experts with it
+#pragma unroll
+                for (int i = N - 1; i >= 0; --i) low = key[i] == most ? lane + 32 * i : low;
+                const int e = __reduce_min_sync(kAll, low);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (k == mine[i].slot) {
+                        mine[i].expert = e;
+                        mine[i].logit = of_order(most);
+                    }
+#pragma unroll
+                for (int i = 0; i < N; ++i) key[i] = e == lane + 32 * i ? 0 : key[i];
             }
-            if (lane == (k & 31)) {
-                chosen[k >> 5] = e;
-                logit[k >> 5] = of_order(most);
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) key[i] = e == lane + 32 * i ? 0 : key[i];
         }
         float sum = 1.0f;
         if (any) {
@@ -146,17 +211,20 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
 #pragma unroll
             for (int i = 0; i < N; ++i) sums[i] = fmaf(x[i], one, sums[i]);
         }
-        float part[2];
+        float part[2] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) part[i] = chosen[i] >= 0 ? expf(logit[i] - top) : 0.0f;
+        for (int i = 0; i < 2; ++i) {
+            if (i == 1 && K <= 32) break;
+            if (mine[i].expert >= 0 && mine[i].slot < K) part[i] = expf(mine[i].logit - top);
+        }
         if (a.normalize && any) sum = dev::warp_sum(part[0] + part[1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int k = lane + 32 * i;
-            if (k >= K) continue;
-            a.idx[t * K + k] = chosen[i];
-            a.weights[t * K + k] = part[i] / sum;
-            if (chosen[i] >= 0) atomicAdd(counts + chosen[i], 1);     // integers: any order gives the same
+            if (i == 1 && K <= 32) break;
+            if (mine[i].slot >= K) continue;
+            a.idx[t * K + mine[i].slot] = mine[i].expert;
+            a.weights[t * K + mine[i].slot] = part[i] / sum;
+            if (mine[i].expert >= 0) atomicAdd(counts + mine[i].expert, 1);     // integers: any order gives the same
         }
     }
 #pragma unroll
