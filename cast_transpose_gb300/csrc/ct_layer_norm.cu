@@ -142,97 +142,166 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
 }
 
 // ---- many rows -----------------------------------------------------------------
-// A block takes every gridDim.x-th row, a thread two groups of eight columns.
+// A block takes every gridDim.x-th row, a thread PER vectors of eight columns.
 // Rows arrive in a ring of shared-memory stages by asynchronous copies that are
-// issued stages ahead.  With G = 8 a thread copies what it will read itself, so
-// that no barrier is needed for it; with G = 1 a row is copied as the aligned
-// 16-byte blocks that cover it.
-constexpr int kRingPer = 2;                     // groups of eight columns per thread
-constexpr int kRingThreads = 768;               // at most, with 80 registers each
+// issued stages ahead; a thread copies what it will read itself, so that no
+// barrier is needed for it.
+//
+// SHIFT: rows that are not whole vectors, in 16-byte-aligned tensors.  Row r begins
+// s = r H mod 8 columns after an aligned vector, in every tensor alike, and with
+// gridDim.x a multiple of 8 that is the same s for all of a block's rows.  So the
+// vectors are taken where they are aligned, s columns before the row's first: a
+// thread keeps its columns from row to row, and only the vectors at the row's ends
+// are not whole.
+// Threads of an SM, and of a block at most: with 80 registers each, 64 with one
+// vector, 128 in the shifted backward pass with two.
+constexpr int ring_threads(int per, bool more) { return per == 1 ? (more ? 768 : 1024) : more ? 512 : 768; }
 constexpr int kRingStages = 4;                  // at most
 constexpr int kRingSmem = 226 * 1024;           // of an SM's blocks together
+constexpr int kShiftRows = 8;
+constexpr int kRingMaxPerSm = 24;               // blocks
+constexpr int kRingFewRows = 6;                 // per block, up to which a thread takes one vector
 
-__host__ __device__ constexpr uint32_t align16(uint32_t v) { return (v + 15) & ~15u; }
-// Bytes of a tensor's row in a stage.
-template <int G>
-__host__ __device__ constexpr uint32_t slot_bytes(int threads, int hidden, int size) {
-    return G == 8 ? uint32_t(threads) * kRingPer * 8 * size : align16(uint32_t(hidden) * size) + 32;
-}
+// Eight columns from `first` on, of which some may lie outside [0, H).
+template <bool SHIFT>
+struct Vec {
+    int first, H;
+    __device__ __forceinline__ bool any() const { return first < H; }
+    __device__ __forceinline__ bool whole() const { return SHIFT ? first >= 0 && first + 8 <= H : first < H; }
+    __device__ __forceinline__ bool has(int j) const { return SHIFT ? unsigned(first + j) < unsigned(H) : first < H; }
 
-template <typename T, int G>
+    template <typename T>
+    __device__ __forceinline__ void store(T* row, const V8& v) const {
+        float f[8];
+        floats(v, f);
+        if (whole()) {
+            dev::store8(row + first, f);
+        } else if (SHIFT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (has(j)) dev::from_f32(row[first + j], f[j]);
+        }
+    }
+    __device__ __forceinline__ void store_codes(uint8_t* row, const float (&f)[8], float scale, int fmt) const {
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float lo = __fmul_rn(f[2 * j], scale), hi = __fmul_rn(f[2 * j + 1], scale);
+            h[j] = fmt == 0 ? dev::cvt_fp8x2<0>(lo, hi) : dev::cvt_fp8x2<1>(lo, hi);
+        }
+        if (whole()) {
+            *reinterpret_cast<uint2*>(row + first) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        } else if (SHIFT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (has(j)) row[first + j] = static_cast<uint8_t>(h[j >> 1] >> (8 * (j & 1)));
+        }
+    }
+    // A parameter's columns, `none` where there is no parameter.
+    template <typename T>
+    __device__ __forceinline__ V8 param(const void* p, int f32, float offset, float none) const {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = none;
+        if (p) {
+            if constexpr (SHIFT) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (has(j))
+                        f[j] = offset + (f32 ? static_cast<const float*>(p)[first + j]
+                                             : dev::to_f32(static_cast<const T*>(p)[first + j]));
+            } else {
+                load_param<T>(p, f32, 0, offset, dev::Cols<8>(first / 8, H), f);
+            }
+        }
+        return pairs(f);
+    }
+    // 0 outside the row.  Without SHIFT a vector that is outside is so as a whole,
+    // and adds nothing by sum().
+    __device__ __forceinline__ void cut(V8& v) const {
+        if (!SHIFT || whole()) return;
+        float f[8];
+        floats(v, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = has(j) ? f[j] : 0.0f;
+        v = pairs(f);
+    }
+    __device__ __forceinline__ float sum(uint64_t part) const { return SHIFT || any() ? lanes_sum(part) : 0.0f; }
+};
+
+// A tensor's rows in the ring.
+template <typename T, bool SHIFT, int PER>
 struct Staged {
-    const T* base;          // the tensor, null: left out
+    const T* base;          // null: left out
     int64_t rows;
-    int H;
+    int H, shift;
+    static constexpr int kWords = sizeof(T) / 2;        // 16-byte words of a vector
 
+    static __host__ __device__ constexpr uint32_t bytes(int threads) { return threads * PER * 16 * kWords; }
     __device__ __forceinline__ void fetch(uint8_t* stage, int64_t row) const {
         if (!base) return;
         const int tid = threadIdx.x, n = blockDim.x;
-        if constexpr (G == 8) {
 #pragma unroll
-            for (int p = 0; p < kRingPer; ++p) {
-                const dev::Cols<8> c(p * n + tid, H);
-                const uint8_t* from = reinterpret_cast<const uint8_t*>(base + row * H + (c.any() ? c.first : 0));
+        for (int p = 0; p < PER; ++p) {
+            int first = (p * n + tid) * 8 - shift;
+            if (first >= H) first = -shift;             // any place will do
+            const int64_t at = row * H + first;
+            int left = 16 * kWords;                     // bytes that are inside the tensor
+            if (SHIFT) left = static_cast<int>(min(int64_t(16 * kWords), (rows * H - at) * int64_t(sizeof(T))));
+            const uint8_t* from = reinterpret_cast<const uint8_t*>(base + at);
 #pragma unroll
-                for (int w = 0; w < int(sizeof(T) / 2); ++w)
-                    dev::cp_async16(stage + ((p * int(sizeof(T) / 2) + w) * n + tid) * 16, from + 16 * w, 16);
-            }
-        } else {
-            const uintptr_t from = reinterpret_cast<uintptr_t>(base + row * H), first = from & ~uintptr_t(15);
-            const uintptr_t begin = reinterpret_cast<uintptr_t>(base), end = begin + rows * H * sizeof(T);
-            const int blocks = static_cast<int>((from - first + H * sizeof(T) + 15) / 16);
-            for (int i = tid; i < blocks; i += n) {
-                const uintptr_t at = first + 16 * uintptr_t(i);
-                if (at >= begin) {
-                    dev::cp_async16(stage + 16 * i, reinterpret_cast<const void*>(at),
-                                    static_cast<int>(min(uintptr_t(16), end - at)));
-                } else {        // the tensor begins inside these 16 bytes
-                    T* to = reinterpret_cast<T*>(stage + (begin - at));
-                    for (int j = 0; j < int((at + 16 - begin) / sizeof(T)) && j < rows * H; ++j) to[j] = base[j];
-                }
+            for (int w = 0; w < kWords; ++w) {
+                const int inside = SHIFT ? max(0, min(16, left - 16 * w)) : 16;
+                dev::cp_async16(stage + ((p * kWords + w) * n + tid) * 16,
+                                inside > 0 ? from + 16 * w : reinterpret_cast<const uint8_t*>(base), inside);
             }
         }
     }
-    // The thread's group p of the row in a stage.
-    __device__ __forceinline__ V8 get(const uint8_t* stage, int64_t row, int p) const {
-        const int tid = threadIdx.x, n = blockDim.x;
+    __device__ __forceinline__ V8 get(const uint8_t* stage, int p) const {
+        dev::Raw8<T> r;
         float f[8];
-        if constexpr (G == 8) {
-            dev::Raw8<T> r;
 #pragma unroll
-            for (int w = 0; w < int(sizeof(T) / 2); ++w)
-                r.v[w] = *reinterpret_cast<const uint4*>(stage + ((p * int(sizeof(T) / 2) + w) * n + tid) * 16);
-            dev::unpack8(r, f);
-        } else {
-            const dev::Cols<1> c(p * n + tid, H);
-            const T* at = reinterpret_cast<const T*>(stage + (reinterpret_cast<uintptr_t>(base + row * H) & 15));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = dev::to_f32(at[c.has(j) ? c.at(j) : 0]);
-        }
+        for (int w = 0; w < kWords; ++w)
+            r.v[w] = *reinterpret_cast<const uint4*>(stage + ((p * kWords + w) * blockDim.x + threadIdx.x) * 16);
+        dev::unpack8(r, f);
         return pairs(f);
     }
 };
 
-// Columns of the thread's group that lie past the row's end are 0 from here on,
-// where there may be some beside others; a group that is past it as a whole adds
-// nothing by on().
-template <int G>
-__device__ __forceinline__ void cut(const dev::Cols<G>& c, V8& v) {
-    if constexpr (G == 8) return;
-    float f[8];
-    floats(v, f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c.has(j) ? f[j] : 0.0f;
-    v = pairs(f);
-}
+// Drops columns of the thread's vectors of a row.  Vector i begins `shift` columns
+// before group i: it takes the last bits of group i - 1, from the lane before or, as
+// the warp's first, from a lane that made them besides.  The whole warp has to call
+// it.
+template <bool SHIFT, int PER>
+struct RowDrops {
+    const Drops& drops;
+    uint32_t row;
+    int shift;
+    uint32_t before;        // lane p: the bits of the group before the warp's vector p
 
-template <int G>
-__device__ __forceinline__ void drop(const Drops& drops, int64_t row, int item, V8& v) {
-    float f[8];
-    floats(v, f);
-    drops.apply<G>(static_cast<uint32_t>(row), item, f);
-    v = pairs(f);
-}
+    __device__ __forceinline__ RowDrops(const Drops& drops_, int64_t row_, int shift_)
+        : drops(drops_), row(static_cast<uint32_t>(row_)), shift(shift_), before(0) {
+        if (!SHIFT || !shift) return;
+        const int lane = threadIdx.x & 31, p = lane < PER ? lane : 0;
+        before = Drops::bits(drops.words(row, p * blockDim.x + (threadIdx.x - lane) - 1), drops.cut);
+    }
+    __device__ __forceinline__ void apply(int p, V8& v) const {
+        const int item = p * blockDim.x + threadIdx.x;
+        float f[8];
+        floats(v, f);
+        if (!SHIFT || !shift) {
+            drops.apply<8>(row, item, f);
+        } else {
+            const uint32_t own = Drops::bits(drops.words(row, item), drops.cut);
+            const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, own, 1), first = __shfl_sync(0xFFFFFFFFu, before, p);
+            const uint32_t kept = (((threadIdx.x & 31) == 0 ? first : up) | own << 8) >> (8 - shift);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = (kept >> j) & 1 ? f[j] * drops.scale : 0.0f;
+        }
+        v = pairs(f);
+    }
+};
+
 // s / n, rounded to nearest but for rare last bits, given r = 1 / n.
 __device__ __forceinline__ float divided(float s, float n, float r) {
     const float q = s * r;
@@ -252,24 +321,29 @@ __device__ __forceinline__ void wait_stages(int ahead) {
 }
 __device__ __forceinline__ void commit_stage() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+template <bool SHIFT>
+__device__ __forceinline__ int shift_of(int H) {
+    return SHIFT ? static_cast<int>(int64_t(blockIdx.x) * H % kShiftRows) : 0;
+}
+
 // Forward.  The mean and the squares about it need one exchange: a warp leaves the
 // sum of its columns and the squares about its own mean, from which everyone gets
 //   M2 = sum over warps of M2_w + n_w (mean_w - mean)^2
 // without the cancellation of a difference of squares.
-template <typename T, typename R, int G>
-__global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const LayerNormArgs a, int stages) {
+template <typename T, typename R, bool SHIFT, int PER>
+__global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(const LayerNormArgs a, int stages) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 slots[2][32];
     __shared__ unsigned block_max;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, H = a.hidden;
-    auto cols = [&](int p) { return dev::Cols<G>(p * blockDim.x + tid, H); };
+    const int shift = shift_of<SHIFT>(H);
+    auto vec = [&](int p) { return Vec<SHIFT>{int(p * blockDim.x + tid) * 8 - shift, H}; };
     if (tid == 0) block_max = 0;
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    const Staged<R, G> res{static_cast<const R*>(a.res), a.rows, H};
-    const Staged<T, G> u{static_cast<const T*>(a.u), a.rows, H};
-    const uint32_t second = slot_bytes<G>(blockDim.x, H, sizeof(R));
-    const uint32_t stage_bytes = second + (a.u ? slot_bytes<G>(blockDim.x, H, sizeof(T)) : 0);
+    const Staged<R, SHIFT, PER> res{static_cast<const R*>(a.res), a.rows, H, shift};
+    const Staged<T, SHIFT, PER> u{static_cast<const T*>(a.u), a.rows, H, shift};
+    const uint32_t second = res.bytes(blockDim.x), stage_bytes = second + (a.u ? u.bytes(blockDim.x) : 0);
     auto fetch = [&](int64_t row, int to) {
         if (row < a.rows) {
             res.fetch(smem + to * stage_bytes, row);
@@ -280,20 +354,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const Layer
     for (int i = 0; i + 1 < stages; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
     const Drops drops(a.drop);
     const float scale = a.scale ? *a.scale : 0.0f;
-    V8 w[kRingPer], b[kRingPer];
+    V8 w[PER], b[PER];
 #pragma unroll
-    for (int p = 0; p < kRingPer; ++p) {
-        float f[8];
-        load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(p), f);
-        w[p] = pairs(f);
-        load_bias<T>(a.bias, a.param_f32, 0, cols(p), f);
-        b[p] = pairs(f);
+    for (int p = 0; p < PER; ++p) {
+        w[p] = vec(p).template param<T>(a.weight, a.param_f32, a.weight_offset, 1.0f);
+        b[p] = vec(p).template param<T>(a.bias, a.param_f32, 0.0f, 0.0f);
     }
-    // columns of warp `of`, as many as its groups have inside the row
+    // columns of a warp that are inside the row: some, for every warp
     auto columns_of = [&](int of) {
         int n = 0;
 #pragma unroll
-        for (int p = 0; p < kRingPer; ++p) n += max(0, min(256, H - 256 * (p * warps + of)));
+        for (int p = 0; p < PER; ++p) {
+            const int first = 256 * (p * warps + of) - shift;
+            n += max(0, min(first + 256, H) - max(first, 0));
+        }
         return static_cast<float>(n);
     };
     const float own_columns = columns_of(warp), lane_columns = lane < warps ? columns_of(lane) : 1.0f;
@@ -303,34 +377,33 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const Layer
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t at = row * H;
         wait_stages(stages - 2);
-        if (G != 8) __syncthreads();
         const uint8_t* here = smem + stage * stage_bytes;
-        V8 v[kRingPer];
+        V8 v[PER];
         float sum_w = 0.0f, squares_w = 0.0f;
         if (a.u) {
-            V8 x[kRingPer];
+            V8 x[PER];
 #pragma unroll
-            for (int p = 0; p < kRingPer; ++p) x[p] = u.get(here + second, row, p);
+            for (int p = 0; p < PER; ++p) x[p] = u.get(here + second, p);
             if (drops.some) {
+                const RowDrops<SHIFT, PER> of(drops, row, shift);
 #pragma unroll
-                for (int p = 0; p < kRingPer; ++p) drop<G>(drops, row, p * blockDim.x + tid, x[p]);
+                for (int p = 0; p < PER; ++p) of.apply(p, x[p]);
             }
 #pragma unroll
-            for (int p = 0; p < kRingPer; ++p) {
-                v[p] = res.get(here, row, p);
+            for (int p = 0; p < PER; ++p) {
+                v[p] = res.get(here, p);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[p].p[j] = add2(v[p].p[j], x[p].p[j]);
-                store_v8<G>(static_cast<R*>(a.res_out) + at, cols(p), v[p]);
+                vec(p).store(static_cast<R*>(a.res_out) + at, v[p]);
             }
         } else {
 #pragma unroll
-            for (int p = 0; p < kRingPer; ++p) v[p] = res.get(here, row, p);
+            for (int p = 0; p < PER; ++p) v[p] = res.get(here, p);
         }
 #pragma unroll
-        for (int p = 0; p < kRingPer; ++p) {
-            cut<G>(cols(p), v[p]);
-            const float part = lanes_sum(add2(add2(v[p].p[0], v[p].p[1]), add2(v[p].p[2], v[p].p[3])));
-            sum_w += on(cols(p)) ? part : 0.0f;
+        for (int p = 0; p < PER; ++p) {
+            vec(p).cut(v[p]);
+            sum_w += vec(p).sum(add2(add2(v[p].p[0], v[p].p[1]), add2(v[p].p[2], v[p].p[3])));
         }
         // the stage before this one is free
         fetch(row + int64_t(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
@@ -339,15 +412,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const Layer
         const float mean_w = divided(sum_w, own_columns, per_own);
         const uint64_t away = pair(-mean_w, -mean_w);
 #pragma unroll
-        for (int p = 0; p < kRingPer; ++p) {
+        for (int p = 0; p < PER; ++p) {
             V8 d;
             uint64_t part = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) d.p[j] = add2(v[p].p[j], away);
-            cut<G>(cols(p), d);
+            vec(p).cut(d);
 #pragma unroll
             for (int j = 0; j < 4; ++j) part = fma2(d.p[j], d.p[j], part);
-            squares_w += on(cols(p)) ? lanes_sum(part) : 0.0f;
+            squares_w += vec(p).sum(part);
         }
         squares_w = dev::warp_sum(squares_w);
         if (lane == 0) slots[turn][warp] = make_float2(sum_w, squares_w);
@@ -364,20 +437,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const Layer
         }
         const uint64_t mean2 = pair(-mean, -mean), rstd2 = pair(rstd, rstd);
 #pragma unroll
-        for (int p = 0; p < kRingPer; ++p) {
+        for (int p = 0; p < PER; ++p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 v[p].p[j] = fma2(mul2(add2(v[p].p[j], mean2), rstd2), w[p].p[j], b[p].p[j]);
             if (!a.scale) {
-                store_v8<G>(static_cast<T*>(a.y) + at, cols(p), v[p]);
+                vec(p).store(static_cast<T*>(a.y) + at, v[p]);
                 continue;
             }
             float f[8];
             floats(v[p], f);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (cols(p).has(j)) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-            store_fp8<G>(static_cast<uint8_t*>(a.y) + at, cols(p), f, scale, a.fmt);
+                if (vec(p).has(j)) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+            vec(p).store_codes(static_cast<uint8_t*>(a.y) + at, f, scale, a.fmt);
         }
     }
     dev::pdl_launch_dependents();
@@ -394,20 +467,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_kernel(const Layer
 // Backward.  The two sums of a row are exchanged together; the column sums dw = sum
 // dy xh and db = sum dy of the block's rows stay in registers, dy and res_out are
 // read from the stage a second time instead.
-template <typename T, typename R, int G>
-__global__ void __launch_bounds__(kRingThreads, 1)
+template <typename T, typename R, bool SHIFT, int PER>
+__global__ void __launch_bounds__(ring_threads(PER, SHIFT))
     layer_norm_backward_kernel(const LayerNormBackwardArgs a, int stages) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 slots[2][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, H = a.hidden;
-    auto cols = [&](int p) { return dev::Cols<G>(p * blockDim.x + tid, H); };
+    const int shift = shift_of<SHIFT>(H);
+    auto vec = [&](int p) { return Vec<SHIFT>{int(p * blockDim.x + tid) * 8 - shift, H}; };
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    const Staged<R, G> res{static_cast<const R*>(a.res_out), a.rows, H};
-    const Staged<R, G> down{static_cast<const R*>(a.dres_out), a.rows, H};
-    const Staged<T, G> dy{static_cast<const T*>(a.dy), a.rows, H};
-    const uint32_t second = slot_bytes<G>(blockDim.x, H, sizeof(R));
-    const uint32_t third = second + slot_bytes<G>(blockDim.x, H, sizeof(T));
+    const Staged<R, SHIFT, PER> res{static_cast<const R*>(a.res_out), a.rows, H, shift};
+    const Staged<R, SHIFT, PER> down{static_cast<const R*>(a.dres_out), a.rows, H, shift};
+    const Staged<T, SHIFT, PER> dy{static_cast<const T*>(a.dy), a.rows, H, shift};
+    const uint32_t second = res.bytes(blockDim.x), third = second + dy.bytes(blockDim.x);
     const uint32_t stage_bytes = third + (a.dres_out ? second : 0);
     auto fetch = [&](int64_t row, int to) {
         if (row < a.rows) {
@@ -419,13 +492,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     };
     for (int i = 0; i + 1 < stages; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
     const Drops drops(a.drop);
-    V8 w[kRingPer], dw[kRingPer] = {}, db[kRingPer] = {};
+    V8 w[PER], dw[PER] = {}, db[PER] = {};
 #pragma unroll
-    for (int p = 0; p < kRingPer; ++p) {
-        float f[8];
-        load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(p), f);
-        w[p] = pairs(f);
-    }
+    for (int p = 0; p < PER; ++p)
+        w[p] = vec(p).template param<T>(a.weight, a.param_f32, a.weight_offset, 1.0f);
     const float per_column = 1.0f / H;
     float mean = 0.0f, rstd = 0.0f;
     if (blockIdx.x < a.rows) {
@@ -438,18 +508,18 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         const int64_t next = min(row + gridDim.x, a.rows - 1);
         const float next_mean = a.mean[next], next_rstd = a.rstd[next];
         wait_stages(stages - 2);
-        if (G != 8) __syncthreads();
         const uint8_t* here = smem + stage * stage_bytes;
+        // the stage before this one is free
         fetch(row + int64_t(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
         if (++stage == stages) stage = 0;
         const uint64_t mean2 = pair(-mean, -mean), rstd2 = pair(rstd, rstd);
         float one = 0.0f, two = 0.0f;
 #pragma unroll
-        for (int p = 0; p < kRingPer; ++p) {
-            const V8 x = res.get(here, row, p);
-            V8 g = dy.get(here + second, row, p);
+        for (int p = 0; p < PER; ++p) {
+            V8 x = res.get(here, p), g = dy.get(here + second, p);
             uint64_t sum_g = 0, sum_gx = 0;
-            cut<G>(cols(p), g);
+            vec(p).cut(x);
+            vec(p).cut(g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint64_t hat = mul2(add2(x.p[j], mean2), rstd2), gw = mul2(g.p[j], w[p].p[j]);
@@ -458,8 +528,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 sum_g = add2(sum_g, gw);
                 sum_gx = fma2(gw, hat, sum_gx);
             }
-            one += on(cols(p)) ? lanes_sum(sum_g) : 0.0f;
-            two += on(cols(p)) ? lanes_sum(sum_gx) : 0.0f;
+            one += vec(p).sum(sum_g);
+            two += vec(p).sum(sum_gx);
         }
         one = dev::warp_sum(one);
         two = dev::warp_sum(two);
@@ -469,20 +539,21 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         turn ^= 1;
         const float level = -dev::warp_sum(other.x) * per_column, along = -dev::warp_sum(other.y) * per_column;
         const uint64_t level2 = pair(level, level), along2 = pair(along, along);
+        const RowDrops<SHIFT, PER> of(drops, row, drops.some ? shift : 0);
 #pragma unroll
-        for (int p = 0; p < kRingPer; ++p) {
-            const V8 x = res.get(here, row, p), g = dy.get(here + second, row, p);
+        for (int p = 0; p < PER; ++p) {
+            const V8 x = res.get(here, p), g = dy.get(here + second, p);
             V8 d = {};
-            if (a.dres_out) d = down.get(here + third, row, p);
+            if (a.dres_out) d = down.get(here + third, p);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint64_t hat = mul2(add2(x.p[j], mean2), rstd2);
                 d.p[j] = fma2(rstd2, fma2(hat, along2, fma2(g.p[j], w[p].p[j], level2)), d.p[j]);
             }
-            store_v8<G>(static_cast<R*>(a.dres) + at, cols(p), d);
+            vec(p).store(static_cast<R*>(a.dres) + at, d);
             if (!a.du) continue;
-            if (drops.some) drop<G>(drops, row, p * blockDim.x + tid, d);
-            store_v8<G>(static_cast<T*>(a.du) + at, cols(p), d);
+            if (drops.some) of.apply(p, d);
+            vec(p).store(static_cast<T*>(a.du) + at, d);
         }
         mean = next_mean;
         rstd = next_rstd;
@@ -491,32 +562,60 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     if (!a.dweight && !a.dbias) return;
     float* sums = a.workspace + 2 * int64_t(blockIdx.x) * H;
 #pragma unroll
-    for (int p = 0; p < kRingPer; ++p) {
-        store_v8<G>(sums, cols(p), dw[p]);
-        store_v8<G>(sums + H, cols(p), db[p]);
+    for (int p = 0; p < PER; ++p) {
+        float f[2][8];
+        floats(dw[p], f[0]);
+        floats(db[p], f[1]);
+        if (!SHIFT && !vec(p).any()) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float* to = sums + k * H + vec(p).first;
+            if constexpr (!SHIFT) {
+                dev::store8(to, f[k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (vec(p).has(j)) to[j] = f[k][j];
+            }
+        }
     }
 }
 
+// Threads of a block that holds a row of `hidden` columns, PER vectors of eight each.
+int row_threads(int hidden, int per) { return (hidden + 256 * per - 1) / (256 * per) * 32; }
+int row_per(int hidden) { return hidden <= 8192 ? 1 : hidden <= 16384 ? 2 : 4; }
+
+
 // How a launch of many rows is divided.
 struct RingShape {
-    int threads, blocks, stages;        // blocks 0: the rows do not fit
+    int per, threads, blocks, stages;   // blocks 0: not a launch of many rows
     size_t smem;
 };
-// stage_bytes(threads): of one row.
-template <typename F>
-RingShape ring_shape(int64_t rows, int hidden, F&& stage_bytes) {
+// column_bytes: of a column in a stage; more: the kernel needs more registers.
+RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, bool more, int per) {
     RingShape s = {};
-    s.threads = (hidden + 256 * kRingPer - 1) / (256 * kRingPer) * 32;
-    if (s.threads > kRingThreads) return s;
-    const uint32_t bytes = stage_bytes(s.threads);
-    for (int per_sm = std::min(kRingThreads / s.threads, 24); per_sm > 0; --per_sm) {
+    s.per = per;
+    s.threads = row_threads(hidden + (shifted ? 7 : 0), per);
+    const int sm_threads = ring_threads(per, more);
+    if (s.threads > sm_threads) return s;
+    const int bytes = s.threads * per * 8 * column_bytes;
+    for (int per_sm = std::min(sm_threads / s.threads, kRingMaxPerSm); per_sm > 0; --per_sm) {
         s.stages = std::min<int>(kRingStages, (kRingSmem / per_sm - 2048) / bytes);
         if (s.stages < 3 && !(per_sm == 1 && s.stages == 2)) continue;
         s.smem = size_t(s.stages) * bytes;
-        s.blocks = static_cast<int>(std::min<int64_t>(rows, int64_t(sm_count()) * per_sm));
+        int64_t blocks = int64_t(sm_count()) * per_sm;
+        if (shifted) blocks = blocks / kShiftRows * kShiftRows;
+        s.blocks = rows > blocks ? static_cast<int>(blocks) : 0;
         return s;
     }
     return s;
+}
+// Two vectors per thread, or one, which halves a row's way through the block but not
+// what its warps do besides the columns.
+RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, bool more) {
+    const RingShape one = ring_shape(rows, hidden, shifted, column_bytes, more, 1);
+    if (one.blocks > 0 && rows < kRingFewRows * one.blocks) return one;
+    return ring_shape(rows, hidden, shifted, column_bytes, more, 2);
 }
 
 // Launches a kernel of many rows; the first time on a device it is allowed its
@@ -575,8 +674,8 @@ __global__ void __launch_bounds__(32 * kColumnWarps)
 }
 
 // Joins the sums of `parts` blocks or shares, [part][2][H], in a fixed order: a warp
-// takes every so many-th part of 32 columns, eight loads at a time.
-constexpr int kJoinBatch = 8;
+// takes every so many-th part of 32 columns, kJoinBatch loads at a time.
+constexpr int kJoinBatch = 16;
 
 template <typename T>
 __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const LayerNormBackwardArgs a, int parts) {
@@ -603,10 +702,6 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const LayerNormBa
     set_param<T>(out, a.param_f32, col, sum);
 }
 
-// Threads of a block that holds a row of `hidden` columns, PER groups of eight each.
-int row_threads(int hidden, int per) { return (hidden + 256 * per - 1) / (256 * per) * 32; }
-int row_per(int hidden) { return hidden <= 8192 ? 1 : hidden <= 16384 ? 2 : 4; }
-
 int column_shares(int64_t rows, int64_t hidden) {
     const int64_t blocks = (hidden + 31) / 32;
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + 127) / 128, 600 / std::max<int64_t>(blocks, 1))));
@@ -614,26 +709,30 @@ int column_shares(int64_t rows, int64_t hidden) {
 
 // Blocks of a launch of many rows, at most: the workspace has room for them.
 int64_t most_blocks(int64_t rows, int64_t hidden) {
-    const int threads = row_threads(static_cast<int>(hidden), kRingPer);
-    if (threads < 1 || threads > kRingThreads || rows <= sm_count()) return 0;
-    return std::min<int64_t>(rows, int64_t(sm_count()) * std::min(kRingThreads / threads, 24));
+    int most = 0;
+    for (int per = 1; per <= 2; ++per) {
+        const int threads = row_threads(static_cast<int>(hidden), per);
+        if (threads > 0) most = std::max(most, std::min(ring_threads(per, false) / threads, kRingMaxPerSm));
+    }
+    const int64_t blocks = int64_t(sm_count()) * most;
+    return rows > sm_count() ? std::min(rows, blocks) : 0;
 }
 
 }  // namespace
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int res_dtype, cudaStream_t stream) {
-    const bool vec = a.hidden % 8 == 0 && all_aligned(a.u, a.res, a.weight, a.bias, a.res_out, a.y);
+    const bool aligned = all_aligned(a.u, a.res, a.weight, a.bias, a.res_out, a.y), vec = aligned && a.hidden % 8 == 0;
     const int per = row_per(a.hidden);
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const RingShape s = ring_shape(a.rows, a.hidden, [&](int threads) {
-            auto of = [&](int size) { return vec ? slot_bytes<8>(threads, a.hidden, size) : slot_bytes<1>(threads, a.hidden, size); };
-            return of(sizeof(R)) + (a.u ? of(sizeof(T)) : 0);
-        });
-        if (s.blocks > 0 && a.rows > s.blocks)
-            return vec ? launch_ring<layer_norm_kernel<T, R, 8>>(s, a, stream)
-                       : launch_ring<layer_norm_kernel<T, R, 1>>(s, a, stream);
+        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + (a.u ? sizeof(T) : 0), false)
+                                    : RingShape{};
+        if (s.blocks > 0)
+            return s.per == 1 ? (vec ? launch_ring<layer_norm_kernel<T, R, false, 1>>(s, a, stream)
+                                     : launch_ring<layer_norm_kernel<T, R, true, 1>>(s, a, stream))
+                              : (vec ? launch_ring<layer_norm_kernel<T, R, false, 2>>(s, a, stream)
+                                     : launch_ring<layer_norm_kernel<T, R, true, 2>>(s, a, stream));
         auto* kernel = per == 1 ? (vec ? layer_norm_row_kernel<T, R, 8, 1> : layer_norm_row_kernel<T, R, 1, 1>)
                      : per == 2 ? (vec ? layer_norm_row_kernel<T, R, 8, 2> : layer_norm_row_kernel<T, R, 1, 2>)
                                 : (vec ? layer_norm_row_kernel<T, R, 8, 4> : layer_norm_row_kernel<T, R, 1, 4>);
@@ -650,21 +749,22 @@ size_t layer_norm_backward_workspace(int64_t rows, int64_t hidden) {
 
 cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype, int res_dtype,
                                        cudaStream_t stream) {
-    const bool vec = a.hidden % 8 == 0 &&
-                     all_aligned(a.dy, a.dres_out, a.res_out, a.weight, a.dres, a.du);
+    const bool aligned = all_aligned(a.dy, a.dres_out, a.res_out, a.weight, a.dres, a.du);
+    const bool vec = aligned && a.hidden % 8 == 0;
     const int per = row_per(a.hidden);
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const RingShape s = ring_shape(a.rows, a.hidden, [&](int threads) {
-            auto of = [&](int size) { return vec ? slot_bytes<8>(threads, a.hidden, size) : slot_bytes<1>(threads, a.hidden, size); };
-            return of(sizeof(R)) * (a.dres_out ? 2 : 1) + of(sizeof(T));
-        });
+        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) * (a.dres_out ? 2 : 1) + sizeof(T),
+                                                 !vec)
+                                    : RingShape{};
         cudaError_t e = cudaSuccess;
         int parts;
-        if (s.blocks > 0 && a.rows > s.blocks) {
-            e = vec ? launch_ring<layer_norm_backward_kernel<T, R, 8>>(s, a, stream)
-                    : launch_ring<layer_norm_backward_kernel<T, R, 1>>(s, a, stream);
+        if (s.blocks > 0) {
+            e = s.per == 1 ? (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 1>>(s, a, stream)
+                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 1>>(s, a, stream))
+                           : (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 2>>(s, a, stream)
+                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 2>>(s, a, stream));
             if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
             parts = s.blocks;
         } else {

@@ -14,8 +14,8 @@ namespace {
 
 // A warp takes a token; its lane l holds the logits of the experts l, l + 32, ...
 constexpr int kRouterWarps = 8;
-constexpr int kRouterCluster = 8;
-constexpr int kRouterMaxClusters = 48;
+constexpr int kRouterCluster = 4;
+constexpr int kRouterMaxClusters = 108;
 constexpr int kRouterOneCluster = 8;    // tokens per warp up to which one cluster takes them all
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
