@@ -160,7 +160,16 @@ constexpr int kRingStages = 4;                  // at most
 constexpr int kRingSmem = 226 * 1024;           // of an SM's blocks together
 constexpr int kShiftRows = 8;
 constexpr int kRingMaxPerSm = 24;               // blocks
-constexpr int kRingFewRows = 6;                 // per block, up to which a thread takes one vector
+constexpr int kRingFewRows = 6;                 // per block, of kRingShortRow columns at most: one vector per
+constexpr int kRingShortRow = 1024;             // thread in the backward pass
+
+// How a launch of many rows is divided.
+struct RingShape {
+    int per, threads, blocks;           // blocks 0: not a launch of many rows
+    int stages;
+    bool once;                          // backward: dres_out has one place beside the stages
+    size_t smem;
+};
 
 // Eight columns from `first` on, of which some may lie outside [0, H).
 template <bool SHIFT>
@@ -241,19 +250,24 @@ struct Staged {
     __device__ __forceinline__ void fetch(uint8_t* stage, int64_t row) const {
         if (!base) return;
         const int tid = threadIdx.x, n = blockDim.x;
+        // a row's last vector may go on for seven elements after it
+        const bool inside = !SHIFT || (rows - 1 - row) * H >= 7;
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             int first = (p * n + tid) * 8 - shift;
             if (first >= H) first = -shift;             // any place will do
             const int64_t at = row * H + first;
-            int left = 16 * kWords;                     // bytes that are inside the tensor
-            if (SHIFT) left = static_cast<int>(min(int64_t(16 * kWords), (rows * H - at) * int64_t(sizeof(T))));
             const uint8_t* from = reinterpret_cast<const uint8_t*>(base + at);
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
-                const int inside = SHIFT ? max(0, min(16, left - 16 * w)) : 16;
-                dev::cp_async16(stage + ((p * kWords + w) * n + tid) * 16,
-                                inside > 0 ? from + 16 * w : reinterpret_cast<const uint8_t*>(base), inside);
+                uint8_t* to = stage + ((p * kWords + w) * n + tid) * 16;
+                if (inside) {
+                    dev::cp_async16(to, from + 16 * w, 16);
+                } else {                                // no more than what the tensor has
+                    const int64_t left = (rows * H - at) * int64_t(sizeof(T)) - 16 * w;
+                    dev::cp_async16(to, left > 0 ? from + 16 * w : reinterpret_cast<const uint8_t*>(base),
+                                    left > 0 ? static_cast<int>(min(left, int64_t(16))) : 0);
+                }
             }
         }
     }
@@ -313,13 +327,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// Waits for the thread's copies but those of the last `ahead` stages.
-__device__ __forceinline__ void wait_stages(int ahead) {
+// Waits for the thread's copies but those of the last `ahead` commits.
+__device__ __forceinline__ void wait_copies(int ahead) {
     if (ahead == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
     else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (ahead == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (ahead == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else asm volatile("cp.async.wait_group 5;" ::: "memory");
 }
-__device__ __forceinline__ void commit_stage() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 template <bool SHIFT>
 __device__ __forceinline__ int shift_of(int H) {
@@ -349,7 +365,7 @@ __global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(co
             res.fetch(smem + to * stage_bytes, row);
             u.fetch(smem + to * stage_bytes + second, row);
         }
-        commit_stage();
+        commit_copies();
     };
     for (int i = 0; i + 1 < stages; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
     const Drops drops(a.drop);
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(co
     int stage = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t at = row * H;
-        wait_stages(stages - 2);
+        wait_copies(stages - 2);
         const uint8_t* here = smem + stage * stage_bytes;
         V8 v[PER];
         float sum_w = 0.0f, squares_w = 0.0f;
@@ -466,8 +482,10 @@ __global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(co
 
 // Backward.  The two sums of a row are exchanged together; the column sums dw = sum
 // dy xh and db = sum dy of the block's rows stay in registers, dy and res_out are
-// read from the stage a second time instead.
-template <typename T, typename R, bool SHIFT, int PER>
+// read from the stage a second time instead.  dres_out, which only the second half of
+// a row's work needs, may have a single place, into which a thread copies the next
+// row's as soon as it has read this one's (ONCE): where whole stages would be too few.
+template <typename T, typename R, bool SHIFT, int PER, bool ONCE>
 __global__ void __launch_bounds__(ring_threads(PER, SHIFT))
     layer_norm_backward_kernel(const LayerNormBackwardArgs a, int stages) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -481,16 +499,26 @@ __global__ void __launch_bounds__(ring_threads(PER, SHIFT))
     const Staged<R, SHIFT, PER> down{static_cast<const R*>(a.dres_out), a.rows, H, shift};
     const Staged<T, SHIFT, PER> dy{static_cast<const T*>(a.dy), a.rows, H, shift};
     const uint32_t second = res.bytes(blockDim.x), third = second + dy.bytes(blockDim.x);
-    const uint32_t stage_bytes = third + (a.dres_out ? second : 0);
+    const uint32_t stage_bytes = third + (a.dres_out && !ONCE ? second : 0);
     auto fetch = [&](int64_t row, int to) {
         if (row < a.rows) {
             res.fetch(smem + to * stage_bytes, row);
             dy.fetch(smem + to * stage_bytes + second, row);
-            down.fetch(smem + to * stage_bytes + third, row);
+            if (!ONCE) down.fetch(smem + to * stage_bytes + third, row);
         }
-        commit_stage();
+        commit_copies();
     };
-    for (int i = 0; i + 1 < stages; ++i) fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
+    auto fetch_down = [&](int64_t row) {
+        if (!ONCE) return;
+        if (row < a.rows) down.fetch(smem + stages * stage_bytes, row);
+        commit_copies();
+    };
+    // the commits are those of the loop: a stage's and, with dres_out apart, its own
+    for (int i = 0; i + 1 < stages; ++i) {
+        fetch(blockIdx.x + int64_t(i) * gridDim.x, i);
+        if (ONCE && i + 2 < stages) commit_copies();
+    }
+    fetch_down(blockIdx.x);
     const Drops drops(a.drop);
     V8 w[PER], dw[PER] = {}, db[PER] = {};
 #pragma unroll
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(ring_threads(PER, SHIFT))
         const int64_t at = row * H;
         const int64_t next = min(row + gridDim.x, a.rows - 1);
         const float next_mean = a.mean[next], next_rstd = a.rstd[next];
-        wait_stages(stages - 2);
+        wait_copies(ONCE ? 2 * stages - 3 : stages - 2);
         const uint8_t* here = smem + stage * stage_bytes;
         // the stage before this one is free
         fetch(row + int64_t(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
@@ -539,12 +567,14 @@ __global__ void __launch_bounds__(ring_threads(PER, SHIFT))
         turn ^= 1;
         const float level = -dev::warp_sum(other.x) * per_column, along = -dev::warp_sum(other.y) * per_column;
         const uint64_t level2 = pair(level, level), along2 = pair(along, along);
+        if (ONCE) wait_copies(1);
+        const uint8_t* down_here = ONCE ? smem + stages * stage_bytes : here + third;
         const RowDrops<SHIFT, PER> of(drops, row, drops.some ? shift : 0);
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const V8 x = res.get(here, p), g = dy.get(here + second, p);
             V8 d = {};
-            if (a.dres_out) d = down.get(here + third, p);
+            if (a.dres_out) d = down.get(down_here, p);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint64_t hat = mul2(add2(x.p[j], mean2), rstd2);
@@ -555,6 +585,7 @@ __global__ void __launch_bounds__(ring_threads(PER, SHIFT))
             if (drops.some) of.apply(p, d);
             vec(p).store(static_cast<T*>(a.du) + at, d);
         }
+        fetch_down(row + gridDim.x);
         mean = next_mean;
         rstd = next_rstd;
     }
@@ -586,36 +617,30 @@ int row_threads(int hidden, int per) { return (hidden + 256 * per - 1) / (256 * 
 int row_per(int hidden) { return hidden <= 8192 ? 1 : hidden <= 16384 ? 2 : 4; }
 
 
-// How a launch of many rows is divided.
-struct RingShape {
-    int per, threads, blocks, stages;   // blocks 0: not a launch of many rows
-    size_t smem;
-};
-// column_bytes: of a column in a stage; more: the kernel needs more registers.
-RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, bool more, int per) {
+// column_bytes: of a column in a stage, extra_bytes: of what may be once beside the
+// stages instead; more: the kernel needs more registers.
+RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, int extra_bytes, bool more, int per) {
     RingShape s = {};
     s.per = per;
     s.threads = row_threads(hidden + (shifted ? 7 : 0), per);
-    const int sm_threads = ring_threads(per, more);
+    const int sm_threads = ring_threads(per, more), columns = s.threads * per * 8;
     if (s.threads > sm_threads) return s;
-    const int bytes = s.threads * per * 8 * column_bytes;
     for (int per_sm = std::min(sm_threads / s.threads, kRingMaxPerSm); per_sm > 0; --per_sm) {
-        s.stages = std::min<int>(kRingStages, (kRingSmem / per_sm - 2048) / bytes);
-        if (s.stages < 3 && !(per_sm == 1 && s.stages == 2)) continue;
-        s.smem = size_t(s.stages) * bytes;
+        const int room = kRingSmem / per_sm - 2048;
+        s.once = false;
+        s.stages = std::min(kRingStages, room / (columns * (column_bytes + extra_bytes)));
+        if (s.stages < 3 && extra_bytes && !shifted && per == 2) {
+            s.once = true;
+            s.stages = std::min(kRingStages, (room - columns * extra_bytes) / (columns * column_bytes));
+        }
+        if (s.stages < (s.once || per_sm == 1 ? 2 : 3)) continue;
+        s.smem = size_t(columns) * (s.stages * (column_bytes + (s.once ? 0 : extra_bytes)) + (s.once ? extra_bytes : 0));
         int64_t blocks = int64_t(sm_count()) * per_sm;
         if (shifted) blocks = blocks / kShiftRows * kShiftRows;
         s.blocks = rows > blocks ? static_cast<int>(blocks) : 0;
         return s;
     }
     return s;
-}
-// Two vectors per thread, or one, which halves a row's way through the block but not
-// what its warps do besides the columns.
-RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, bool more) {
-    const RingShape one = ring_shape(rows, hidden, shifted, column_bytes, more, 1);
-    if (one.blocks > 0 && rows < kRingFewRows * one.blocks) return one;
-    return ring_shape(rows, hidden, shifted, column_bytes, more, 2);
 }
 
 // Launches a kernel of many rows; the first time on a device it is allowed its
@@ -726,13 +751,11 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int res_dtype, 
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + (a.u ? sizeof(T) : 0), false)
+        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + (a.u ? sizeof(T) : 0), 0, false, 2)
                                     : RingShape{};
         if (s.blocks > 0)
-            return s.per == 1 ? (vec ? launch_ring<layer_norm_kernel<T, R, false, 1>>(s, a, stream)
-                                     : launch_ring<layer_norm_kernel<T, R, true, 1>>(s, a, stream))
-                              : (vec ? launch_ring<layer_norm_kernel<T, R, false, 2>>(s, a, stream)
-                                     : launch_ring<layer_norm_kernel<T, R, true, 2>>(s, a, stream));
+            return vec ? launch_ring<layer_norm_kernel<T, R, false, 2>>(s, a, stream)
+                       : launch_ring<layer_norm_kernel<T, R, true, 2>>(s, a, stream);
         auto* kernel = per == 1 ? (vec ? layer_norm_row_kernel<T, R, 8, 1> : layer_norm_row_kernel<T, R, 1, 1>)
                      : per == 2 ? (vec ? layer_norm_row_kernel<T, R, 8, 2> : layer_norm_row_kernel<T, R, 1, 2>)
                                 : (vec ? layer_norm_row_kernel<T, R, 8, 4> : layer_norm_row_kernel<T, R, 1, 4>);
@@ -755,16 +778,26 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) * (a.dres_out ? 2 : 1) + sizeof(T),
-                                                 !vec)
-                                    : RingShape{};
+        // With one vector per thread a row's way through its block is shorter, but its
+        // warps do more besides the columns: short runs of short rows take it
+        // (4099x777 24.1 us against 26.4, 2048x1024 13.7 against 15.1; but 16384x777
+        // 58.6 against 54.8, 3000x2048 21.1 against 20.8).
+        RingShape s = {};
+        if (aligned) {
+            auto of = [&](int per) {
+                return ring_shape(a.rows, a.hidden, !vec, sizeof(R) + sizeof(T), a.dres_out ? sizeof(R) : 0, !vec, per);
+            };
+            if (a.hidden <= kRingShortRow) s = of(1);
+            if (a.rows >= int64_t(kRingFewRows) * s.blocks) s = of(2);
+        }
         cudaError_t e = cudaSuccess;
         int parts;
         if (s.blocks > 0) {
-            e = s.per == 1 ? (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 1>>(s, a, stream)
-                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 1>>(s, a, stream))
-                           : (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 2>>(s, a, stream)
-                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 2>>(s, a, stream));
+            e = s.once ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, true>>(s, a, stream)
+              : s.per == 1 ? (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 1, false>>(s, a, stream)
+                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 1, false>>(s, a, stream))
+                           : (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, false>>(s, a, stream)
+                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 2, false>>(s, a, stream));
             if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
             parts = s.blocks;
         } else {
