@@ -153,20 +153,26 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
 // vectors are taken where they are aligned, s columns before the row's first: a
 // thread keeps its columns from row to row, and only the vectors at the row's ends
 // are not whole.
-// Threads of an SM, and of a block at most: with 80 registers each, 64 with one
-// vector, 128 in the shifted backward pass with two.
-constexpr int ring_threads(int per, bool more) { return per == 1 ? (more ? 768 : 1024) : more ? 512 : 768; }
+// Threads of an SM, and of a block at most: with 80 registers each, or 128 in the
+// shifted backward pass.
+constexpr int ring_threads(bool more) { return more ? 512 : 768; }
+// Rows of whole vectors that fit a warp (ONE) need no exchange between warps: up to
+// 512 columns with two vectors per thread and, where the exchange is most of the
+// rest, in the backward pass, 1024 with four.  Blocks of an SM, by their registers
+// (more blocks with fewer are slower: backward 16384x1024 37.8 us with 8, 50.5 with
+// 12; two warps per row 45.7).
+constexpr int one_blocks(int per, bool sums) { return per == 4 ? 8 : sums ? 12 : 16; }
+constexpr int kOneRows = 4;             // of a block with four vectors, at least: 2048x1024 17.0 us, else 15.1
+constexpr int ring_block(bool one, bool more) { return one ? 32 : ring_threads(more); }
 constexpr int kRingStages = 4;                  // at most
 constexpr int kRingSmem = 226 * 1024;           // of an SM's blocks together
 constexpr int kShiftRows = 8;
-constexpr int kRingMaxPerSm = 24;               // blocks
-constexpr int kRingFewRows = 6;                 // per block, of kRingShortRow columns at most: one vector per
-constexpr int kRingShortRow = 1024;             // thread in the backward pass
 
 // How a launch of many rows is divided.
 struct RingShape {
     int per, threads, blocks;           // blocks 0: not a launch of many rows
     int stages;
+    bool one;                           // a warp per row
     bool once;                          // backward: dres_out has one place beside the stages
     size_t smem;
 };
@@ -346,8 +352,9 @@ __device__ __forceinline__ int shift_of(int H) {
 // sum of its columns and the squares about its own mean, from which everyone gets
 //   M2 = sum over warps of M2_w + n_w (mean_w - mean)^2
 // without the cancellation of a difference of squares.
-template <typename T, typename R, bool SHIFT, int PER>
-__global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(const LayerNormArgs a, int stages) {
+template <typename T, typename R, bool SHIFT, int PER, bool ONE>
+__global__ void __launch_bounds__(ring_block(ONE, false), ONE ? one_blocks(PER, false) : 1)
+    layer_norm_kernel(const LayerNormArgs a, int stages) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 slots[2][32];
     __shared__ unsigned block_max;
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(co
         fetch(row + int64_t(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
         if (++stage == stages) stage = 0;
         sum_w = dev::warp_sum(sum_w);
-        const float mean_w = divided(sum_w, own_columns, per_own);
+        const float mean_w = ONE ? sum_w / H : divided(sum_w, own_columns, per_own);
         const uint64_t away = pair(-mean_w, -mean_w);
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
@@ -439,13 +446,16 @@ __global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(co
             squares_w += vec(p).sum(part);
         }
         squares_w = dev::warp_sum(squares_w);
-        if (lane == 0) slots[turn][warp] = make_float2(sum_w, squares_w);
-        __syncthreads();
-        const float2 other = lane < warps ? slots[turn][lane] : make_float2(0.0f, 0.0f);
-        turn ^= 1;
-        const float mean = dev::warp_sum(other.x) / H;
-        const float apart = lane < warps ? divided(other.x, lane_columns, per_lane) - mean : 0.0f;
-        const float squares = dev::warp_sum(fmaf(lane_columns * apart, apart, other.y));
+        float mean = mean_w, squares = squares_w;
+        if (!ONE) {
+            if (lane == 0) slots[turn][warp] = make_float2(sum_w, squares_w);
+            __syncthreads();
+            const float2 other = lane < warps ? slots[turn][lane] : make_float2(0.0f, 0.0f);
+            turn ^= 1;
+            mean = dev::warp_sum(other.x) / H;
+            const float apart = lane < warps ? divided(other.x, lane_columns, per_lane) - mean : 0.0f;
+            squares = dev::warp_sum(fmaf(lane_columns * apart, apart, other.y));
+        }
         const float rstd = rsqrtf(fmaf(squares, per_column, a.eps));
         if (tid == 0) {
             if (a.mean) a.mean[row] = mean;
@@ -485,8 +495,8 @@ __global__ void __launch_bounds__(ring_threads(PER, false)) layer_norm_kernel(co
 // read from the stage a second time instead.  dres_out, which only the second half of
 // a row's work needs, may have a single place, into which a thread copies the next
 // row's as soon as it has read this one's (ONCE): where whole stages would be too few.
-template <typename T, typename R, bool SHIFT, int PER, bool ONCE>
-__global__ void __launch_bounds__(ring_threads(PER, SHIFT))
+template <typename T, typename R, bool SHIFT, int PER, bool ONE, bool ONCE>
+__global__ void __launch_bounds__(ring_block(ONE, SHIFT), ONE ? one_blocks(PER, true) : 1)
     layer_norm_backward_kernel(const LayerNormBackwardArgs a, int stages) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 slots[2][32];
@@ -561,11 +571,15 @@ __global__ void __launch_bounds__(ring_threads(PER, SHIFT))
         }
         one = dev::warp_sum(one);
         two = dev::warp_sum(two);
-        if (lane == 0) slots[turn][warp] = make_float2(one, two);
-        __syncthreads();
-        const float2 other = lane < warps ? slots[turn][lane] : make_float2(0.0f, 0.0f);
-        turn ^= 1;
-        const float level = -dev::warp_sum(other.x) * per_column, along = -dev::warp_sum(other.y) * per_column;
+        if (!ONE) {
+            if (lane == 0) slots[turn][warp] = make_float2(one, two);
+            __syncthreads();
+            const float2 other = lane < warps ? slots[turn][lane] : make_float2(0.0f, 0.0f);
+            turn ^= 1;
+            one = dev::warp_sum(other.x);
+            two = dev::warp_sum(other.y);
+        }
+        const float level = -one * per_column, along = -two * per_column;
         const uint64_t level2 = pair(level, level), along2 = pair(along, along);
         if (ONCE) wait_copies(1);
         const uint8_t* down_here = ONCE ? smem + stages * stage_bytes : here + third;
@@ -618,22 +632,26 @@ int row_per(int hidden) { return hidden <= 8192 ? 1 : hidden <= 16384 ? 2 : 4; }
 
 
 // column_bytes: of a column in a stage, extra_bytes: of what may be once beside the
-// stages instead; more: the kernel needs more registers.
-RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, int extra_bytes, bool more, int per) {
+// stages instead; sums: the kernel keeps column sums.
+RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, int extra_bytes, bool sums) {
     RingShape s = {};
-    s.per = per;
-    s.threads = row_threads(hidden + (shifted ? 7 : 0), per);
-    const int sm_threads = ring_threads(per, more), columns = s.threads * per * 8;
+    s.one = !shifted && (hidden <= 512 || (sums && hidden <= 1024 &&
+                                           rows >= int64_t(kOneRows) * sm_count() * one_blocks(4, true)));
+    s.per = s.one && hidden > 512 ? 4 : 2;
+    s.threads = row_threads(hidden + (shifted ? kShiftRows - 1 : 0), s.per);
+    const int sm_threads = s.one ? 32 * one_blocks(s.per, sums) : ring_threads(sums && shifted);
+    const int columns = s.threads * s.per * 8;
     if (s.threads > sm_threads) return s;
-    for (int per_sm = std::min(sm_threads / s.threads, kRingMaxPerSm); per_sm > 0; --per_sm) {
+    for (int per_sm = sm_threads / s.threads; per_sm > 0; --per_sm) {
         const int room = kRingSmem / per_sm - 2048;
         s.once = false;
         s.stages = std::min(kRingStages, room / (columns * (column_bytes + extra_bytes)));
-        if (s.stages < 3 && extra_bytes && !shifted && per == 2) {
+        if (s.stages < 3 && extra_bytes && !shifted && !s.one) {
             s.once = true;
             s.stages = std::min(kRingStages, (room - columns * extra_bytes) / (columns * column_bytes));
         }
-        if (s.stages < (s.once || per_sm == 1 ? 2 : 3)) continue;
+        // a row ahead is enough where many blocks have one each
+        if (s.stages < (s.once || s.one || per_sm == 1 ? 2 : 3)) continue;
         s.smem = size_t(columns) * (s.stages * (column_bytes + (s.once ? 0 : extra_bytes)) + (s.once ? extra_bytes : 0));
         int64_t blocks = int64_t(sm_count()) * per_sm;
         if (shifted) blocks = blocks / kShiftRows * kShiftRows;
@@ -732,15 +750,10 @@ int column_shares(int64_t rows, int64_t hidden) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + 127) / 128, 600 / std::max<int64_t>(blocks, 1))));
 }
 
-// Blocks of a launch of many rows, at most: the workspace has room for them.
+// Blocks of a backward launch of many rows, at most: the workspace has room for them.
 int64_t most_blocks(int64_t rows, int64_t hidden) {
-    int most = 0;
-    for (int per = 1; per <= 2; ++per) {
-        const int threads = row_threads(static_cast<int>(hidden), per);
-        if (threads > 0) most = std::max(most, std::min(ring_threads(per, false) / threads, kRingMaxPerSm));
-    }
-    const int64_t blocks = int64_t(sm_count()) * most;
-    return rows > sm_count() ? std::min(rows, blocks) : 0;
+    const int of_rings = ring_threads(false) / row_threads(static_cast<int>(std::max<int64_t>(hidden, 1)), 2);
+    return rows > sm_count() ? std::min(rows, int64_t(sm_count()) * of_rings) : 0;
 }
 
 }  // namespace
@@ -751,11 +764,12 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int res_dtype, 
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + (a.u ? sizeof(T) : 0), 0, false, 2)
+        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + (a.u ? sizeof(T) : 0), 0, false)
                                     : RingShape{};
         if (s.blocks > 0)
-            return vec ? launch_ring<layer_norm_kernel<T, R, false, 2>>(s, a, stream)
-                       : launch_ring<layer_norm_kernel<T, R, true, 2>>(s, a, stream);
+            return s.one ? launch_ring<layer_norm_kernel<T, R, false, 2, true>>(s, a, stream)
+                 : vec   ? launch_ring<layer_norm_kernel<T, R, false, 2, false>>(s, a, stream)
+                         : launch_ring<layer_norm_kernel<T, R, true, 2, false>>(s, a, stream);
         auto* kernel = per == 1 ? (vec ? layer_norm_row_kernel<T, R, 8, 1> : layer_norm_row_kernel<T, R, 1, 1>)
                      : per == 2 ? (vec ? layer_norm_row_kernel<T, R, 8, 2> : layer_norm_row_kernel<T, R, 1, 2>)
                                 : (vec ? layer_norm_row_kernel<T, R, 8, 4> : layer_norm_row_kernel<T, R, 1, 4>);
@@ -778,26 +792,17 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        // With one vector per thread a row's way through its block is shorter, but its
-        // warps do more besides the columns: short runs of short rows take it
-        // (4099x777 24.1 us against 26.4, 2048x1024 13.7 against 15.1; but 16384x777
-        // 58.6 against 54.8, 3000x2048 21.1 against 20.8).
-        RingShape s = {};
-        if (aligned) {
-            auto of = [&](int per) {
-                return ring_shape(a.rows, a.hidden, !vec, sizeof(R) + sizeof(T), a.dres_out ? sizeof(R) : 0, !vec, per);
-            };
-            if (a.hidden <= kRingShortRow) s = of(1);
-            if (a.rows >= int64_t(kRingFewRows) * s.blocks) s = of(2);
-        }
+        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + sizeof(T),
+                                                 a.dres_out ? sizeof(R) : 0, true)
+                                    : RingShape{};
         cudaError_t e = cudaSuccess;
         int parts;
         if (s.blocks > 0) {
-            e = s.once ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, true>>(s, a, stream)
-              : s.per == 1 ? (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 1, false>>(s, a, stream)
-                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 1, false>>(s, a, stream))
-                           : (vec ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, false>>(s, a, stream)
-                                  : launch_ring<layer_norm_backward_kernel<T, R, true, 2, false>>(s, a, stream));
+            e = s.once ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, false, true>>(s, a, stream)
+              : s.one  ? (s.per == 2 ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, true, false>>(s, a, stream)
+                                     : launch_ring<layer_norm_backward_kernel<T, R, false, 4, true, false>>(s, a, stream))
+              : vec    ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, false, false>>(s, a, stream)
+                       : launch_ring<layer_norm_backward_kernel<T, R, true, 2, false, false>>(s, a, stream);
             if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
             parts = s.blocks;
         } else {

@@ -2,7 +2,8 @@
 library's operators:
 
     junction   res, h = block_norm(branch of the block before, res)
-    router     probabilities of h @ w_router, the best K of E experts per token
+    router     moe_router on h @ w_router: the best K of E experts per token, their
+               weights (a softmax over them), the balance and z losses
     sort       moe_sort
     dispatch   fp8_moe_dispatch: h in expert order, E4M3, with its transpose
     experts    y_e = x_e @ w_e^T (the weights by fp8_cast_transpose)
@@ -12,9 +13,9 @@ library's operators:
 and back, the output gradient of the experts being E5M2 (fp8_moe_dispatch with
 the router's weights), then the delayed-scaling update of every FP8 tensor.
 
-The experts' products and the router are plain torch products here, on the FP8
-values: they stand for the FP8 matrix products of a real block.  Shapes are
-static (the sorted buffers hold any routing); only the loop over the experts
+The experts' products and the router's are plain torch products here, the first on
+the FP8 values: they stand for the FP8 matrix products of a real block.  Shapes
+are static (the sorted buffers hold any routing); only the loop over the experts
 reads their offsets on the host.
 
     python examples/moe_block.py [--steps N]
@@ -60,7 +61,7 @@ def values(q, scale_inv, fmt):
 
 
 class MoeBlock:
-    def __init__(self, hidden, experts, topk, tokens, seed=0):
+    def __init__(self, hidden, experts, topk, tokens, seed=0, balance=0.0, z=0.0):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def normal(*shape, std):
@@ -83,6 +84,11 @@ class MoeBlock:
         self.wq_t = torch.empty(experts, hidden, hidden, **u8)
         size = ct.block_norm_backward_workspace_size(tokens, hidden)
         self.workspace = torch.empty(size, **u8)
+        # the losses' weights in the training loss, whose gradient is 1
+        self.losses = {"balance": balance, "z": z}
+        self.dloss = torch.ones(1, device="cuda")
+        size = ct.moe_router_workspace_size(tokens, topk, experts)
+        self.router_workspace = torch.empty(size, **u8)
 
     # -- forward ---------------------------------------------------------------
     def junction(self, i, u, res):
@@ -96,16 +102,23 @@ class MoeBlock:
         return kept, y
 
     def route(self, h):
-        logits = (h @ self.router).float()
-        best, idx = logits.topk(self.topk, dim=1)
-        return torch.softmax(best, 1), idx
+        """The router's choices [tokens, topk] and their weights, and what its
+        backward pass needs."""
+        slots, i32 = (self.tokens, self.topk), dict(dtype=torch.int32, device="cuda")
+        kept = {"logits": (h @ self.router).float(), "expert_idx": torch.empty(slots, **i32),
+                "counts": torch.empty(self.experts + 1, **i32)}
+        weights, loss = torch.empty(slots, device="cuda"), torch.empty(1, device="cuda")
+        ct.moe_router(weights=weights, loss=loss, workspace=self.router_workspace, **kept,
+                      **self.losses)
+        return kept, weights, loss
 
     def forward(self, u, res):
         """u, res [tokens, hidden] -> (res_out, out) and what backward needs."""
         m, s = self.forward_meta, {}
         s["first"], s["h"] = self.junction(0, u, res)
-        s["weights"], s["idx"] = self.route(s["h"])
-        ct.moe_sort(s["idx"], self.plan)
+        s["routed"], s["weights"], s["loss"] = self.route(s["h"])
+        s["idx"] = s["routed"]["expert_idx"].long()
+        ct.moe_sort(s["routed"]["expert_idx"], self.plan)
         ct.fp8_moe_dispatch(s["h"], self.plan, *m.of("x"), self.x, self.x_t, m.fmt)
         for e in range(self.experts):
             ct.fp8_cast_transpose(self.w[e], *m.of(f"w{e}"), self.wq[e], self.wq_t[e], m.fmt)
@@ -152,10 +165,9 @@ class MoeBlock:
             grads["w"][e] = (d_t @ x_t.t()).float() * (sd * sx)
         dh = torch.empty_like(s["h"])
         ct.moe_dispatch_backward(dx, self.plan, dh)
-        # through the softmax over the chosen logits, to the router and h
-        p = s["weights"]
-        dlogits = torch.zeros(self.tokens, self.experts, device="cuda")
-        dlogits.scatter_(1, s["idx"], p * (dweights - (p * dweights).sum(1, keepdim=True)))
+        # through the router's weights and losses, to the router and h
+        dlogits = torch.empty_like(s["routed"]["logits"])
+        ct.moe_router_backward(dweights, self.dloss, dlogits=dlogits, **s["routed"], **self.losses)
         dlogits = dlogits.to(BF16)
         grads["router"] = s["h"].t() @ dlogits
         dh += dlogits @ self.router.t()
@@ -171,7 +183,7 @@ def main():
     p.add_argument("--hidden", type=int, default=512)
     p.add_argument("--tokens", type=int, default=1000)
     args = p.parse_args()
-    block = MoeBlock(args.hidden, experts=8, topk=2, tokens=args.tokens)
+    block = MoeBlock(args.hidden, experts=8, topk=2, tokens=args.tokens, balance=1e-2, z=1e-3)
     g = torch.Generator(device="cuda").manual_seed(1)
     u, res, d1, d2 = (torch.randn(args.tokens, args.hidden, generator=g, device="cuda").to(BF16)
                       for _ in range(4))
@@ -179,7 +191,8 @@ def main():
         res_out, out, saved = block.forward(u, res)
         du, dres, grads = block.backward(saved, 1e-3 * d1, 1e-3 * d2)
         print(f"step {step}: |out| {out.float().norm():.3f}  |du| {du.float().norm():.5f}  "
-              f"|dw| {grads['w'].float().norm():.4f}  scale of x {block.forward_meta.scale[0]:.3f}, "
+              f"|dw| {grads['w'].float().norm():.4f}  router loss {saved['loss'].item():.4f}  "
+              f"scale of x {block.forward_meta.scale[0]:.3f}, "
               f"of dy {block.backward_meta.scale[0]:.3e}")
 
 
