@@ -39,22 +39,39 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_row_kernel(const La
     if (tid == 0) block_max = 0;
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    float v[PER][8];
+    // with PER = 1 everything is on its way before the first of it is used
+    constexpr bool AHEAD = PER == 1;
+    dev::RawCols<G, R> res[PER];
+    dev::RawCols<G, T> u[PER];
+    float v[PER][8], w[8], b[8];
     float sum = 0.0f;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        dev::load_cols<G>(static_cast<const R*>(a.res) + at, cols(p), v[p]);
-        if (a.u) {
-            float u[8];
-            dev::load_cols<G>(static_cast<const T*>(a.u) + at, cols(p), u);
-            const Drops drops(a.drop);
-            if (drops.some) drops.apply<G>(static_cast<uint32_t>(row), p * blockDim.x + tid, u);
+        res[p].load(static_cast<const R*>(a.res) + at, cols(p));
+        if (a.u) u[p].load(static_cast<const T*>(a.u) + at, cols(p));
+    }
+    if (AHEAD) {
+        load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(0), w);
+        load_bias<T>(a.bias, a.param_f32, 0, cols(0), b);
+    }
+    const Drops drops(a.drop);
+    const float scale = a.scale ? *a.scale : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[p][j] += u[j];
+    for (int p = 0; p < PER; ++p) {
+        res[p].get(v[p]);
+        if (a.u) {
+            float f[8];
+            u[p].get(f);
+            if (drops.some) drops.apply<G>(static_cast<uint32_t>(row), p * blockDim.x + tid, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[p][j] += f[j];
             dev::store_cols<G>(static_cast<R*>(a.res_out) + at, cols(p), v[p]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += v[p][j];       // 0 past the row's end
+        for (int j = 0; j < 8; ++j) {
+            v[p][j] = cols(p).has(j) ? v[p][j] : 0.0f;
+            sum += v[p][j];
+        }
     }
     const float mean = block_sums(sum, 0.0f, slots).x / H;
     float squares = 0.0f;
@@ -70,13 +87,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_row_kernel(const La
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
-    const float scale = a.scale ? *a.scale : 0.0f;
     unsigned most = 0;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        float w[8], b[8];
-        load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(p), w);
-        load_bias<T>(a.bias, a.param_f32, 0, cols(p), b);
+        if (!AHEAD) {
+            load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(p), w);
+            load_bias<T>(a.bias, a.param_f32, 0, cols(p), b);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             v[p][j] = fmaf(v[p][j] * rstd, w[j], b[j]);
@@ -109,18 +126,28 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     const float mean = a.mean[row], rstd = a.rstd[row];
+    constexpr bool AHEAD = PER == 1;
+    dev::RawCols<G, T> dy[PER];
+    dev::RawCols<G, R> res[PER], down[AHEAD ? PER : 1];
     float g[PER][8], x[PER][8];
     float sum_g = 0.0f, sum_gx = 0.0f;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        float w[8];
-        dev::load_cols<G>(static_cast<const T*>(a.dy) + at, cols(p), g[p]);
-        dev::load_cols<G>(static_cast<const R*>(a.res_out) + at, cols(p), x[p]);
-        load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(p), w);
+        dy[p].load(static_cast<const T*>(a.dy) + at, cols(p));
+        res[p].load(static_cast<const R*>(a.res_out) + at, cols(p));
+        if (AHEAD && a.dres_out) down[p].load(static_cast<const R*>(a.dres_out) + at, cols(p));
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {                      // dy is 0 past the row's end
-            x[p][j] = (x[p][j] - mean) * rstd;
-            g[p][j] *= w[j];
+    for (int p = 0; p < PER; ++p) {
+        float w[8];
+        load_param<T>(a.weight, a.param_f32, 0, a.weight_offset, cols(p), w);
+        dy[p].get(g[p]);
+        res[p].get(x[p]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool has = cols(p).has(j);
+            x[p][j] = has ? (x[p][j] - mean) * rstd : 0.0f;
+            g[p][j] = has ? g[p][j] * w[j] : 0.0f;
             sum_g += g[p][j];
             sum_gx = fmaf(g[p][j], x[p][j], sum_gx);
         }
@@ -131,7 +158,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
         float d[8] = {};
-        if (a.dres_out) dev::load_cols<G>(static_cast<const R*>(a.dres_out) + at, cols(p), d);
+        if (a.dres_out) {
+            if (!AHEAD) down[0].load(static_cast<const R*>(a.dres_out) + at, cols(p));
+            down[AHEAD ? p : 0].get(d);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, g[p][j] - level - x[p][j] * along, d[j]);
         dev::store_cols<G>(static_cast<R*>(a.dres) + at, cols(p), d);
