@@ -37,7 +37,7 @@ def embedding_backward_workspace_size(tokens: int, vocab: int, hidden: int) -> i
     return int(lib().embedding_backward_workspace_size(tokens, vocab, hidden))
 
 
-def embedding_backward(idx, dout, dtable, workspace, scale=1.0, accumulate=False, noop_flag=None,
+def embedding_backward(idx, dout, dtable, workspace=None, scale=1.0, accumulate=False, noop_flag=None,
                        stream=None) -> None:
     """dout [T, hidden] -> dtable [V, hidden] of its type or fp32: scale * the
     sum of the rows of each id; accumulate: added to what dtable holds.

@@ -770,7 +770,7 @@ int embedding(const void* idx, int index_bytes, int64_t tokens, const void* tabl
               int64_t hidden, int dtype, float scale, void* out, const float* noop_flag,
               void* stream);
 
-/* Bytes of workspace embedding_backward needs (16-byte aligned). */
+/* Bytes of workspace embedding_backward needs (16-byte aligned; 0 for few tokens). */
 size_t embedding_backward_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden);
 
 /*

@@ -102,7 +102,7 @@ def test_gradient(T, V, H, types):
 
 
 @pytest.mark.parametrize("kind", ["uniform", "one", "two", "runs", "descending", "none"])
-@pytest.mark.parametrize("T,V,H", [(33, 10, 64), (4097, 300, 72), (4096, 70000, 8), (20000, 2000, 16),
+@pytest.mark.parametrize("T,V,H", [(33, 10, 64), (1024, 400, 264), (1025, 400, 264), (500, 3, 2056), (512, 90, 1032), (513, 90, 1032), (4097, 300, 72), (4096, 70000, 8), (20000, 2000, 16),
                                    (1000, 65536, 13), (70000, 257, 8), (300000, 1 << 18, 1)])
 def test_distributions(kind, T, V, H):
     idx, dout = ids(T, V, kind=kind), data((T, H), BF, T)

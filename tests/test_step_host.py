@@ -176,11 +176,12 @@ def test_embedding_backward_rejects(L):
         assert call(**kw) == SHAPE
     for kw in (dict(idx=None), dict(dout=None), dict(dtable=None)):
         assert call(**kw) == NULL
-    assert call(dtable=C + 2) == ALIGN and call(ws=D + 4) == ALIGN
-    assert call(dtable=B) == ALIAS and call(dtable=A) == ALIAS and call(ws=B) == ALIAS
-    need = L.embedding_backward_workspace_size(10, 100, 64)
-    assert need > 0
-    assert call(ws=None) == WORKSPACE and call(wsb=need - 1) == WORKSPACE
+    assert call(dtable=C + 2) == ALIGN
+    assert call(dtable=B) == ALIAS and call(dtable=A) == ALIAS
+    need = L.embedding_backward_workspace_size(5000, 100, 64)
+    assert need > 0 and L.embedding_backward_workspace_size(10, 100, 64) == 0
+    assert call(tokens=5000, ws=None) == WORKSPACE and call(tokens=5000, wsb=need - 1) == WORKSPACE
+    assert call(tokens=5000, ws=D + 4) == ALIGN and call(tokens=5000, ws=B) == ALIAS
     assert call(hidden=0) == OK and call(vocab=0) == OK and call(tokens=0, acc=1) == OK
     for bad in ((-1, 10, 10), (10, -1, 10), (10, 10, -1), (2 ** 31, 1, 1)):
         assert L.embedding_backward_workspace_size(*bad) == 0
