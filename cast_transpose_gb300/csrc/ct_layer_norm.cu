@@ -184,16 +184,20 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
 // thread keeps its columns from row to row, and only the vectors at the row's ends
 // are not whole.
 // Threads of an SM, and of a block at most: with 80 registers each, or 128 in the
-// shifted backward pass.
-constexpr int ring_threads(bool more) { return more ? 512 : 768; }
+// shifted backward pass, or 168 with four vectors.  (What does not fit goes through
+// L2: nearly all of the SM's memory is the ring's.  Backward with two vectors and 80
+// registers, of which 16 bytes do not: 8192x12288 190 us, so: 174; forward with
+// three and 96: 8191x6144 100 us, two and 80: 76, four and 168: 75, but 132 against
+// 122 with an fp32 residual.)
+constexpr int ring_threads(int per, bool more) { return per == 4 ? 384 : more ? 512 : 768; }
 // Rows of whole vectors that fit a warp (ONE) need no exchange between warps: up to
 // 512 columns with two vectors per thread and, where the exchange is most of the
 // rest, in the backward pass, 1024 with four.  Blocks of an SM, by their registers
 // (more blocks with fewer are slower: backward 16384x1024 37.8 us with 8, 50.5 with
 // 12; two warps per row 45.7).
 constexpr int one_blocks(int per, bool sums) { return per == 4 ? 8 : sums ? 12 : 16; }
-constexpr int kOneRows = 4;             // of a block with four vectors, at least: 2048x1024 17.0 us, else 15.1
-constexpr int ring_block(bool one, bool more) { return one ? 32 : ring_threads(more); }
+constexpr int kOneRows = 4;             // of a block with four vectors, at least: 2048x1024 17.0 us, else 16.0
+constexpr int ring_block(int per, bool one, bool more) { return one ? 32 : ring_threads(per, more); }
 constexpr int kRingStages = 4;                  // at most
 constexpr int kRingSmem = 226 * 1024;           // of an SM's blocks together
 constexpr int kShiftRows = 8;
@@ -383,7 +387,7 @@ __device__ __forceinline__ int shift_of(int H) {
 //   M2 = sum over warps of M2_w + n_w (mean_w - mean)^2
 // without the cancellation of a difference of squares.
 template <typename T, typename R, bool SHIFT, int PER, bool ONE>
-__global__ void __launch_bounds__(ring_block(ONE, false), ONE ? one_blocks(PER, false) : 1)
+__global__ void __launch_bounds__(ring_block(PER, ONE, false), ONE ? one_blocks(PER, false) : 1)
     layer_norm_kernel(const LayerNormArgs a, int stages) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 slots[2][32];
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(ring_block(ONE, false), ONE ? one_blocks(PER, 
 // a row's work needs, may have a single place, into which a thread copies the next
 // row's as soon as it has read this one's (ONCE): where whole stages would be too few.
 template <typename T, typename R, bool SHIFT, int PER, bool ONE, bool ONCE>
-__global__ void __launch_bounds__(ring_block(ONE, SHIFT), ONE ? one_blocks(PER, true) : 1)
+__global__ void __launch_bounds__(ring_block(PER, ONE, SHIFT), ONE ? one_blocks(PER, true) : 1)
     layer_norm_backward_kernel(const LayerNormBackwardArgs a, int stages) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 slots[2][32];
@@ -667,9 +671,9 @@ RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, i
     RingShape s = {};
     s.one = !shifted && (hidden <= 512 || (sums && hidden <= 1024 &&
                                            rows >= int64_t(kOneRows) * sm_count() * one_blocks(4, true)));
-    s.per = s.one && hidden > 512 ? 4 : 2;
+    s.per = sums && !shifted && hidden > 512 ? 4 : 2;
     s.threads = row_threads(hidden + (shifted ? kShiftRows - 1 : 0), s.per);
-    const int sm_threads = s.one ? 32 * one_blocks(s.per, sums) : ring_threads(sums && shifted);
+    const int sm_threads = s.one ? 32 * one_blocks(s.per, sums) : ring_threads(s.per, sums && shifted);
     const int columns = s.threads * s.per * 8;
     if (s.threads > sm_threads) return s;
     for (int per_sm = sm_threads / s.threads; per_sm > 0; --per_sm) {
@@ -691,10 +695,11 @@ RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, i
     return s;
 }
 
-// Launches a kernel of many rows; the first time on a device it is allowed its
-// shared memory.
-template <auto KERNEL, typename Args>
+// Launches a kernel of many rows for PER vectors per thread, which the shape has to
+// be for; the first time on a device it is allowed its shared memory.
+template <auto KERNEL, int PER, bool ONE, typename Args>
 cudaError_t launch_ring(const RingShape& s, const Args& a, cudaStream_t stream) {
+    if (s.per != PER || s.one != ONE || (ONE && s.threads != 32)) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> known{0};       // a bit per device
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
@@ -782,7 +787,7 @@ int column_shares(int64_t rows, int64_t hidden) {
 
 // Blocks of a backward launch of many rows, at most: the workspace has room for them.
 int64_t most_blocks(int64_t rows, int64_t hidden) {
-    const int of_rings = ring_threads(false) / row_threads(static_cast<int>(std::max<int64_t>(hidden, 1)), 2);
+    const int of_rings = ring_threads(2, false) / row_threads(static_cast<int>(std::max<int64_t>(hidden, 1)), 2);
     return rows > sm_count() ? std::min(rows, int64_t(sm_count()) * of_rings) : 0;
 }
 
@@ -797,9 +802,9 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int res_dtype, 
         const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + (a.u ? sizeof(T) : 0), 0, false)
                                     : RingShape{};
         if (s.blocks > 0)
-            return s.one ? launch_ring<layer_norm_kernel<T, R, false, 2, true>>(s, a, stream)
-                 : vec   ? launch_ring<layer_norm_kernel<T, R, false, 2, false>>(s, a, stream)
-                         : launch_ring<layer_norm_kernel<T, R, true, 2, false>>(s, a, stream);
+            return s.one ? launch_ring<layer_norm_kernel<T, R, false, 2, true>, 2, true>(s, a, stream)
+                 : vec   ? launch_ring<layer_norm_kernel<T, R, false, 2, false>, 2, false>(s, a, stream)
+                         : launch_ring<layer_norm_kernel<T, R, true, 2, false>, 2, false>(s, a, stream);
         auto* kernel = per == 1 ? (vec ? layer_norm_row_kernel<T, R, 8, 1> : layer_norm_row_kernel<T, R, 1, 1>)
                      : per == 2 ? (vec ? layer_norm_row_kernel<T, R, 8, 2> : layer_norm_row_kernel<T, R, 1, 2>)
                                 : (vec ? layer_norm_row_kernel<T, R, 8, 4> : layer_norm_row_kernel<T, R, 1, 4>);
@@ -828,11 +833,11 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype
         cudaError_t e = cudaSuccess;
         int parts;
         if (s.blocks > 0) {
-            e = s.once ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, false, true>>(s, a, stream)
-              : s.one  ? (s.per == 2 ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, true, false>>(s, a, stream)
-                                     : launch_ring<layer_norm_backward_kernel<T, R, false, 4, true, false>>(s, a, stream))
-              : vec    ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, false, false>>(s, a, stream)
-                       : launch_ring<layer_norm_backward_kernel<T, R, true, 2, false, false>>(s, a, stream);
+            e = s.once ? launch_ring<layer_norm_backward_kernel<T, R, false, 4, false, true>, 4, false>(s, a, stream)
+              : s.one  ? (s.per == 2 ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, true, false>, 2, true>(s, a, stream)
+                                     : launch_ring<layer_norm_backward_kernel<T, R, false, 4, true, false>, 4, true>(s, a, stream))
+              : vec    ? launch_ring<layer_norm_backward_kernel<T, R, false, 4, false, false>, 4, false>(s, a, stream)
+                       : launch_ring<layer_norm_backward_kernel<T, R, true, 2, false, false>, 2, false>(s, a, stream);
             if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
             parts = s.blocks;
         } else {
