@@ -175,3 +175,15 @@ def test_offsets_past_32_bits():
     ct.embedding_backward(idx, out, table, ws)
     assert (table[-1] == 2).all() and (table[-300000] == 3).all() and not table[0].any()
     assert table.sum(dtype=torch.float64).item() == 5.0 * H
+
+
+def test_gradient_past_32_bits():
+    """More than 2^31 elements of gradients come in, of many tokens."""
+    T, V, H = 600000, 100, 4096
+    idx = torch.arange(T, device="cuda") % V
+    dout = torch.ones(T, H, dtype=BF, device="cuda")
+    dout[-1] = 3.0
+    out = torch.empty(V, H, device="cuda")
+    ws = torch.empty(ct.embedding_backward_workspace_size(T, V, H), dtype=torch.uint8, device="cuda")
+    ct.embedding_backward(idx, dout, out, ws)
+    assert (out[:-1] == T // V).all() and (out[-1] == T // V + 2).all()

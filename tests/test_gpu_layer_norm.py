@@ -372,3 +372,48 @@ def test_rows_past_32_bits():
                        (SEED % 2 ** 32, SEED >> 32))
     bits = np.stack([h for w in words for h in (w % 65536, w // 65536)], 2).reshape(2, -1)
     assert np.array_equal((x[-2:] > 0).cpu().numpy(), bits >= ref.cut_of(0.25))
+
+
+@pytest.mark.parametrize("hidden", [4096, 4095])
+def test_layer_norm_past_32_bits(hidden):
+    """Offsets beyond 2^31 elements: the last rows are those of a small call."""
+    rows, last = 540000, 3
+    res = torch.empty(rows, hidden, dtype=BF, device="cuda").normal_()
+    y, dres = torch.empty_like(res), torch.empty_like(res)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    w = data((hidden,), BF, 1, 0.2, 1.0).cuda()
+    ct.layer_norm(None, res, None, y, weight=w, mean=mean, rstd=rstd)
+    small = torch.empty(last, hidden, dtype=BF, device="cuda")
+    ct.layer_norm(None, res[-last:].clone(), None, small, weight=w)
+    one = torch.ones(last, hidden, dtype=torch.float64)
+    n = ref.LayerNorm(None, res[-last:].cpu(), w.cpu(), None, EPS, 0.0, one).forward()
+    for out in (y[-last:], small):
+        base.close(out, n.y, base.rounded(n.y, n.y_err, BF), "y")
+    ws = torch.empty(ct.layer_norm_backward_workspace_size(rows, hidden), dtype=torch.uint8, device="cuda")
+    dbias = torch.empty(hidden, dtype=BF, device="cuda")
+    y.zero_()
+    y[-1] = 2.0                                  # the only gradient, of the last row
+    ct.layer_norm_backward(y, None, res, mean, rstd, dres, dbias=dbias, workspace=ws, weight=w)
+    want = n.backward(y[-last:].cpu(), None, res[-last:].cpu(), mean[-last:].cpu(), rstd[-last:].cpu())["dres"]
+    base.close(dres[-last:], want[0], base.rounded(*want, BF), "dres")
+    assert not dres[:-1].any() and (dbias == 2.0).all()
+
+
+def test_two_host_threads():
+    """Calls from two threads on streams of their own, a workspace each."""
+    import threading
+    c = [Case(700, 1032, seed=i) for i in range(2)]
+    want = [x.backward()[0] for x in c]
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                got = c[i].backward()[0]
+                stream.synchronize()
+                wrong.extend(k for k in got if not torch.equal(got[k], want[i][k]))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not wrong

@@ -211,3 +211,22 @@ def test_the_same_from_call_to_call():
     one, two = c.forward(), c.forward()
     for k in one:
         assert torch.equal(one[k], two[k])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens are those of a small call."""
+    T, E, K, last = 2100003, 1024, 2, 5
+    logits = torch.empty(T, E, dtype=BF, device="cuda").normal_()
+    idx, w = torch.empty(T, K, dtype=torch.int32, device="cuda"), torch.empty(T, K, device="cuda")
+    counts = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(ct.moe_router_workspace_size(T, K, E), dtype=torch.uint8, device="cuda")
+    ct.moe_router(logits, idx, w, counts, workspace=ws)
+    r = ref.Router(logits[-last:].cpu(), None, K, True, 0.0, 0.0).forward()
+    assert torch.equal(idx[-last:].cpu(), r.idx) and counts[E].item() == T
+    assert counts[:E].sum().item() == T * K
+    base.close(w[-last:], r.weights, r.w_err, "weights")
+    dl = torch.empty_like(logits)
+    ct.moe_router_backward(torch.ones(T, K, device="cuda") * torch.tensor([1.0, -1.0], device="cuda"), None, logits,
+                           idx, counts, dl)
+    value, err = r.backward(torch.tensor([[1.0, -1.0]]).expand(last, K), 0.0)
+    base.close(dl[-last:], value, base.rounded(value, err, BF), "dlogits")
