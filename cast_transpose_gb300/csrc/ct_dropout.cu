@@ -44,12 +44,12 @@ __device__ __forceinline__ dev::Raw8<T> dropped8(const dev::Raw8<T>& raw, uint32
 }
 
 // Rows of whole groups in 16-byte-aligned buffers: a block takes consecutive groups,
-// a thread kDropItems at a time, whose loads are in flight together, kDropRounds
-// times.
+// a thread ITEMS at a time, whose loads are in flight together, `rounds` times: four
+// twice, or one once where that would not fill the GPU.
 constexpr int kDropItems = 4, kDropRounds = 2;
 
-template <typename T>
-__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutArgs a, int64_t groups) {
+template <typename T, int ITEMS>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutArgs a, int64_t groups, int rounds) {
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
@@ -57,19 +57,19 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropoutArgs
     constexpr int step = kDropThreads;
     const T* x = static_cast<const T*>(a.x);
     T* out = static_cast<T*>(a.out);
-    int64_t g0 = int64_t(blockIdx.x) * (kDropRounds * kDropItems * step) + threadIdx.x;
+    int64_t g0 = int64_t(blockIdx.x) * (rounds * (ITEMS * step)) + threadIdx.x;
     // the row of a group, and its number there
     const uint32_t row_groups = static_cast<uint32_t>(a.cols / 8);
     const uint32_t step_rows = step / row_groups, step_cols = step - step_rows * row_groups;
     uint32_t row = static_cast<uint32_t>((groups >> 32) == 0 ? uint32_t(g0) / row_groups : g0 / row_groups);
     uint32_t col = static_cast<uint32_t>(g0 - int64_t(row) * row_groups);
 #pragma unroll 1
-    for (int round = 0; round < kDropRounds && g0 < groups; ++round, g0 += kDropItems * step) {
-        dev::Raw8<T> raw[kDropItems];
+    for (int round = 0; round < rounds && g0 < groups; ++round, g0 += ITEMS * step) {
+        dev::Raw8<T> raw[ITEMS];
 #pragma unroll
-        for (int i = 0; i < kDropItems; ++i) raw[i] = dev::load8(x + 8 * min(g0 + i * step, groups - 1));
+        for (int i = 0; i < ITEMS; ++i) raw[i] = dev::load8(x + 8 * min(g0 + i * step, groups - 1));
 #pragma unroll
-        for (int i = 0; i < kDropItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             const int64_t g = g0 + i * step;
             if (g >= groups) break;
             if (keyed.drops.some) {
@@ -207,9 +207,15 @@ cudaError_t launch_dropout(const DropoutArgs& a, int dtype, cudaStream_t stream)
     return by_types(dtype, dtype, [&](auto t, auto) {
         using T = decltype(t);
         const int64_t n = a.rows * a.cols;
-        if (a.cols % 8 == 0 && all_aligned(a.x, a.out))
-            return launch_pdl(dropout_kernel<T>, dim3(blocks_of(n / 8, kDropThreads * kDropItems * kDropRounds)), dim3(kDropThreads), 0, stream,
-                              a, n / 8);
+        if (a.cols % 8 == 0 && all_aligned(a.x, a.out)) {
+            // a group per thread: 64x4096 bf16 in 128 blocks, not 16
+            if (n / 8 < int64_t(sm_count()) * kDropThreads * kDropItems * kDropRounds)
+                return launch_pdl(dropout_kernel<T, 1>, dim3(blocks_of(n / 8, kDropThreads)), dim3(kDropThreads), 0,
+                                  stream, a, n / 8, 1);
+            return launch_pdl(dropout_kernel<T, kDropItems>,
+                              dim3(blocks_of(n / 8, kDropThreads * kDropItems * kDropRounds)), dim3(kDropThreads), 0,
+                              stream, a, n / 8, int(kDropRounds));
+        }
         const int off = static_cast<int>(reinterpret_cast<uintptr_t>(a.x) % 16);
         if (a.drop.cut && a.cols >= kFlatMinCols && off == int(reinterpret_cast<uintptr_t>(a.out) % 16)) {
             const int head = static_cast<int>(std::min<int64_t>(n, (16 - off) % 16 / int(sizeof(T))));

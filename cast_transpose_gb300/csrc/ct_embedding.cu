@@ -502,9 +502,9 @@ __global__ void __launch_bounds__(kJoinThreads)
                     float4 v[kJoinBatch];
 #pragma unroll
                     for (int i = 0; i < kJoinBatch; ++i)
-                        v[i] = *reinterpret_cast<const float4*>(part + 2 * min(i0 + i * kJoinWays, more) * s.stride);
+                        v[i] = dev::load_now(reinterpret_cast<const float4*>(part + 2 * min(i0 + i * kJoinWays, more) * s.stride));
 #pragma unroll
-                    for (int i = 0; i < kJoinBatch; ++i) {     // a condition around the sums would draw the loads in
+                    for (int i = 0; i < kJoinBatch; ++i) { 
                         const bool use = i0 + i * kJoinWays <= more;
                         sum.x += use ? v[i].x : 0.0f;
                         sum.y += use ? v[i].y : 0.0f;

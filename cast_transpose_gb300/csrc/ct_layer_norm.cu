@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const LayerNormBa
     for (int i0 = warp; i0 < parts; i0 += ways * kJoinBatch) {
         float v[kJoinBatch];
 #pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i) v[i] = from[2 * int64_t(min(i0 + i * ways, parts - 1)) * H];
+        for (int i = 0; i < kJoinBatch; ++i) v[i] = dev::load_now(from + 2 * int64_t(min(i0 + i * ways, parts - 1)) * H);
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i) sum += i0 + i * ways < parts ? v[i] : 0.0f;
     }

@@ -292,69 +292,69 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
     cluster.sync();      // before a block leaves that others read from
 }
 
-// Joins the clusters' sums in a fixed order: a thread takes every `ways`-th of them
-// for one expert, eight loads at a time.
-constexpr int kRouterJoinThreads = 1024, kJoinBatch = 8;
+// Joins the clusters' sums in a fixed order, a cluster of blocks with some of the
+// experts each (one SM alone would take 2 us to read 108 sums of 256 experts): a
+// thread takes every `ways`-th of the sums for one expert, kJoinBatch loads at a time.
+constexpr int kJoinThreads = 256, kJoinBlocks = 8, kJoinBatch = 8;
 
-__global__ void __launch_bounds__(kRouterJoinThreads) router_join_kernel(const RouterArgs a, int parts) {
-    __shared__ float probs[kRouterJoinThreads];
-    __shared__ int counts[kRouterJoinThreads];
-    __shared__ float warp_sums[32];
+__global__ void __launch_bounds__(kJoinThreads) router_join_kernel(const RouterArgs a, int parts) {
+    __shared__ float probs[kJoinThreads], warp_sums[kJoinThreads / 32], block_balance;
+    __shared__ int counts[kJoinThreads];
+    const auto cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, words = sum_words(E);
-    const int columns = min((E + 32) / 32 * 32, kRouterJoinThreads), ways = kRouterJoinThreads / columns;
-    const int x = tid % columns, y = tid / columns;
+    const int columns = (E + kJoinBlocks) / kJoinBlocks, ways = kJoinThreads / columns;     // at most 128
+    const int x = tid % columns, y = tid / columns, e = blockIdx.x * columns + x;
     const float* sums = static_cast<const float*>(a.workspace);
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
-    float balance = 0.0f, squares = 0.0f;
-    int tokens = 0;
-    for (int e0 = 0; e0 <= E; e0 += columns) {
-        const int e = e0 + x;
-        float p = 0.0f;
-        int count = 0;
-        if (e <= E && y < ways)
-            for (int b0 = y; b0 < parts; b0 += ways * kJoinBatch) {
-                float q[kJoinBatch];
-                int c[kJoinBatch];
+    const bool here = e <= E && y < ways;
+    float p = 0.0f;
+    int count = 0;
+    if (here)
+        for (int b0 = y; b0 < parts; b0 += ways * kJoinBatch) {
+            float q[kJoinBatch];
+            int c[kJoinBatch];
 #pragma unroll
-                for (int i = 0; i < kJoinBatch; ++i) {
-                    const float* part = sums + min(b0 + i * ways, parts - 1) * words;
-                    q[i] = part[e < E ? e : 2 * E + 1];
-                    c[i] = reinterpret_cast<const int*>(part)[E + e];
-                }
+            for (int i = 0; i < kJoinBatch; ++i) {
+                const float* part = sums + min(b0 + i * ways, parts - 1) * words;
+                q[i] = dev::load_now(part + (e < E ? e : 2 * E + 1));
+                c[i] = dev::load_now(reinterpret_cast<const int*>(part) + E + e);
+            }
 #pragma unroll
-                for (int i = 0; i < kJoinBatch; ++i) {
-                    const bool use = b0 + i * ways < parts;
-                    p += use ? q[i] : 0.0f;
-                    count += use ? c[i] : 0;
-                }
-            }
-        probs[tid] = p;
-        counts[tid] = count;
-        __syncthreads();
-        if (y == 0 && e <= E) {
-            for (int w = 1; w < ways; ++w) {
-                p += probs[w * columns + x];
-                count += counts[w * columns + x];
-            }
-            a.counts[e] = count;
-            if (e < E) {
-                balance = fmaf(static_cast<float>(count), p, balance);
-            } else {                        // this thread keeps them for the loss
-                tokens = count;
-                squares = p;
+            for (int i = 0; i < kJoinBatch; ++i) {
+                const bool use = b0 + i * ways < parts;
+                p += use ? q[i] : 0.0f;
+                count += use ? c[i] : 0;
             }
         }
-        __syncthreads();
+    probs[tid] = p;
+    counts[tid] = count;
+    __syncthreads();
+    float balance = 0.0f;
+    if (here && y == 0) {
+        for (int w = 1; w < ways; ++w) {
+            p += probs[w * columns + x];
+            count += counts[w * columns + x];
+        }
+        a.counts[e] = count;
+        if (e < E) balance = static_cast<float>(count) * p;
     }
     balance = dev::warp_sum(balance);
     if (lane == 0) warp_sums[warp] = balance;
     __syncthreads();
-    if (tid != E % columns) return;
-    balance = 0.0f;
-    for (int w = 0; w < 32; ++w) balance += warp_sums[w];
-    put_loss(a, balance, squares, tokens);
+    if (tid == 0) {
+        balance = 0.0f;
+        for (int w = 0; w < kJoinThreads / 32; ++w) balance += warp_sums[w];
+        block_balance = balance;
+    }
+    cluster.sync();
+    if (here && y == 0 && e == E) {          // its count is the tokens', its sum the squares'
+        balance = 0.0f;
+        for (int b = 0; b < kJoinBlocks; ++b) balance += *cluster.map_shared_rank(&block_balance, b);
+        put_loss(a, balance, p, count);
+    }
+    cluster.sync();      // before a block leaves that another reads from
 }
 
 // With p = softmax(logits), A_e = c f_e + (its weight's gradient, where weights are
@@ -509,7 +509,11 @@ cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream) {
         return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a);
     });
     if (e != cudaSuccess || parts <= 1) return e;
-    return launch_pdl(router_join_kernel, dim3(1), dim3(kRouterJoinThreads), 0, stream, a, parts);
+    cfg.gridDim = dim3(kJoinBlocks);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    attr[1].val.clusterDim.x = kJoinBlocks;
+    return cudaLaunchKernelEx(&cfg, router_join_kernel, a, parts);
 }
 
 cudaError_t launch_router_backward(const RouterArgs& a, int dtype, cudaStream_t stream) {
