@@ -189,7 +189,11 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
 // registers, of which 16 bytes do not: 8192x12288 190 us, so: 174; forward with
 // three and 96: 8191x6144 100 us, two and 80: 76, four and 168: 75, but 132 against
 // 122 with an fp32 residual.)
-constexpr int ring_threads(int per, bool more) { return per == 4 ? 384 : more ? 512 : 768; }
+constexpr int ring_threads(int per, bool more) { return per == 4 ? 384 : per == 2 && more ? 512 : 768; }
+// Short shifted rows, few to a block: with one vector per thread a row's way through
+// the backward pass is shorter, though its warps do more besides the columns
+// (4099x777 24.1 us against 27.2, 16384x777 58.6 against 52.6).
+constexpr int kFewRows = 6, kFewColumns = 1024 - 7;
 // Rows of whole vectors that fit a warp (ONE) need no exchange between warps: up to
 // 512 columns with two vectors per thread and, where the exchange is most of the
 // rest, in the backward pass, 1024 with four.  Blocks of an SM, by their registers
@@ -666,12 +670,13 @@ int row_per(int hidden) { return hidden <= 8192 ? 1 : hidden <= 16384 ? 2 : 4; }
 
 
 // column_bytes: of a column in a stage, extra_bytes: of what may be once beside the
-// stages instead; sums: the kernel keeps column sums.
-RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, int extra_bytes, bool sums) {
+// stages instead; sums: the kernel keeps column sums; few: one vector per thread.
+RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, int extra_bytes, bool sums,
+                     bool few = false) {
     RingShape s = {};
     s.one = !shifted && (hidden <= 512 || (sums && hidden <= 1024 &&
                                            rows >= int64_t(kOneRows) * sm_count() * one_blocks(4, true)));
-    s.per = sums && !shifted && hidden > 512 ? 4 : 2;
+    s.per = sums && !shifted && hidden > 512 ? 4 : few ? 1 : 2;
     s.threads = row_threads(hidden + (shifted ? kShiftRows - 1 : 0), s.per);
     const int sm_threads = s.one ? 32 * one_blocks(s.per, sums) : ring_threads(s.per, sums && shifted);
     const int columns = s.threads * s.per * 8;
@@ -788,7 +793,8 @@ int column_shares(int64_t rows, int64_t hidden) {
 // Blocks of a backward launch of many rows, at most: the workspace has room for them.
 int64_t most_blocks(int64_t rows, int64_t hidden) {
     const int of_rings = ring_threads(2, false) / row_threads(static_cast<int>(std::max<int64_t>(hidden, 1)), 2);
-    return rows > sm_count() ? std::min(rows, int64_t(sm_count()) * of_rings) : 0;
+    const int least = sm_count() / kShiftRows * kShiftRows;      // blocks of such a launch
+    return rows > least ? std::min(rows, int64_t(sm_count()) * of_rings) : 0;
 }
 
 }  // namespace
@@ -827,9 +833,14 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + sizeof(T),
-                                                 a.dres_out ? sizeof(R) : 0, true)
-                                    : RingShape{};
+        auto shape = [&](bool few) {
+            return ring_shape(a.rows, a.hidden, !vec, sizeof(R) + sizeof(T), a.dres_out ? sizeof(R) : 0, true, few);
+        };
+        RingShape s = {};
+        if (aligned) {
+            if (!vec && a.hidden <= kFewColumns) s = shape(true);
+            if (a.rows >= int64_t(kFewRows) * s.blocks) s = shape(false);      // also where there are none
+        }
         cudaError_t e = cudaSuccess;
         int parts;
         if (s.blocks > 0) {
@@ -837,7 +848,8 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype
               : s.one  ? (s.per == 2 ? launch_ring<layer_norm_backward_kernel<T, R, false, 2, true, false>, 2, true>(s, a, stream)
                                      : launch_ring<layer_norm_backward_kernel<T, R, false, 4, true, false>, 4, true>(s, a, stream))
               : vec    ? launch_ring<layer_norm_backward_kernel<T, R, false, 4, false, false>, 4, false>(s, a, stream)
-                       : launch_ring<layer_norm_backward_kernel<T, R, true, 2, false, false>, 2, false>(s, a, stream);
+              : s.per == 1 ? launch_ring<layer_norm_backward_kernel<T, R, true, 1, false, false>, 1, false>(s, a, stream)
+                           : launch_ring<layer_norm_backward_kernel<T, R, true, 2, false, false>, 2, false>(s, a, stream);
             if (e != cudaSuccess || (!a.dweight && !a.dbias)) return e;
             parts = s.blocks;
         } else {
