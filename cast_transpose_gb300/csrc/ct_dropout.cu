@@ -1,4 +1,11 @@
 // ct_dropout.cu -- dropout of a matrix by a counter-based generator.
+//
+// Each element is read and written once: HBM bounds fp32, and nearly 16-bit types,
+// whose eight columns to a call of the generator cost some 110 instructions, 140
+// where rows are not whole groups.  Measured, one GB300, of the measured copy rate:
+// 8192x6144 fp32 61.7 us (0.96), 8192x12288 bf16 63.7 us (403 MB, 0.93),
+// 8191x12287 bf16 71.1 us (0.83; instructions issue on 65% of the cycles),
+// 8191x6145 fp32 62.6 (0.95).
 #include "ct_device.cuh"
 #include "ct_dropout.cuh"
 #include "ct_ops.h"

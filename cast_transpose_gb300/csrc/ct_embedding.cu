@@ -1,5 +1,13 @@
 // ct_embedding.cu -- the embedding: rows of a table by token id, scaled, and
 // the gradient of the table, the tokens sorted by id.
+//
+// Bound by HBM.  Measured, one GB300, of the measured copy rate: 16384 rows of 6144
+// bf16 44.5 us (278 MB of distinct rows and output, 0.92); the gradient of 16384
+// tokens into 65536x4096 fp32 213 us (1208 MB, 0.84).  Of that the zeros of the rows
+// without a token take 154 us (908 MB: 5.9 TB/s, what stores alone reach here),
+// beside which the sort costs nothing; the sums 43 us, the join of frequent ids 8.
+// The gradient is deterministic: the sort is stable, an id's rows are added in the
+// order of the tokens within a chunk, and the chunks in theirs.
 #include "ct_device.cuh"
 #include "ct_ops.h"
 #include "ct_types.cuh"

@@ -1,6 +1,25 @@
 // ct_layer_norm.cu -- the junction between two blocks whose norm is a layer
 // norm: the branch's dropout, the residual sum and the norm, forward and
 // backward.
+//
+// Forward reads u and res and writes res_out and y, backward reads dy, res_out and
+// dres_out and writes dres and du: HBM would bound both, if the work on a column
+// were less.  A row takes two sums over its columns before anything of y or dres is
+// known, and a dropout some 11 instructions a column for its random bits alone.
+// Measured, one GB300, bf16, p = 0.1, of the measured copy rate: forward 8191x6144
+// 75.4 us (403 MB, 0.79; without dropout 70, 0.84), 8192x12288 153 (0.78; 127,
+// 0.93), backward with its join 8192x12288 173.7 us (1007 MB, 0.85), 8191x6144 94
+// (0.79).  Instructions issue on 60 to 65% of the cycles; warps wait little for
+// memory.  So:
+//   - rows come by asynchronous copies into rings of shared memory, stages ahead,
+//     so that no register holds what has not arrived and no warp waits for it;
+//   - a row takes one exchange between its warps and one barrier, two slots in turn
+//     (a forward pass that began the next row before it, so that the barrier found
+//     every warp with work left, was slower: 8191x6144 83 us);
+//   - arithmetic on pairs of columns, 16 to 32 columns a thread.
+// Launches of fewer rows than blocks fit take a kernel of a block per row, those
+// whose rows are not aligned to 16 bytes, too; its backward pass sums columns in a
+// kernel of its own.
 #include "ct_device.cuh"
 #include "ct_dropout.cuh"
 #include "ct_ops.h"
@@ -689,8 +708,10 @@ RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, i
             s.once = true;
             s.stages = std::min(kRingStages, (room - columns * extra_bytes) / (columns * column_bytes));
         }
-        // a row ahead is enough where many blocks have one each
-        if (s.stages < (s.once || s.one || per_sm == 1 ? 2 : 3)) continue;
+        // A row ahead is enough where many blocks have one each, and forward, which is
+        // done with a stage early (8192x6144 all fp32: two blocks with two 175 us, one
+        // with four 199).
+        if (s.stages < (!sums || s.once || s.one || per_sm == 1 ? 2 : 3)) continue;
         s.smem = size_t(columns) * (s.stages * (column_bytes + (s.once ? 0 : extra_bytes)) + (s.once ? extra_bytes : 0));
         int64_t blocks = int64_t(sm_count()) * per_sm;
         if (shifted) blocks = blocks / kShiftRows * kShiftRows;
