@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                     for (int i = 0; i < kJoinBatch; ++i)
                         v[i] = dev::load_now(reinterpret_cast<const float4*>(part + 2 * min(i0 + i * kJoinWays, more) * s.stride));
 #pragma unroll
-                    for (int i = 0; i < kJoinBatch; ++i) { 
+                    for (int i = 0; i < kJoinBatch; ++i) {
                         const bool use = i0 + i * kJoinWays <= more;
                         sum.x += use ? v[i].x : 0.0f;
                         sum.y += use ? v[i].y : 0.0f;

@@ -379,7 +379,8 @@ struct RowDrops {
     }
 };
 
-// s / n, rounded to nearest but for rare last bits, given r = 1 / n.
+// s / n, rounded to nearest but for rare last bits, given r = 1 / n: Newton's step for
+// the quotient, q + (s - q n) r, whose residual a fused multiply-add has exactly.
 __device__ __forceinline__ float divided(float s, float n, float r) {
     const float q = s * r;
     return fmaf(fmaf(-q, n, s), r, q);
@@ -686,7 +687,6 @@ __global__ void __launch_bounds__(ring_block(PER, ONE, SHIFT), ONE ? one_blocks(
 // Threads of a block that holds a row of `hidden` columns, PER vectors of eight each.
 int row_threads(int hidden, int per) { return (hidden + 256 * per - 1) / (256 * per) * 32; }
 int row_per(int hidden) { return hidden <= 8192 ? 1 : hidden <= 16384 ? 2 : 4; }
-
 
 // column_bytes: of a column in a stage, extra_bytes: of what may be once beside the
 // stages instead; sums: the kernel keeps column sums; few: one vector per thread.
