@@ -17,6 +17,7 @@
 #include "ct_vec.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <cooperative_groups.h>
 
 namespace ct {
@@ -25,7 +26,13 @@ namespace {
 // A warp takes a token; its lane l holds the logits of the experts l, l + 32, ...
 constexpr int kRouterWarps = 8;
 constexpr int kRouterCluster = 4;
-constexpr int kRouterMaxClusters = 108;
+// Blocks of an SM, by their registers, and clusters on the GPU at a time with each.
+// (16384 tokens of 1024 experts 43.7 us; with three blocks' clusters, of which most
+// come after the first ones, 58; of 64 experts 13.4, and 14.3.)
+constexpr int router_sm_blocks(int experts) {
+    return experts <= 64 ? 6 : experts <= 128 ? 4 : experts <= 256 ? 3 : experts <= 512 ? 2 : 1;
+}
+constexpr int kRouterClusters = 36;
 constexpr int kRouterOneCluster = 2;    // tokens per warp up to which one cluster takes them all
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
@@ -81,44 +88,68 @@ struct Choice {
     float logit;
 };
 
+// What a warp needs to choose by.
+struct Among {
+    unsigned key[32];
+    int expert[32];
+};
+
 // The K <= 32 largest logits x of a token, whose largest, `top`, is a number.  The
 // K-th largest of the lanes' own largest is a bound that K logits reach at least,
-// and few more do (with 8 of 256 some 10): those go to a lane each and are ranked by
+// and few more do (with 8 of 256 some 10; equal ones, which leave together, lower
+// it): those go to a lane each, which reads the logit again, and are ranked by
 // comparing all with all.  False where more than 32 reach it: many equal ones.
-template <int N>
-__device__ __forceinline__ bool choose_few(const float (&x)[N], float best, float top, int K, float2* among,
-                                           Choice& mine) {
+template <int N, typename T>
+__device__ __forceinline__ bool choose_few(const T* row, const float (&x)[N], float best, float top, int K,
+                                           Among& among, Choice& mine) {
     const int lane = threadIdx.x & 31;
     float bound = top;
     for (int k = 1; k < K; ++k) {
-        const unsigned with = __ballot_sync(kAll, best == bound);
-        if (lane == __ffs(with) - 1) best = -INFINITY;
+        if (best == bound) best = -INFINITY;
         bound = lanes_max(best);
     }
-    int total = 0;
+    bound = fmaxf(bound, -FLT_MAX);         // -inf is not to be chosen
+    unsigned reach = 0;                     // a bit for each of the lane's logits
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const bool reaches = x[i] >= bound && x[i] > -INFINITY;
-        const unsigned with = __ballot_sync(kAll, reaches);
+    for (int i = 0; i < N; ++i) reach |= x[i] >= bound ? 1u << i : 0;
+    int total = 0;
+    while (const unsigned with = __ballot_sync(kAll, reach)) {
         const int at = total + __popc(with & ((1u << lane) - 1));
-        if (reaches && at < 32) among[at] = make_float2(x[i], __int_as_float(lane + 32 * i));
+        if (reach && at < 32) among.expert[at] = lane + 32 * (__ffs(reach) - 1);
+        reach &= reach - 1;
         total += __popc(with);
     }
     if (total > 32) return false;
     __syncwarp();
     const bool here = lane < total;
-    const float2 own = among[here ? lane : 0];
-    mine.logit = own.x;
-    mine.expert = __float_as_int(own.y);
-    int before = 0;
-    for (int j = 0; j < total; ++j) {
-        const float2 other = among[j];
-        before += other.x > mine.logit || (other.x == mine.logit && __float_as_int(other.y) < mine.expert);
-    }
+    mine.expert = here ? among.expert[lane] : -1;
+    mine.logit = here ? dev::to_f32(row[mine.expert]) : -INFINITY;
+    // A 16-bit logit leaves 13 bits of its order free, and there the expert decides
+    // between equal ones.
+    constexpr bool kRoom = sizeof(T) == 2;
+    constexpr unsigned kFree = 0x1FFF;
+    static_assert(kMaxExperts <= kFree + 1);
+    unsigned key = order_of(mine.logit);
+    if (kRoom) key = (key & ~kFree) | (kFree - mine.expert);
+    key = here ? key : 0;
+    among.key[lane] = key;
     __syncwarp();
+    int before = 0;
+#pragma unroll 1                            // some three rounds: unrolled 4% slower
+    for (int j = 0; j < total; j += 4) {
+        const uint4 other = *reinterpret_cast<const uint4*>(among.key + j);
+        if (other.x > key) ++before;
+        if (other.y > key) ++before;
+        if (other.z > key) ++before;
+        if (other.w > key) ++before;
+    }
     // slots past the number of those that can be chosen get none
-    mine.slot = here ? before : lane;
-    if (!here) mine.expert = -1;
+    if (!here) before = lane;
+    // all ranks are there once, unless some are equal: those by their expert
+    if (!kRoom && __reduce_add_sync(kAll, before) != 31 * 32 / 2)
+        for (int j = 0; j < total; ++j) before += here && among.key[j] == key && among.expert[j] < mine.expert;
+    __syncwarp();
+    mine.slot = before;
     return true;
 }
 
@@ -138,25 +169,29 @@ __device__ __forceinline__ float exponentials(float (&x)[N], float top) {
 // tokens), the squared logsumexps.  In the workspace one for each cluster.
 __host__ __device__ constexpr int sum_words(int experts) { return 2 * experts + 2; }
 
+// Without a z loss squares past fp32, of a token whose logits are all the lowest
+// number, do not matter.
 __device__ __forceinline__ void put_loss(const RouterArgs& a, float balance, float squares, int tokens) {
     if (!a.loss) return;
     const float n = static_cast<float>(tokens);
-    *a.loss = tokens == 0 ? 0.0f
-                          : a.balance * a.experts * (balance / (n * a.topk)) / n + a.z * (squares / n);
+    float loss = 0.0f;
+    if (tokens > 0) loss = a.balance * a.experts * (balance / (n * a.topk)) / n;
+    if (tokens > 0 && a.z != 0.0f) loss += a.z * (squares / n);
+    *a.loss = loss;
 }
 
 // A cluster's blocks add up their sums through each other's shared memory, each
 // some of the experts; a launch of one cluster goes on to the loss, else
 // router_join_kernel does.
 template <int N, typename T>
-__global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterArgs a) {
+__global__ void __launch_bounds__(32 * kRouterWarps, router_sm_blocks(32 * N)) router_kernel(const RouterArgs a) {
     extern __shared__ float smem[];
     float* own = smem;                                                  // [sum_words]: of this block
     int* counts = reinterpret_cast<int*>(own + a.experts);
     float* probs = own + sum_words(a.experts);                          // [warps][E]
     __shared__ float warp_squares[kRouterWarps], warp_balance[kRouterWarps];
     __shared__ float block_balance;
-    __shared__ float2 among[kRouterWarps][32];
+    __shared__ __align__(16) Among among[kRouterWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, K = a.topk;
     const auto cluster = cooperative_groups::this_cluster();
     const int blocks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -187,7 +222,8 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
         Choice mine[2] = {{lane, -1, 0.0f}, {lane + 32, -1, 0.0f}};
         // (with a lane's one or two logits there is nothing to leave out first)
         const bool few = N >= 4 && K <= 32 && top == top;
-        if (any && !(few && choose_few<N>(x, best, top, K, among[warp], mine[0]))) {
+        const T* row = static_cast<const T*>(a.logits) + t * E;
+        if (any && !(few && choose_few<N>(row, x, best, top, K, among[warp], mine[0]))) {
             // one after the other
             unsigned key[N];
 #pragma unroll
@@ -372,17 +408,24 @@ __global__ void __launch_bounds__(kJoinThreads) router_join_kernel(const RouterA
 //   dlogits_e = p_e (A_e - sum p A + 2 dloss z logsumexp / n)
 // and, where weights are a softmax over the chosen experts, w_k (dw_k - sum w dw)
 // at those.
+//
+// The slots' gradients get to the lanes of their experts through shared memory: a
+// lane of the K puts its own in the expert's place.
 template <int N, typename T>
-__global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(const RouterArgs a) {
+__global__ void __launch_bounds__(32 * kRouterWarps, router_sm_blocks(32 * N))
+    router_backward_kernel(const RouterArgs a) {
+    __shared__ int places[kRouterWarps][32 * N];        // zeros between tokens
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, K = a.topk;
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     if (a.noop && *a.noop != 0.0f) return;
     const float n = static_cast<float>(max(a.counts[E], 1)), dloss = a.dloss ? *a.dloss : 0.0f;
     const float z = 2.0f * a.z * dloss / n;
+    int* const place = places[warp];
     float load[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+        place[lane + 32 * i] = 0;
         const int e = lane + 32 * i;
         load[i] = e < E ? a.balance * dloss * E / n * (a.counts[e] / (n * K)) : 0.0f;
     }
@@ -434,7 +477,25 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
 #pragma unroll
             for (int i = 0; i < 2; ++i) dw[i] = w[i] / sum * (dw[i] - dot);
         }
-        if (a.dweights)
+        const bool has = chosen[0] >= 0;
+        bool one_by_one = K > 32;
+        if (a.dweights && !one_by_one) {
+            __syncwarp();
+            if (has) place[chosen[0]] = lane;
+            __syncwarp();
+            one_by_one = __any_sync(kAll, has && place[chosen[0]] != lane);     // an expert twice
+            if (has) place[chosen[0]] = one_by_one ? 0 : __float_as_int(dw[0]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float d = __int_as_float(place[lane + 32 * i]);
+                if (a.normalize) g[i] = d;
+                else each[i] += d;
+            }
+            __syncwarp();
+            if (has) place[chosen[0]] = 0;
+        }
+        if (a.dweights && one_by_one)
             for (int k = 0; k < K; ++k) {
                 const int e = __shfl_sync(kAll, k < 32 ? chosen[0] : chosen[1], k & 31);
                 const float d = __shfl_sync(kAll, k < 32 ? dw[0] : dw[1], k & 31);
@@ -462,12 +523,12 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
 }
 
 // Blocks of a launch; up to kRouterCluster of them are one cluster.
-int router_blocks(int64_t tokens) {
+int router_blocks(int64_t tokens, int experts) {
     const int64_t blocks = std::max<int64_t>(1, (tokens + kRouterWarps - 1) / kRouterWarps);
     if (blocks <= kRouterCluster) return static_cast<int>(blocks);
     if (blocks <= kRouterCluster * kRouterOneCluster) return kRouterCluster;
-    return static_cast<int>(std::min<int64_t>(kRouterMaxClusters, (blocks + kRouterCluster - 1) / kRouterCluster)) *
-           kRouterCluster;
+    return static_cast<int>(std::min<int64_t>(kRouterClusters * router_sm_blocks(experts),
+                                              (blocks + kRouterCluster - 1) / kRouterCluster)) * kRouterCluster;
 }
 
 // The kernel for this many experts, K<N, T>::get(), N of them per lane.
@@ -492,12 +553,12 @@ struct Backward {
 }  // namespace
 
 size_t router_workspace(int64_t tokens, int topk, int experts) {
-    const int blocks = router_blocks(tokens);
+    const int blocks = router_blocks(tokens, experts);
     return blocks > kRouterCluster ? size_t(blocks / kRouterCluster) * sum_words(experts) * 4 : 0;
 }
 
 cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream) {
-    const int blocks = router_blocks(a.tokens), parts = blocks / kRouterCluster;
+    const int blocks = router_blocks(a.tokens, a.experts), parts = blocks / kRouterCluster;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(blocks);
@@ -527,7 +588,8 @@ cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream) {
 }
 
 cudaError_t launch_router_backward(const RouterArgs& a, int dtype, cudaStream_t stream) {
-    const int64_t blocks = std::min<int64_t>((a.tokens + kRouterWarps - 1) / kRouterWarps, int64_t(sm_count()) * 8);
+    const int64_t blocks = std::min<int64_t>((a.tokens + kRouterWarps - 1) / kRouterWarps,
+                                             int64_t(sm_count()) * router_sm_blocks(a.experts));
     return by_experts<Backward>(a.experts, dtype, [&](auto kernel) {
         return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kRouterWarps), 0, stream, a);
     });

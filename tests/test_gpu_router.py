@@ -101,6 +101,22 @@ def test_equal_logits_go_to_the_lowest_index():
         c.check()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+def test_a_few_equal_logits_of_either_sign(dtype):
+    """Groups of equal logits at the choice's edge, fewer than a warp has lanes."""
+    for E, K in ((100, 5), (128, 16), (256, 8), (1024, 30)):
+        c = Case(60, E, K, dtype=dtype)
+        g = torch.Generator().manual_seed(E)
+        high = torch.rand(60, E, generator=g) < 20 / E
+        level = torch.randint(0, 4, (60, E), generator=g).float()
+        c.logits = torch.where(high, level * 0.25 - 1.0, c.logits.float() - 50.0).to(dtype)
+        c.logits[30:][high[30:] & (level[30:] == 0)] = 300.0
+        c.logits[20:30][high[20:30] & (level[20:30] == 3)] = -0.0
+        w = c.check()
+        assert len(set(w.idx[0].tolist())) == K
+        c.backward()
+
+
 @pytest.mark.parametrize("normalize", [False, True])
 @pytest.mark.parametrize("lowest", [-INF, torch.finfo(F32).min])
 def test_masked_experts(normalize, lowest):
@@ -117,6 +133,17 @@ def test_masked_experts(normalize, lowest):
     if lowest == -INF:
         assert w.idx[3].tolist() == [-1] * 4 and w.idx[4, 2:].tolist() == [-1] * 2
         assert w.counts[-1] == 49
+
+
+def test_a_row_of_the_lowest_number_without_a_z_loss():
+    """A mask by the lowest number that leaves a token nothing; its logsumexp's
+    square, past fp32, counts for nothing."""
+    for T in (4, 2000):
+        c = Case(T, 40, 4)
+        c.logits[3] = torch.finfo(F32).min
+        c.kw["z"] = 0.0
+        c.check()
+        c.backward()
 
 
 def test_all_padding():
@@ -172,6 +199,24 @@ def test_dropped_slots_gradients_are_not_read():
         dl = torch.empty(30, 16, device="cuda")
         ct.moe_router_backward(dw.cuda(), scalar(1.0), c.logits.cuda(), idx.cuda(), w.counts.cuda(), dl, **c.kw)
         assert torch.isfinite(dl).all()
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_an_expert_twice(normalize):
+    """idx as another choice may leave it: each slot counts."""
+    for E, K in ((16, 4), (64, 3), (256, 8), (1000, 32), (1000, 40)):
+        c = Case(45, E, K, normalize=normalize)
+        w = c.reference()
+        w.idx[::2, 1] = w.idx[::2, 0]
+        w.idx[::4] = w.idx[::4, :1].clone()
+        w.weights = w.p.gather(1, w.idx.long())
+        if normalize:
+            w.weights /= w.weights.sum(1, keepdim=True)
+        value, err = w.backward(c.dweights, c.dloss)
+        dl = torch.empty(45, E, device="cuda")
+        ct.moe_router_backward(c.dweights.cuda(), scalar(c.dloss), c.logits.cuda(), w.idx.cuda(), w.counts.cuda(), dl,
+                               **c.kw)
+        base.close(dl, value, base.rounded(value, err, F32), "dlogits")
 
 
 def test_a_part_of_the_gradient():
