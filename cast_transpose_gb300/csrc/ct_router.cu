@@ -443,17 +443,12 @@ __global__ void __launch_bounds__(32 * kRouterWarps, router_sm_blocks(32 * N))
             dw[i] = here ? a.dweights[t * K + k] : 0.0f;
         }
         float x[N], g[N] = {}, each[N];
-        float top = -INFINITY;
-        bool some = false;                       // a logit that is not -inf
         token.get(a, x);
+        float top = x[0];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            top = fmaxf(top, x[i]);
-            some |= !(x[i] == -INFINITY);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-        if (!__any_sync(kAll, some && token.counted)) {       // padding
+        for (int i = 1; i < N; ++i) top = max_nan(top, x[i]);
+        top = lanes_max(top);                    // with a NaN all of the token's gradients are
+        if (!token.counted || top == -INFINITY) {             // padding
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (lane + 32 * i < E) dev::from_f32(out[lane + 32 * i], 0.0f);
@@ -469,13 +464,19 @@ __global__ void __launch_bounds__(32 * kRouterWarps, router_sm_blocks(32 * N))
         for (int i = 0; i < N; ++i) each[i] = load[i];
         if (a.normalize) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                w[i] = chosen[i] >= 0
-                           ? expf(dev::to_f32(static_cast<const T*>(a.logits)[t * E + chosen[i]]) - top) : 0.0f;
+            for (int i = 0; i < 2; ++i) {
+                w[i] = 0.0f;
+                if (i == 1 && K <= 32) break;
+                if (chosen[i] >= 0)
+                    w[i] = expf(dev::to_f32(static_cast<const T*>(a.logits)[t * E + chosen[i]]) - top);
+            }
             const float sum = dev::warp_sum(w[0] + w[1]);
             const float dot = dev::warp_sum(w[0] * dw[0] + w[1] * dw[1]) / sum;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) dw[i] = w[i] / sum * (dw[i] - dot);
+            for (int i = 0; i < 2; ++i) {
+                if (i == 1 && K <= 32) break;
+                dw[i] = w[i] / sum * (dw[i] - dot);
+            }
         }
         const bool has = chosen[0] >= 0;
         bool one_by_one = K > 32;
