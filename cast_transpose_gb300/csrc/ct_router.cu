@@ -6,11 +6,12 @@
 // its probabilities to sums that stay in registers too; blocks add theirs up through
 // their cluster's shared memory, a second launch joins the clusters', all in a fixed
 // order.  The logits are few bytes (16384 tokens of 256 fp32 17 MB, 2.6 us of HBM);
-// what bounds it are instructions, some 700 a token: the choice of 8 among 256, 256
-// exponentials, the sums.  Measured, one GB300: that case 21.6 us with its join (20
-// of the launch alone, cold; instructions issue on 62% of the cycles, 80 registers
-// leave 24 warps to an SM), a decoding step of 4 tokens 3 us and the call; the
-// gradient of 8191 tokens of 64 bf16 logits 7.9 us, the call's time.
+// what bounds it are instructions, some 610 a token: the choice of 8 among 256 takes a
+// third of the time, 256 exponentials a tenth.  Measured, one GB300: that case 19.9 us
+// with its join (18 of the launch alone, cold; instructions issue on 61% of the
+// cycles, 80 registers leave 24 warps to an SM; 131072 tokens 94), a decoding step of 4
+// tokens 3 us and the call; the gradient of the 16384 13.2 us (131072: 86), of 8191
+// tokens of 64 bf16 logits 4.1 and the call.
 #include "ct_device.cuh"
 #include "ct_ops.h"
 #include "ct_types.cuh"
@@ -410,7 +411,8 @@ __global__ void __launch_bounds__(kJoinThreads) router_join_kernel(const RouterA
 // at those.
 //
 // The slots' gradients get to the lanes of their experts through shared memory: a
-// lane of the K puts its own in the expert's place.
+// lane of the K puts its own in the expert's place (K comparisons for each of a lane's
+// experts instead: 16384 tokens of 256 21.1 us, so 14.4).
 template <int N, typename T>
 __global__ void __launch_bounds__(32 * kRouterWarps, router_sm_blocks(32 * N))
     router_backward_kernel(const RouterArgs a) {
