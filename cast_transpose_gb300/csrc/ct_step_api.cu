@@ -107,10 +107,10 @@ int layer_norm(const ct_layer_norm_config* cfg, const void* u, const void* res, 
     const ct_layer_norm_config& c = *cfg;
     if (scale && fmt != CT_E4M3 && fmt != CT_E5M2) return CT_ERR_FORMAT;
     ct::LayerNormArgs a;
-    if (!drop_of(c.p, c.rng, c.site, &a.drop)) return CT_ERR_ARG;
+    a.drop = no_drop();
+    if (u && !drop_of(c.p, c.rng, c.site, &a.drop)) return CT_ERR_ARG;
     if (c.rows == 0 || c.hidden == 0) return CT_OK;
     if (!u && res_out) return CT_ERR_ARG;
-    if (!u) a.drop = no_drop();
     const int b = elem_bytes(c.dtype), rb = elem_bytes(c.res_dtype), pb = elem_bytes(c.param_dtype);
     const int64_t n = c.rows * c.hidden;
     const bool in_place = res_out == res;
@@ -161,8 +161,8 @@ int layer_norm_backward(const ct_layer_norm_config* cfg, const void* dy, const v
     if (st != CT_OK) return st;
     const ct_layer_norm_config& c = *cfg;
     ct::LayerNormBackwardArgs a;
-    if (!drop_of(c.p, c.rng, c.site, &a.drop)) return CT_ERR_ARG;
-    if (!du) a.drop = no_drop();
+    a.drop = no_drop();
+    if (du && !drop_of(c.p, c.rng, c.site, &a.drop)) return CT_ERR_ARG;
     if (c.hidden == 0) return CT_OK;
     const int b = elem_bytes(c.dtype), rb = elem_bytes(c.res_dtype), pb = elem_bytes(c.param_dtype);
     const int64_t n = c.rows * c.hidden;

@@ -179,7 +179,7 @@ def layer_norm(u, res, res_out=None, y=None, weight=None, bias=None, eps=1e-5, w
     """u [rows, hidden] (or None), res -> res_out = res + dropout(u) (res itself
     for an update in place; None without u) and y, its layer norm.  res is of
     u's type or fp32; weight and bias are both of u's type or both fp32.  p, rng
-    and site: the dropout of u.  mean, rstd fp32 [rows]: kept for the backward
+    and site: the dropout of u, not used without it.  mean, rstd fp32 [rows]: kept for the backward
     pass.  With scale, amax and scale_inv (fp32 scalars) y is FP8 of format fmt,
     cast as fp8_cast does."""
     device, handle = _here(stream)
@@ -191,6 +191,8 @@ def layer_norm(u, res, res_out=None, y=None, weight=None, bias=None, eps=1e-5, w
         dtype = _dtype_of(y, "y") if scale is None else rtype
     first = weight if weight is not None else bias
     ptype = dtype if first is None else _dtype_of(first, "weight" if first is weight else "bias")
+    if u is None:
+        p, rng, site = 0.0, None, 0
     cfg = _layer_config(shape, rtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site,
                         device)
     if scale is None:
@@ -226,6 +228,8 @@ def layer_norm_backward(dy, dres_out, res_out, mean, rstd, dres, du=None, dweigh
     first = weight if weight is not None else dweight if dweight is not None else dbias
     ptype = dtype if first is None else _dtype_of(
         first, "weight" if first is weight else "dweight" if first is dweight else "dbias")
+    if du is None:
+        p, rng, site = 0.0, None, 0
     cfg = _layer_config(shape, rtype, dtype, ptype, weight, None, rng, 0.0, weight_offset, p, site,
                         device)
     _check(lib().layer_norm_backward(

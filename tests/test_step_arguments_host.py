@@ -1,0 +1,48 @@
+"""Arguments that a call says it does not use are not looked at (no GPU needed).
+The C calls here end in another refusal, so that nothing is launched; the
+pointers passed are never dereferenced."""
+import struct
+
+import pytest
+import torch
+
+import cast_transpose_gb300 as ct
+from test_step_host import A, ARG, B, NULL, config, fake, L  # noqa: F401
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+FIELDS = ("rows", "hidden", "weight", "bias", "rng", "eps", "weight_offset", "p", "site", "dtype",
+          "res_dtype", "param_dtype")
+
+
+def unpacked(call):
+    return dict(zip(FIELDS, struct.unpack("@2q3P3fI3i4x", call[1][0])))
+
+
+@pytest.mark.parametrize("p", [1.0, -0.5, float("nan"), 0.1])
+def test_the_dropout_of_a_norm_without_a_branch(L, p):  # noqa: F811
+    cfg, _ = config(p=p, rng=None)
+    assert L.layer_norm(cfg, None, A, None, None, None, None, None, None, None, 0, None, None) == NULL
+    assert L.layer_norm_backward(cfg, None, None, A, B, B + 4096, A + 4096, None, None, None, None, 0, None,
+                                 None) == NULL
+
+
+def test_the_dropout_of_a_norm_with_a_branch_is_checked(L):  # noqa: F811
+    cfg, _ = config(p=1.0)
+    assert L.layer_norm(cfg, A, B, B, None, None, None, None, None, None, 0, None, None) == ARG
+    assert L.layer_norm_backward(cfg, None, None, A, B, B + 4096, A + 4096, A + 8192, None, None, None, 0,
+                                 None, None) == ARG
+
+
+def test_the_bindings_dropout_without_a_branch(fake):  # noqa: F811
+    x, stats = torch.zeros(4, 8, dtype=BF), torch.zeros(4)
+    for more in (dict(p=0.1), dict(p=0.1, site=-1), dict(p=2.0)):
+        ct.layer_norm(None, x, None, x, **more)
+        ct.layer_norm_backward(x, x, x, stats, stats, x, **more)
+        with pytest.raises(ValueError, match="rng|site"):
+            ct.layer_norm(x, x, x, x, **more)
+        with pytest.raises(ValueError, match="rng|site"):
+            ct.layer_norm_backward(x, x, x, stats, stats, x, x.clone(), **more)
+    assert len(fake.calls) == 6
+    for call in fake.calls:
+        got = unpacked(call)
+        assert got["p"] == 0.0 and got["rng"] == 0
