@@ -41,9 +41,7 @@ int check_norm(const ct_layer_norm_config* c) {
     if (!dtype_ok(c->dtype) || (c->res_dtype != c->dtype && c->res_dtype != CT_FP32) ||
         (c->param_dtype != c->dtype && c->param_dtype != CT_FP32))
         return CT_ERR_FORMAT;
-    const int st = check_matrix(c->rows, c->hidden, ct::kMaxNormHidden);
-    if (st != CT_OK) return st;
-    return c->eps >= 0.0f ? CT_OK : CT_ERR_ARG;
+    return check_matrix(c->rows, c->hidden, ct::kMaxNormHidden);
 }
 
 int check_router(const ct_router_config* c) {
@@ -105,6 +103,7 @@ int layer_norm(const ct_layer_norm_config* cfg, const void* u, const void* res, 
     int st = check_norm(cfg);
     if (st != CT_OK) return st;
     const ct_layer_norm_config& c = *cfg;
+    if (!(c.eps >= 0.0f)) return CT_ERR_ARG;
     if (scale && fmt != CT_E4M3 && fmt != CT_E5M2) return CT_ERR_FORMAT;
     ct::LayerNormArgs a;
     a.drop = no_drop();

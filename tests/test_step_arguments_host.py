@@ -46,3 +46,11 @@ def test_the_bindings_dropout_without_a_branch(fake):  # noqa: F811
     for call in fake.calls:
         got = unpacked(call)
         assert got["p"] == 0.0 and got["rng"] == 0
+
+
+@pytest.mark.parametrize("eps", [-1.0, float("nan")])
+def test_the_backward_pass_has_no_eps(L, eps):  # noqa: F811
+    cfg, _ = config(eps=eps)
+    assert L.layer_norm_backward(cfg, None, None, A, B, B + 4096, A + 4096, None, None, None, None, 0, None,
+                                 None) == NULL
+    assert L.layer_norm(cfg, None, A, None, None, None, None, None, None, None, 0, None, None) == ARG
