@@ -87,7 +87,7 @@ int dropout(const void* x, int64_t rows, int64_t cols, int dtype, float p, const
     const bool in_place = out == x;
     st = check_buffers({{x, bytes, b, in_place},
                         {in_place ? nullptr : out, bytes, b, true, in_place},
-                        {rng, 16, 8, false, a.drop.cut == 0}});
+                        {a.drop.cut ? rng : nullptr, 16, 8, false, a.drop.cut == 0}});
     if (st != CT_OK) return st;
     a.x = x;
     a.out = out;

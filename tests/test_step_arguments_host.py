@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import cast_transpose_gb300 as ct
-from test_step_host import A, ARG, B, NULL, config, fake, L  # noqa: F401
+from test_step_host import A, ALIAS, ALIGN, ARG, B, NULL, config, fake, L  # noqa: F401
 
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
 FIELDS = ("rows", "hidden", "weight", "bias", "rng", "eps", "weight_offset", "p", "site", "dtype",
@@ -54,3 +54,10 @@ def test_the_backward_pass_has_no_eps(L, eps):  # noqa: F811
     assert L.layer_norm_backward(cfg, None, None, A, B, B + 4096, A + 4096, None, None, None, None, 0, None,
                                  None) == NULL
     assert L.layer_norm(cfg, None, A, None, None, None, None, None, None, None, 0, None, None) == ARG
+
+
+def test_the_generator_of_a_dropout_of_nothing(L):  # noqa: F811
+    def call(p, rng, out=A + 2):
+        return L.dropout(A, 10, 64, 0, p, rng, 0, out, None, None)
+    assert call(0.0, B + 4) == ALIAS and call(1e-6, B + 4) == ALIAS and call(0.0, None) == ALIAS
+    assert call(0.1, B + 4) == ALIGN and call(0.1, None) == NULL
