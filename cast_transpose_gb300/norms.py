@@ -178,19 +178,24 @@ def layer_norm(u, res, res_out=None, y=None, weight=None, bias=None, eps=1e-5, w
                scale_inv=None, fmt=E4M3, noop_flag=None, stream=None) -> None:
     """u [rows, hidden] (or None), res -> res_out = res + dropout(u) (res itself
     for an update in place; None without u) and y, its layer norm.  res is of
-    u's type or fp32; weight and bias are both of u's type or both fp32.  p, rng
-    and site: the dropout of u, not used without it.  mean, rstd fp32 [rows]: kept for the backward
-    pass.  With scale, amax and scale_inv (fp32 scalars) y is FP8 of format fmt,
-    cast as fp8_cast does."""
+    u's type or fp32; weight and bias are both of u's type or both fp32.  Without
+    u, y has the type that u would have; where y is FP8 an fp32 res takes weight
+    and bias of any.  p, rng and site: the dropout of u, not used without it.
+    mean, rstd fp32 [rows]: kept for the backward pass.  With scale, amax and
+    scale_inv (fp32 scalars) y is FP8 of format fmt, cast as fp8_cast does."""
     device, handle = _here(stream)
     shape, rtype = _matrix(res, "res")
     rows = shape[:1]
+    first = weight if weight is not None else bias
+    ptype = None if first is None else _dtype_of(first, "weight" if first is weight else "bias")
     if u is not None:
         dtype = _dtype_of(u, "u")
+    elif scale is None:
+        dtype = _dtype_of(y, "y")
     else:
-        dtype = _dtype_of(y, "y") if scale is None else rtype
-    first = weight if weight is not None else bias
-    ptype = dtype if first is None else _dtype_of(first, "weight" if first is weight else "bias")
+        dtype = ptype if ptype is not None and rtype is _F32 else rtype
+    if ptype is None:
+        ptype = dtype
     if u is None:
         p, rng, site = 0.0, None, 0
     cfg = _layer_config(shape, rtype, dtype, ptype, weight, bias, rng, eps, weight_offset, p, site,

@@ -61,3 +61,16 @@ def test_the_generator_of_a_dropout_of_nothing(L):  # noqa: F811
         return L.dropout(A, 10, 64, 0, p, rng, 0, out, None, None)
     assert call(0.0, B + 4) == ALIAS and call(1e-6, B + 4) == ALIAS and call(0.0, None) == ALIAS
     assert call(0.1, B + 4) == ALIGN and call(0.1, None) == NULL
+
+
+@pytest.mark.parametrize("res,param,want", [(F32, BF, (0, 2, 0)), (F32, HF, (1, 2, 1)), (F32, F32, (2, 2, 2)),
+                                            (F32, None, (2, 2, 2)), (BF, F32, (0, 0, 2)), (BF, BF, (0, 0, 0)),
+                                            (HF, None, (1, 1, 1))])
+def test_types_of_an_fp8_norm_without_a_branch(fake, res, param, want):  # noqa: F811
+    """Neither u nor y has the data's type: that of 16-bit parameters, else res's."""
+    x, y, one = torch.zeros(4, 8, dtype=res), torch.zeros(4, 8, dtype=torch.uint8), torch.ones(1)
+    p = None if param is None else torch.zeros(8, dtype=param)
+    for kw in (dict(weight=p), dict(bias=p)):
+        ct.layer_norm(None, x, None, y, scale=one, amax=one.clone(), scale_inv=one.clone(), **kw)
+        got = unpacked(fake.calls.pop())
+        assert (got["dtype"], got["res_dtype"], got["param_dtype"]) == want
