@@ -130,6 +130,7 @@ def lib() -> ctypes.CDLL:
             L.layer_norm_backward_workspace_size.restype = c.c_size_t
             L.layer_norm_backward_workspace_size.argtypes = [i64, i64]
             L.layer_norm_backward.argtypes = [vp] * 11 + [c.c_size_t, vp, vp]
+            L.ct_layer_norm_kernel.argtypes = [vp, i32, i32, vp]
             L.moe_router_workspace_size.restype = c.c_size_t
             L.moe_router_workspace_size.argtypes = [i64, i32, i32]
             L.moe_router.argtypes = [vp] * 8 + [c.c_size_t, vp, vp]
@@ -139,8 +140,9 @@ def lib() -> ctypes.CDLL:
             L.embedding_backward_workspace_size.argtypes = [i64, i64, i64]
             L.embedding_backward.argtypes = [vp, i32, i64, vp, i64, i64, i32, c.c_float, vp, i32,
                                              i32, vp, c.c_size_t, vp, vp]
-            for name in ("dropout", "layer_norm", "layer_norm_backward", "moe_router",
-                         "moe_router_backward", "embedding", "embedding_backward", "moe_sort", "moe_dispatch", "moe_dispatch_backward", "fp8_moe_dispatch",
+            for name in ("dropout", "layer_norm", "layer_norm_backward", "ct_layer_norm_kernel",
+                         "moe_router", "moe_router_backward", "embedding", "embedding_backward",
+                         "moe_sort", "moe_dispatch", "moe_dispatch_backward", "fp8_moe_dispatch",
                          "moe_combine", "moe_combine_backward", "block_norm",
                          "block_norm_backward",
                          "fp8_cast_transpose", "fp8_cast_transpose_ex", "fp8_cast",

@@ -721,6 +721,22 @@ RingShape ring_shape(int64_t rows, int hidden, bool shifted, int column_bytes, i
     return s;
 }
 
+// The shapes of launches on 16-byte-aligned buffers.  column_bytes: of res and u;
+// x_bytes: of dy; res_bytes: of res_out and, where it is given (down), of dres_out.
+RingShape forward_shape(int64_t rows, int hidden, int column_bytes) {
+    return ring_shape(rows, hidden, hidden % 8 != 0, column_bytes, 0, false);
+}
+RingShape backward_shape(int64_t rows, int hidden, int x_bytes, int res_bytes, bool down) {
+    const bool shifted = hidden % 8 != 0;
+    auto shape = [&](bool few) {
+        return ring_shape(rows, hidden, shifted, res_bytes + x_bytes, down ? res_bytes : 0, true, few);
+    };
+    RingShape s = {};
+    if (shifted && hidden <= kFewColumns) s = shape(true);
+    if (rows >= int64_t(kFewRows) * s.blocks) s = shape(false);        // also where there are none
+    return s;
+}
+
 // Launches a kernel of many rows for PER vectors per thread, which the shape has to
 // be for; the first time on a device it is allowed its shared memory.
 template <auto KERNEL, int PER, bool ONE, typename Args>
@@ -826,8 +842,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int res_dtype, 
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const RingShape s = aligned ? ring_shape(a.rows, a.hidden, !vec, sizeof(R) + (a.u ? sizeof(T) : 0), 0, false)
-                                    : RingShape{};
+        const RingShape s = aligned ? forward_shape(a.rows, a.hidden, sizeof(R) + (a.u ? sizeof(T) : 0)) : RingShape{};
         if (s.blocks > 0)
             return s.one ? launch_ring<layer_norm_kernel<T, R, false, 2, true>, 2, true>(s, a, stream)
                  : vec   ? launch_ring<layer_norm_kernel<T, R, false, 2, false>, 2, false>(s, a, stream)
@@ -838,6 +853,13 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, int dtype, int res_dtype, 
         return launch_pdl(kernel, dim3(static_cast<unsigned>(a.rows)), dim3(row_threads(a.hidden, per)), 0,
                           stream, a);
     });
+}
+
+LayerNormPlan layer_norm_plan(int64_t rows, int hidden, int x_bytes, int res_bytes, bool backward, bool with) {
+    const RingShape s = backward ? backward_shape(rows, hidden, x_bytes, res_bytes, with)
+                                 : forward_shape(rows, hidden, res_bytes + (with ? x_bytes : 0));
+    if (s.blocks == 0) return {};
+    return {s.blocks, s.per, s.stages, hidden % 8 != 0, s.one, s.once};
 }
 
 size_t layer_norm_backward_workspace(int64_t rows, int64_t hidden) {
@@ -854,14 +876,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype
     return by_types(dtype, res_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        auto shape = [&](bool few) {
-            return ring_shape(a.rows, a.hidden, !vec, sizeof(R) + sizeof(T), a.dres_out ? sizeof(R) : 0, true, few);
-        };
-        RingShape s = {};
-        if (aligned) {
-            if (!vec && a.hidden <= kFewColumns) s = shape(true);
-            if (a.rows >= int64_t(kFewRows) * s.blocks) s = shape(false);      // also where there are none
-        }
+        const RingShape s = aligned ? backward_shape(a.rows, a.hidden, sizeof(T), sizeof(R), a.dres_out) : RingShape{};
         cudaError_t e = cudaSuccess;
         int parts;
         if (s.blocks > 0) {

@@ -146,6 +146,11 @@ struct LayerNormBackwardArgs {
     int hidden, param_f32;
 };
 size_t layer_norm_backward_workspace(int64_t rows, int64_t hidden);
+// Which kernel a launch on aligned buffers takes: see ct_layer_norm_kernel.
+struct LayerNormPlan {
+    int blocks, vectors, stages, shifted, warp_per_row, once;
+};
+LayerNormPlan layer_norm_plan(int64_t rows, int hidden, int x_bytes, int res_bytes, bool backward, bool with);
 cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, int dtype, int res_dtype,
                                        cudaStream_t stream);
 

@@ -200,6 +200,18 @@ int layer_norm_backward(const ct_layer_norm_config* cfg, const void* dy, const v
                                                       static_cast<cudaStream_t>(stream)));
 }
 
+int ct_layer_norm_kernel(const ct_layer_norm_config* cfg, int backward, int with, ct_layer_norm_plan* plan) {
+    if (!plan) return CT_ERR_NULL;
+    const int st = check_norm(cfg);
+    if (st != CT_OK) return st;
+    ct::LayerNormPlan p = {};
+    if (cfg->rows > 0 && cfg->hidden > 0)
+        p = ct::layer_norm_plan(cfg->rows, static_cast<int>(cfg->hidden), elem_bytes(cfg->dtype),
+                                elem_bytes(cfg->res_dtype), backward != 0, with != 0);
+    *plan = {p.blocks, p.vectors, p.stages, p.shifted, p.warp_per_row, p.once};
+    return CT_OK;
+}
+
 size_t moe_router_workspace_size(int64_t tokens, int topk, int experts) {
     if (experts < 1 || experts > ct::kMaxExperts || topk < 1 || topk > kMaxRouterTopk || tokens < 0 ||
         tokens > kMaxIndex / topk)

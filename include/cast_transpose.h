@@ -816,6 +816,22 @@ int ct_selftest_bounded_wait(unsigned int limit_us, void* stream);
  */
 int ct_selftest_norm_wait(int blocks, int thread, unsigned int limit_us, void* stream);
 
+/*
+ * ct_layer_norm_kernel -- which kernel a layer_norm call of this config takes,
+ * or, with `backward`, a layer_norm_backward call, on 16-byte-aligned buffers;
+ * `with`: u, or dres_out, is given.  Launches nothing.  For tests, which have to
+ * reach each form.  Errors: as those calls'.
+ */
+typedef struct {
+    int blocks;               /* of a launch of many rows; 0: a block per row, the rest 0 */
+    int vectors;              /* of eight columns per thread */
+    int stages;               /* rows of a block's ring */
+    int shifted;              /* rows that are not whole vectors */
+    int warp_per_row;
+    int once;                 /* dres_out has one place beside the ring */
+} ct_layer_norm_plan;
+int ct_layer_norm_kernel(const ct_layer_norm_config* cfg, int backward, int with, ct_layer_norm_plan* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,13 +1,14 @@
 """Arguments that a call says it does not use are not looked at (no GPU needed).
 The C calls here end in another refusal, so that nothing is launched; the
 pointers passed are never dereferenced."""
+import ctypes
 import struct
 
 import pytest
 import torch
 
 import cast_transpose_gb300 as ct
-from test_step_host import A, ALIAS, ALIGN, ARG, B, NULL, config, fake, L  # noqa: F401
+from test_step_host import A, ALIAS, ALIGN, ARG, B, FORMAT, NULL, SHAPE, config, fake, L  # noqa: F401
 
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
 FIELDS = ("rows", "hidden", "weight", "bias", "rng", "eps", "weight_offset", "p", "site", "dtype",
@@ -74,3 +75,19 @@ def test_types_of_an_fp8_norm_without_a_branch(fake, res, param, want):  # noqa:
         ct.layer_norm(None, x, None, y, scale=one, amax=one.clone(), scale_inv=one.clone(), **kw)
         got = unpacked(fake.calls.pop())
         assert (got["dtype"], got["res_dtype"], got["param_dtype"]) == want
+
+
+def test_which_kernel(L):  # noqa: F811
+    def kernel(backward=0, given=1, **kw):
+        out = (ctypes.c_int * 6)()
+        return L.ct_layer_norm_kernel(config(**kw)[0], backward, given, out), list(out)
+    assert kernel(rows=4, hidden=4096) == (0, [0] * 6) == kernel(rows=0) == kernel(hidden=0)
+    for backward in (0, 1):
+        assert kernel(backward, rows=10 ** 6, hidden=32768) == (0, [0] * 6)
+        status, (blocks, vectors, stages, shifted, one, once) = kernel(backward, rows=10 ** 6, hidden=777)
+        assert status == 0 and blocks > 0 and blocks % 8 == 0 and (vectors, shifted, one, once) == (2, 1, 0, 0)
+    assert kernel(rows=10 ** 6, hidden=264)[1][4] == 1
+    assert kernel(1, rows=10 ** 6, hidden=2048)[1][5] == 1 and kernel(1, 0, rows=10 ** 6, hidden=2048)[1][5] == 0
+    assert kernel(dtype=3)[0] == FORMAT and kernel(rows=-1)[0] == SHAPE
+    assert L.ct_layer_norm_kernel(config()[0], 0, 0, None) == NULL
+    assert L.ct_layer_norm_kernel(None, 0, 0, (ctypes.c_int * 6)()) == NULL
