@@ -379,12 +379,6 @@ struct RowDrops {
     }
 };
 
-// s / n, rounded to nearest but for rare last bits, given r = 1 / n: Newton's step for
-// the quotient, q + (s - q n) r, whose residual a fused multiply-add has exactly.
-__device__ __forceinline__ float divided(float s, float n, float r) {
-    const float q = s * r;
-    return fmaf(fmaf(-q, n, s), r, q);
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -407,9 +401,12 @@ __device__ __forceinline__ int shift_of(int H) {
 }
 
 // Forward.  The mean and the squares about it need one exchange: a warp leaves the
-// sum of its columns and the squares about its own mean, from which everyone gets
-//   M2 = sum over warps of M2_w + n_w (mean_w - mean)^2
-// without the cancellation of a difference of squares.
+// sum S_w of its n_w columns and their squares Q_w about a number c_w next to its
+// own mean, S_w times 1 / n_w, from which everyone gets
+//   M2 = sum over warps of Q_w + (c_w - mean) (n_w (c_w - mean) + 2 (S_w - n_w c_w))
+// without the cancellation of a difference of squares.  This holds for any c_w, so
+// that its rounding adds nothing; S_w - n_w c_w is one fused multiply-add.  (Quotients
+// S_w / n_w, for which the last term is 0, cost 4%: 8191x6144 78.8 us against 75.9.)
 template <typename T, typename R, bool SHIFT, int PER, bool ONE>
 __global__ void __launch_bounds__(ring_block(PER, ONE, false), ONE ? one_blocks(PER, false) : 1)
     layer_norm_kernel(const LayerNormArgs a, int stages) {
@@ -490,7 +487,7 @@ __global__ void __launch_bounds__(ring_block(PER, ONE, false), ONE ? one_blocks(
         fetch(row + int64_t(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
         if (++stage == stages) stage = 0;
         sum_w = dev::warp_sum(sum_w);
-        const float mean_w = ONE ? sum_w / H : divided(sum_w, own_columns, per_own);
+        const float mean_w = ONE ? sum_w / H : __fmul_rn(sum_w, per_own);
         const uint64_t away = pair(-mean_w, -mean_w);
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
@@ -511,8 +508,10 @@ __global__ void __launch_bounds__(ring_block(PER, ONE, false), ONE ? one_blocks(
             const float2 other = lane < warps ? slots[turn][lane] : make_float2(0.0f, 0.0f);
             turn ^= 1;
             mean = dev::warp_sum(other.x) / H;
-            const float apart = lane < warps ? divided(other.x, lane_columns, per_lane) - mean : 0.0f;
-            squares = dev::warp_sum(fmaf(lane_columns * apart, apart, other.y));
+            // c of this lane's warp, as that has it; where there is none, no columns
+            const float c = __fmul_rn(other.x, per_lane), left = fmaf(-lane_columns, c, other.x);
+            const float apart = lane < warps ? c - mean : 0.0f;
+            squares = max_nan(dev::warp_sum(fmaf(apart, fmaf(lane_columns, apart, left + left), other.y)), 0.0f);
         }
         const float rstd = rsqrtf(fmaf(squares, per_column, a.eps));
         if (tid == 0) {

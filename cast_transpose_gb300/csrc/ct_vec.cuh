@@ -72,6 +72,13 @@ __device__ __forceinline__ float lanes_sum(uint64_t v) {
     return lo + hi;
 }
 
+// The larger one, a NaN if there is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // ---- parameters ------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void set_param(void* p, int f32, int64_t i, float v) {

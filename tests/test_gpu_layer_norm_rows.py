@@ -187,6 +187,20 @@ def test_constant_rows(hidden):
     assert torch.equal(out["y"].cpu(), c.bias.expand(c.rows, -1))
 
 
+@pytest.mark.parametrize("hidden", [264, 1024, 6144, 777, 4099])
+def test_a_variance_is_never_below_zero(hidden):
+    """Without eps, rows of equal or nearly equal values: 1 / sqrt of a number."""
+    rows = many_rows(hidden, F32, F32, u=False, times=2)
+    has(plan(rows, hidden, F32, F32, given=False))
+    values = torch.tensor([0.1, 3.0, 2000.3, -7.77e-12, 1.3e15])[torch.arange(rows) % 5]
+    res = values[:, None].expand(-1, hidden).contiguous().cuda()
+    last = torch.arange(hidden, device="cuda") % 97 == 0
+    res[rows // 2:] = torch.where(last, torch.nextafter(res, res * 2), res)[rows // 2:]
+    y, rstd = torch.empty_like(res), torch.empty(rows, device="cuda")
+    ct.layer_norm(None, res, None, y, eps=0.0, rstd=rstd)
+    assert (rstd > 0).all()
+
+
 @pytest.mark.parametrize("hidden", [264, 4096, 259])
 def test_in_place(hidden):
     c = Rows(many_rows(hidden, res=F32), hidden, res=F32)
