@@ -170,7 +170,7 @@ struct RouterArgs {
     float balance, z;
     int experts, topk, normalize;
 };
-size_t router_workspace(int64_t tokens, int topk, int experts);
+size_t router_workspace(int64_t tokens, int experts);
 cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream);
 cudaError_t launch_router_backward(const RouterArgs& a, int dtype, cudaStream_t stream);
 

@@ -165,6 +165,11 @@ __device__ __forceinline__ float exponentials(float (&x)[N], float top) {
 // tokens), the squared logsumexps.  In the workspace one for each cluster.
 __host__ __device__ constexpr int sum_words(int experts) { return 2 * experts + 2; }
 
+// A block's shared memory besides its warps' choices: its sums, and its warps'
+// probabilities.  No launch needs more than a kernel may have unasked.
+constexpr size_t router_smem(int experts) { return (size_t(kRouterWarps) * experts + sum_words(experts)) * 4; }
+static_assert(router_smem(kMaxExperts) + kRouterWarps * sizeof(Among) + 256 <= 48 * 1024);
+
 // Without a z loss squares past fp32, of a token whose logits are all the lowest
 // number, do not matter.
 __device__ __forceinline__ void put_loss(const RouterArgs& a, float balance, float squares, int tokens) {
@@ -550,7 +555,7 @@ struct Backward {
 
 }  // namespace
 
-size_t router_workspace(int64_t tokens, int topk, int experts) {
+size_t router_workspace(int64_t tokens, int experts) {
     const int blocks = router_blocks(tokens, experts);
     return blocks > kRouterCluster ? size_t(blocks / kRouterCluster) * sum_words(experts) * 4 : 0;
 }
@@ -561,7 +566,7 @@ cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(32 * kRouterWarps);
-    cfg.dynamicSmemBytes = (size_t(kRouterWarps) * a.experts + sum_words(a.experts)) * 4;
+    cfg.dynamicSmemBytes = router_smem(a.experts);
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -570,13 +575,7 @@ cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = by_experts<Forward>(a.experts, dtype, [&](auto kernel) {
-        cudaError_t e = cudaSuccess;
-        if (cfg.dynamicSmemBytes > 48 * 1024)      // of more than 512 experts
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (kRouterWarps * kMaxExperts + sum_words(kMaxExperts)) * 4);
-        return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a);
-    });
+    const cudaError_t e = by_experts<Forward>(a.experts, dtype, [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a); });
     if (e != cudaSuccess || parts <= 1) return e;
     cfg.gridDim = dim3(kJoinBlocks);
     cfg.blockDim = dim3(kJoinThreads);

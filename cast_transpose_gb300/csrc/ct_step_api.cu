@@ -216,7 +216,7 @@ size_t moe_router_workspace_size(int64_t tokens, int topk, int experts) {
     if (experts < 1 || experts > ct::kMaxExperts || topk < 1 || topk > kMaxRouterTopk || tokens < 0 ||
         tokens > kMaxIndex / topk)
         return 0;
-    return ct::router_workspace(tokens, topk, experts);
+    return ct::router_workspace(tokens, experts);
 }
 
 int moe_router(const ct_router_config* cfg, const void* logits, const uint8_t* mask, int* expert_idx,
@@ -225,7 +225,7 @@ int moe_router(const ct_router_config* cfg, const void* logits, const uint8_t* m
     int st = check_router(cfg);
     if (st != CT_OK) return st;
     const ct_router_config& c = *cfg;
-    const size_t need = ct::router_workspace(c.tokens, c.topk, c.experts);
+    const size_t need = ct::router_workspace(c.tokens, c.experts);
     if (need > 0 && (!workspace || workspace_bytes < need)) return CT_ERR_WORKSPACE;
     const int b = elem_bytes(c.dtype);
     const int64_t slots = c.tokens * c.topk;
