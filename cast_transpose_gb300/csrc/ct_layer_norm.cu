@@ -7,7 +7,7 @@
 // were less.  A row takes two sums over its columns before anything of y or dres is
 // known, and a dropout some 11 instructions a column for its random bits alone.
 // Measured, one GB300, bf16, p = 0.1, of the measured copy rate: forward 8191x6144
-// 75.4 us (403 MB, 0.79; without dropout 70, 0.84), 8192x12288 153 (0.78; 127,
+// 75.4 us (403 MB, 0.79; without dropout 70, 0.84), 8192x12288 152 (0.78; 127,
 // 0.93), backward with its join 8192x12288 173.7 us (1007 MB, 0.85), 8191x6144 94
 // (0.79).  Instructions issue on 60 to 65% of the cycles; warps wait little for
 // memory.  So:
@@ -205,13 +205,24 @@ __global__ void __launch_bounds__(kMaxRowThreads) layer_norm_backward_row_kernel
 // Threads of an SM, and of a block at most: with 80 registers each, or 128 in the
 // shifted backward pass, or 168 with four vectors.  (What does not fit goes through
 // L2: nearly all of the SM's memory is the ring's.  Backward with two vectors and 80
-// registers, of which 16 bytes do not: 8192x12288 190 us, so: 174; forward with
-// three and 96: 8191x6144 100 us, two and 80: 76, four and 168: 75, but 132 against
-// 122 with an fp32 residual.)
+// registers, of which 16 bytes do not: 8192x12288 190 us, so: 174.)  Forward, bf16,
+// p = 0.1, us, at 8191x6144, 8192x8192 and 8192x6144 with an fp32 residual:
+//   two vectors, 80 registers       75    113   121
+//   three, 128 (512 threads)        74    118   123
+//   three, 96 (640; 32 bytes out)  100    181   150
+//   four, 168                       74    120   131
 constexpr int ring_threads(int per, bool more) { return per == 4 ? 384 : per == 2 && more ? 512 : 768; }
 // Short shifted rows, few to a block: with one vector per thread a row's way through
-// the backward pass is shorter, though its warps do more besides the columns
-// (4099x777 24.1 us against 27.2, 16384x777 58.6 against 52.6).
+// the backward pass is shorter, though its warps do more besides the columns.  us,
+// one vector against two (bf16; fp16 with an fp32 residual):
+//            4099 rows                  16384 rows
+//   259    17.4, 18.9; 18.3, 19.7     37.6, 35.3; 39.8, 42.4
+//   515    19.6, 20.6; 21.4, 25.2     48.4, 52.4; 52.2, 66.4
+//   777    21.6, 22.6; 23.9, 26.5     59.4, 51.8; 66.0, 67.0
+//  1001    23.0, 25.4; 26.3, 28.5     60.3, 54.6; 69.6, 73.0
+// Six rows are where the slower widths change over (12000x777 bf16 45.8, 41.9; 515
+// columns never do).  With up to 2432 rows of less than 512 columns a block per row
+// would be faster (2000x259 8.9, so 13.1): not in the rule.
 constexpr int kFewRows = 6, kFewColumns = 1024 - 7;
 // Rows of whole vectors that fit a warp (ONE) need no exchange between warps: up to
 // 512 columns with two vectors per thread and, where the exchange is most of the

@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kJoinThreads) router_join_kernel(const RouterA
     __shared__ int counts[kJoinThreads];
     const auto cluster = cooperative_groups::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.experts, words = sum_words(E);
-    const int columns = (E + kJoinBlocks) / kJoinBlocks, ways = kJoinThreads / columns;     // at most 128
+    const int columns = (E + kJoinBlocks) / kJoinBlocks, ways = kJoinThreads / columns;     // 1 (1024 experts) to 256
     const int x = tid % columns, y = tid / columns, e = blockIdx.x * columns + x;
     const float* sums = static_cast<const float*>(a.workspace);
     dev::pdl_launch_dependents();
