@@ -87,7 +87,8 @@ int dropout(const void* x, int64_t rows, int64_t cols, int dtype, float p, const
     const bool in_place = out == x;
     st = check_buffers({{x, bytes, b, in_place},
                         {in_place ? nullptr : out, bytes, b, true, in_place},
-                        {a.drop.cut ? rng : nullptr, 16, 8, false, a.drop.cut == 0}});
+                        {a.drop.cut ? rng : nullptr, 16, 8, false, a.drop.cut == 0},
+                        {noop_flag, 4, 4, false, true}});
     if (st != CT_OK) return st;
     a.x = x;
     a.out = out;
@@ -124,7 +125,8 @@ int layer_norm(const ct_layer_norm_config* cfg, const void* u, const void* res, 
                         {rstd, 4 * c.rows, 4, true, true},
                         {scale, 4, 4, false, true},
                         {scale ? amax : nullptr, 4, 4, true, !scale},
-                        {scale ? scale_inv : nullptr, 4, 4, true, !scale}});
+                        {scale ? scale_inv : nullptr, 4, 4, true, !scale},
+                        {noop_flag, 4, 4, false, true}});
     if (st != CT_OK) return st;
     a.u = u;
     a.res = res;
@@ -178,7 +180,8 @@ int layer_norm_backward(const ct_layer_norm_config* cfg, const void* dy, const v
                         {du, n * b, b, true, true},
                         {dweight, c.hidden * pb, pb, true, true},
                         {dbias, c.hidden * pb, pb, true, true},
-                        {need ? workspace : nullptr, int64_t(need), 16, true, true}});
+                        {need ? workspace : nullptr, int64_t(need), 16, true, true},
+                        {noop_flag, 4, 4, false, true}});
     if (st != CT_OK) return st;
     a.dy = dy;
     a.dres_out = dres_out;
@@ -235,7 +238,8 @@ int moe_router(const ct_router_config* cfg, const void* logits, const uint8_t* m
                         {weights, 4 * slots, 4, true},
                         {counts, 4 * (int64_t(c.experts) + 1), 4, true},
                         {loss, 4, 4, true, true},
-                        {need ? workspace : nullptr, int64_t(need), 16, true, true}});
+                        {need ? workspace : nullptr, int64_t(need), 16, true, true},
+                        {noop_flag, 4, 4, false, true}});
     if (st != CT_OK) return st;
     ct::RouterArgs a = router_args(c);
     a.logits = logits;
@@ -265,7 +269,8 @@ int moe_router_backward(const ct_router_config* cfg, const void* logits, const u
                         {counts, 4 * (int64_t(c.experts) + 1), 4, false},
                         {dweights, 4 * slots, 4, false, true},
                         {dloss, 4, 4, false, true},
-                        {dlogits, n * b, b, true}});
+                        {dlogits, n * b, b, true},
+                        {noop_flag, 4, 4, false, true}});
     if (st != CT_OK) return st;
     ct::RouterArgs a = router_args(c);
     a.logits = logits;
@@ -288,7 +293,8 @@ int embedding(const void* idx, int index_bytes, int64_t tokens, const void* tabl
     const int b = elem_bytes(dtype);
     st = check_buffers({{idx, tokens * index_bytes, index_bytes, false},
                         {table, vocab * hidden * b, b, false},
-                        {out, tokens * hidden * b, b, true}});
+                        {out, tokens * hidden * b, b, true},
+                        {noop_flag, 4, 4, false, true}});
     if (st != CT_OK) return st;
     ct::EmbeddingArgs a = {};
     a.idx = idx;
@@ -323,7 +329,8 @@ int embedding_backward(const void* idx, int index_bytes, int64_t tokens, const v
     st = check_buffers({{idx, tokens * index_bytes, index_bytes, false},
                         {dout, tokens * hidden * b, b, false},
                         {dtable, vocab * hidden * gb, gb, true},
-                        {need ? workspace : nullptr, int64_t(need), 16, true, true}});
+                        {need ? workspace : nullptr, int64_t(need), 16, true, true},
+                        {noop_flag, 4, 4, false, true}});
     if (st != CT_OK) return st;
     ct::EmbeddingArgs a = {};
     a.idx = idx;

@@ -628,8 +628,8 @@ int block_norm_backward(const ct_block_norm_config* cfg, const void* dy, const v
  * bytes in 16-byte-aligned buffers are moved as 16-byte vectors).  Arithmetic
  * is fp32, rounded once to each output's type.  Every result is the same from
  * call to call.  Buffers that a call writes must not overlap any other buffer,
- * unless it says so.  A workspace holds nothing between calls; calls that may
- * run at the same time (two streams, two graphs) need one each.
+ * unless it says so; nor noop_flag.  A workspace holds nothing between calls;
+ * calls that may run at the same time (two streams, two graphs) need one each.
  *
  * Random numbers.  `rng` is a device array of two int64: a seed and a step.
  * The kernels read it when they run, so a captured graph drops other elements

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import cast_transpose_gb300 as ct
-from test_step_host import A, ALIAS, ALIGN, ARG, B, FORMAT, NULL, SHAPE, config, fake, L  # noqa: F401
+from test_step_host import A, ALIAS, ALIGN, ARG, B, FORMAT, NULL, SHAPE, config, fake, L, router  # noqa: F401
 
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
 FIELDS = ("rows", "hidden", "weight", "bias", "rng", "eps", "weight_offset", "p", "site", "dtype",
@@ -91,3 +91,30 @@ def test_which_kernel(L):  # noqa: F811
     assert kernel(dtype=3)[0] == FORMAT and kernel(rows=-1)[0] == SHAPE
     assert L.ct_layer_norm_kernel(config()[0], 0, 0, None) == NULL
     assert L.ct_layer_norm_kernel(None, 0, 0, (ctypes.c_int * 6)()) == NULL
+
+
+def test_the_flag_is_a_buffer_like_any_other(L):  # noqa: F811
+    """Off its four bytes it is refused, and so is an output over it, which some
+    blocks would write before others have read it."""
+    far = [0x100000000000 * (i + 1) for i in range(13)]
+    norm, _ = config(p=0.0)
+    choice, _ = router()
+    calls = {
+        "dropout": (lambda out, n: L.dropout(far[0], 10, 64, 2, 0.0, None, 0, out, n, None)),
+        "layer_norm": (lambda out, n: L.layer_norm(norm, far[0], far[1], far[2], out, None, None, None, None, None, 0,
+                                                   n, None)),
+        "layer_norm_backward": (lambda out, n: L.layer_norm_backward(
+            norm, far[0], None, far[2], far[3], far[4], out, None, None, None, None, 0, n, None)),
+        "moe_router": (lambda out, n: L.moe_router(choice, far[0], None, far[1], out, far[3], None, None, 0, n, None)),
+        "moe_router_backward": (lambda out, n: L.moe_router_backward(choice, far[0], None, far[1], far[2], far[3], None,
+                                                                     out, n, None)),
+        "embedding": (lambda out, n: L.embedding(far[0], 8, 10, far[1], 100, 64, 2, 1.0, out, n, None)),
+        "embedding_backward": (lambda out, n: L.embedding_backward(far[0], 8, 10, far[1], 100, 64, 2, 1.0, out, 2, 0,
+                                                                   None, 0, n, None)),
+    }
+    for name, call in calls.items():
+        assert call(far[5] + 1, far[6] + 2) == ALIGN, name
+        assert call(far[0] + 16, far[6] + 2) == ALIGN, name     # which comes before the overlap
+        assert call(far[0] + 16, None) == ALIAS, name
+        assert call(far[5], far[5]) == ALIAS, name
+        assert call(far[5], far[5] + 16) == ALIAS, name
